@@ -11,12 +11,17 @@ The functions carry the C names:
   wq_quant_matmul(a, a_scale, b, b_scale) -> y bf16 [M,N]   (INT8 dense / segments, FP8 groups)
   wq_fused_quant_matmul(x, w, w_scale)    -> y bf16 [M,N]
   wq_moe_sort(ids, E)                     -> (perm, row_token, offsets)
+  wq_group_quant_mxfp4(x)                 -> (x_q uint8 [T,G,D/2], x_s int32 view [T,G,PH], storage [G,PH,TA])
+  wq_group_dequant_mxfp4(x_q, storage)    -> bf16 [T,G,D]
+  wq_kv_append(cache, k, v, ...)             quantises rows into a paged 8-bit cache (KvCache)
+  wq_kv_attention(cache, q, ...)          -> bf16 [T, heads, D] (and lse)
 """
 
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -26,6 +31,8 @@ LIB_PATH = os.path.join(_PKG, "libwq.so")
 WQ_OK = 0
 WQ_IN_BF16, WQ_IN_F32 = 1, 2
 WQ_PAYLOAD_INT8, WQ_PAYLOAD_FP8_E4M3, WQ_PAYLOAD_MXFP8 = 1, 2, 3
+WQ_PAYLOAD_MXFP4, WQ_PAYLOAD_MXFP8_W4 = 4, 5
+WQ_KV_E4M3, WQ_KV_INT8 = 1, 2
 WQ_EPI_BF16, WQ_EPI_SWIGLU_F32 = 1, 2
 WQ_LAYOUT_PLAIN, WQ_LAYOUT_FRAGMENT = 0, 1
 
@@ -55,6 +62,15 @@ class MatmulDesc(ctypes.Structure):
     ]
 
 
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [
+        ("code", ctypes.c_int32),
+        ("pages", _i64), ("heads", _i64), ("page_tokens", _i64), ("head_dim", _i64),
+        ("k", _c_void_p), ("v", _c_void_p), ("k_scale", _c_void_p), ("v_scale", _c_void_p),
+        ("table", _c_void_p), ("table_stride", _i64), ("max_pages", _i64),
+    ]
+
+
 EXPORTS = {
     "wq_status_str": (ctypes.c_char_p, [ctypes.c_int]),
     "wq_abi_version": (ctypes.c_int, []),
@@ -75,6 +91,16 @@ EXPORTS = {
     "wq_fused_path": (ctypes.c_int, [_c_void_p, _i64, _i64, _i64]),
     "wq_group_quant_mxfp8": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p,
                                             _c_void_p]),
+    "wq_group_quant_mxfp4": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p,
+                                            _c_void_p]),
+    "wq_group_dequant_mxfp4": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p,
+                                              _c_void_p]),
+    "wq_kv_append": (ctypes.c_int, [_c_void_p, ctypes.POINTER(KvCacheDesc), _c_void_p, _i64, _c_void_p, _i64, _i64,
+                                    _i64, _c_void_p, _c_void_p, _c_void_p]),
+    "wq_kv_attention": (ctypes.c_int, [_c_void_p, ctypes.POINTER(KvCacheDesc), _c_void_p, _i64, _i64, _i64, _i64,
+                                       _c_void_p, _c_void_p, ctypes.c_float, ctypes.c_int, _c_void_p, _i64,
+                                       _c_void_p, _c_void_p, ctypes.c_size_t, _c_void_p]),
+    "wq_kv_attention_workspace_bytes": (_i64, [_c_void_p, ctypes.POINTER(KvCacheDesc), _i64, _i64, _i64]),
     "wq_pack_weight_i8": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p]),
     "wq_fused_quant_matmul_packed": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p,
                                                     _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p,
@@ -155,6 +181,12 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _same_device(fn, first, *others):
+    for t in others:
+        if t.device != first.device:
+            raise ValueError(f"{fn}: tensors on {first.device} and {t.device}")
+
+
 def _check(fn, st):
     if st != WQ_OK:
         raise WqError(fn, st)
@@ -220,20 +252,105 @@ def wq_group_quant_fp8_ue8m0(x: torch.Tensor, x_q: torch.Tensor | None = None, s
     return x_q, x_s, storage
 
 
+def wq_group_quant_mxfp4(x: torch.Tensor, x_q: torch.Tensor | None = None, storage: torch.Tensor | None = None):
+    """x bf16 [T, G, D] contiguous, D % 32 == 0 -> (x_q uint8 [T, G, D/2], two E2M1 codes to a
+    byte, x_s int32 logical view [T, G, PH], storage [G, PH, TA]), one UE8M0 scale for 32
+    elements.  Weights [N, K] are cast as x = w[:, None, :]."""
+    if x.dim() != 3 or not x.is_contiguous() or x.dtype != torch.bfloat16:
+        raise ValueError("x must be a contiguous bf16 [T, G, D] tensor")
+    T, G, D = x.shape
+    if D % 32:
+        raise ValueError("D must be a multiple of 32")
+    _, PH, TA = packed_scale_dims(T, D, 32)
+    if x_q is None:
+        x_q = torch.empty((T, G, D // 2), dtype=torch.uint8, device=x.device)
+    if storage is None:
+        storage = torch.empty((G, PH, TA), dtype=torch.int32, device=x.device)
+    if x_q.shape != (T, G, D // 2) or x_q.dtype != torch.uint8 or not x_q.is_contiguous() \
+            or storage.shape != (G, PH, TA) or storage.dtype != torch.int32 or not storage.is_contiguous():
+        raise ValueError("x_q must be uint8 [T, G, D/2] and storage int32 [G, PH, TA], both contiguous")
+    _same_device("wq_group_quant_mxfp4", x, x_q, storage)
+    if x.numel() > 0:
+        st = lib().wq_group_quant_mxfp4(context(x.device).handle, x.data_ptr(), T, G, D, x_q.data_ptr(),
+                                        storage.data_ptr(), _stream(x.device))
+        _check("wq_group_quant_mxfp4", st)
+    x_s = storage.transpose(-1, -2)[:, :T, :].transpose(0, 1)
+    return x_q, x_s, storage
+
+
+def wq_group_dequant_mxfp4(x_q: torch.Tensor, storage: torch.Tensor, y: torch.Tensor | None = None):
+    """The values of wq_group_quant_mxfp4's codes: bf16 [T, G, D], exact."""
+    if x_q.dim() != 3 or x_q.dtype != torch.uint8 or not x_q.is_contiguous():
+        raise ValueError("x_q must be a contiguous uint8 [T, G, D/2] tensor")
+    T, G, D = x_q.shape[0], x_q.shape[1], 2 * x_q.shape[2]
+    if D % 32:
+        raise ValueError("D must be a multiple of 32")
+    _, PH, TA = packed_scale_dims(T, D, 32)
+    if storage.shape != (G, PH, TA) or storage.dtype != torch.int32 or not storage.is_contiguous():
+        raise ValueError("storage must be contiguous int32 [G, PH, TA]")
+    if y is None:
+        y = torch.empty((T, G, D), dtype=torch.bfloat16, device=x_q.device)
+    elif y.shape != (T, G, D) or y.dtype != torch.bfloat16 or not y.is_contiguous():
+        raise ValueError("y must be contiguous bf16 [T, G, D]")
+    _same_device("wq_group_dequant_mxfp4", x_q, storage, y)
+    if x_q.numel() > 0:
+        st = lib().wq_group_dequant_mxfp4(context(x_q.device).handle, x_q.data_ptr(), storage.data_ptr(), T, G, D,
+                                          y.data_ptr(), _stream(x_q.device))
+        _check("wq_group_dequant_mxfp4", st)
+    return y
+
+
+def _mx4_matmul(a, a_scale, b, b_scale, G, y):
+    if a.dim() != 3 or b.dim() != 3 or a.dtype != torch.uint8 or b.dtype != torch.uint8 or a.stride(2) != 1 \
+            or b.shape[0] != G or a.shape[1] != G or b.stride(2) != 1 or (b.shape[1] > 1 and b.stride(1) != b.shape[2]):
+        raise ValueError("a must be uint8 [M, G, K/2] or [M, G, K], b uint8 [G, N, K/2], G = fp8_groups")
+    M, N, K = a.shape[0], b.shape[1], 2 * b.shape[2]
+    if a.shape[2] not in (K // 2, K):
+        raise ValueError("a's rows must hold K/2 bytes (E2M1 pairs) or K bytes (E4M3)")
+    for name, s, rows in (("a_scale", a_scale, (M + 3) // 4 * 4), ("b_scale", b_scale, N)):
+        if s.dtype != torch.int32 or s.shape[:2] != (G, (K + 127) // 128) or s.shape[2] < rows or not s.is_contiguous():
+            raise ValueError(f"{name} must be the contiguous int32 storage of its operand's quantisation")
+    if b_scale.shape[2] != N:
+        raise ValueError("b_scale must be [G, K/128, N]")
+    if y is None:
+        y = torch.empty((M, G, N), dtype=torch.bfloat16, device=a.device)
+    elif y.shape != (M, G, N) or y.dtype != torch.bfloat16 or y.stride(2) != 1:
+        raise ValueError("y must be bf16 [M, G, N] with unit stride along N")
+    _same_device("wq_quant_matmul", a, a_scale, b, b_scale, y)
+    d = MatmulDesc()
+    d.payload = WQ_PAYLOAD_MXFP8_W4 if a.shape[2] == K else WQ_PAYLOAD_MXFP4
+    d.epilogue, d.M, d.N, d.K, d.batch = WQ_EPI_BF16, M, N, K, G
+    # a stride of an axis of length one says nothing: the descriptor takes the dense one
+    d.a, d.lda = a.data_ptr(), a.stride(0) if M > 1 else a.shape[2]
+    d.a_batch_stride = a.stride(1) if G > 1 else 0
+    d.a_scale, d.a_scale_tokens = a_scale.data_ptr(), a_scale.shape[2]
+    d.b, d.b_batch_stride, d.b_scale = b.data_ptr(), b.stride(0) if G > 1 else 0, b_scale.data_ptr()
+    d.y, d.ldy, d.y_batch_stride = y.data_ptr(), y.stride(0) if M > 1 else N, y.stride(1) if G > 1 else 0
+    _check("wq_quant_matmul", lib().wq_quant_matmul(context(a.device).handle, ctypes.byref(d), _stream(a.device)))
+    return y
+
+
 def wq_quant_matmul(a, a_scale, b, b_scale, *, y=None, acc_out=None, seg_offsets=None,
                     epilogue=WQ_EPI_BF16, fp8_groups=None, a_scale_tokens=0, b_fragment=False, n=None,
-                    mx=False, expected_rows=0):
+                    mx=False, mx4=False, expected_rows=0):
     """INT8: a int8 [M, K] (row stride a.stride(0)), a_scale f32 [M], b int8 [N, K] (or
     [E, N, K] with seg_offsets int64 [E+1]), b_scale f32 [N] (or [E, N]) -> y.
     FP8 (fp8_groups=G): a uint8 [M, G, K], a_scale = packed storage [G, PH, TA],
     b uint8 [G, N, K], b_scale f32 [G, N/128, K/128] -> y bf16 [M, G, N].
     mx (with fp8_groups): the MX-like 32-element blocks: a_scale = storage of
     wq_group_quant_mxfp8 [G, K/128, TA], b_scale = UE8M0 bytes uint8 [G, N, K/32].
+    mx4 (with fp8_groups): 4-bit weights, b uint8 [G, N, K/2] and b_scale int32 [G, K/128, N]
+    as wq_group_quant_mxfp4 casts each group's w[:, None, :]; a uint8 [M, G, K/2] of
+    wq_group_quant_mxfp4 or [M, G, K] of wq_group_quant_fp8_ue8m0(group=32), a_scale its storage.
     b_fragment: INT8 weights cast by wq_pack_weight_i8: expert weights [E, N, K] (same shape
     and strides) with seg_offsets, or a dense [N, K] cast (flat N*K bytes; give n = N) at
     M < 256 (K % 512 == 0, K <= 4096).
     expected_rows: with seg_offsets, the rows per expert the caller expects (a kernel-choice
     hint; the same bytes for every value)."""
+    if mx4:
+        if fp8_groups is None or acc_out is not None or seg_offsets is not None or epilogue != WQ_EPI_BF16 or b_fragment:
+            raise ValueError("mx4 takes fp8_groups, and no acc_out, segments, SwiGLU epilogue or fragment order")
+        return _mx4_matmul(a, a_scale, b, b_scale, fp8_groups, y)
     d = MatmulDesc()
     d.b_layout = WQ_LAYOUT_FRAGMENT if b_fragment else WQ_LAYOUT_PLAIN
     d.expected_rows = expected_rows
@@ -273,6 +390,105 @@ def wq_quant_matmul(a, a_scale, b, b_scale, *, y=None, acc_out=None, seg_offsets
     ctx = context(dev)
     _check("wq_quant_matmul", lib().wq_quant_matmul(ctx.handle, ctypes.byref(d), _stream(dev)))
     return y
+
+
+class KvCache(NamedTuple):
+    """A paged 8-bit cache (wq.h): codes uint8 (E4M3) or int8, k [pages, heads, page_tokens, D]
+    and v [pages, heads, D, page_tokens], and their UE8M0 bytes [pages, heads]."""
+
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def kv_cache(pages: int, heads: int, page_tokens: int, head_dim: int, *, dtype=torch.uint8, device="cuda") -> KvCache:
+    """A zeroed cache: dtype torch.uint8 for E4M3 codes, torch.int8 for int8."""
+    return KvCache(torch.zeros((pages, heads, page_tokens, head_dim), dtype=dtype, device=device),
+                   torch.zeros((pages, heads, head_dim, page_tokens), dtype=dtype, device=device),
+                   torch.zeros((pages, heads), dtype=torch.uint8, device=device),
+                   torch.zeros((pages, heads), dtype=torch.uint8, device=device))
+
+
+def _kv_desc(fn, cache, offsets, lens, table, *rows) -> KvCacheDesc:
+    k, v, ks, vs = cache
+    if k.dim() != 4 or k.dtype not in (torch.uint8, torch.int8) or v.dtype != k.dtype:
+        raise ValueError("a cache's codes are uint8 (E4M3) or int8, k [pages, heads, page_tokens, D]")
+    pages, heads, page_tokens, D = k.shape
+    if v.shape != (pages, heads, D, page_tokens) or ks.shape != (pages, heads) or vs.shape != (pages, heads) \
+            or ks.dtype != torch.uint8 or vs.dtype != torch.uint8:
+        raise ValueError("a cache has v [pages, heads, D, page_tokens] and uint8 k_scale, v_scale [pages, heads]")
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("a cache's tensors must be contiguous")
+    if offsets.dtype != torch.int64 or lens.dtype != torch.int32 or table.dtype != torch.int32:
+        raise ValueError("offsets are int64, lens and table int32")
+    B = lens.numel()
+    if offsets.shape != (B + 1,) or lens.shape != (B,) or table.dim() != 2 or table.shape[0] != B \
+            or not offsets.is_contiguous() or not lens.is_contiguous() or (table.numel() and table.stride(1) != 1):
+        raise ValueError("offsets must be [B + 1], lens [B] and table [B, pages of a sequence]")
+    _same_device(fn, k, v, ks, vs, offsets, lens, table, *rows)
+    d = KvCacheDesc()
+    d.code = WQ_KV_INT8 if k.dtype == torch.int8 else WQ_KV_E4M3
+    d.pages, d.heads, d.page_tokens, d.head_dim = pages, heads, page_tokens, D
+    d.k, d.v, d.k_scale, d.v_scale = k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr()
+    d.table, d.max_pages = table.data_ptr(), table.shape[1]
+    d.table_stride = table.stride(0) if B > 1 else table.shape[1]
+    return d
+
+
+def _kv_rows(name, x, heads, D):
+    """Row stride of bf16 rows [T, heads, D] whose last two axes are dense."""
+    if x.dim() != 3 or x.dtype != torch.bfloat16 or x.shape[1:] != (heads, D) \
+            or (x.numel() and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != D))):
+        raise ValueError(f"{name} must be bf16 [T, {heads}, {D}] with dense rows")
+    return x.stride(0) if x.shape[0] > 1 else heads * D
+
+
+def wq_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, offsets, lens, table) -> None:
+    """Quantise the rows k, v bf16 [T, heads, D] into the cache, in place.  offsets int64
+    [B + 1]: rows of each sequence; lens int32 [B]: its tokens, these rows among them; table
+    int32 [B, pages of a sequence]."""
+    d = _kv_desc("wq_kv_append", cache, offsets, lens, table, k, v)
+    ldk, ldv = _kv_rows("k", k, d.heads, d.head_dim), _kv_rows("v", v, d.heads, d.head_dim)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same number of rows")
+    st = lib().wq_kv_append(context(k.device).handle, ctypes.byref(d), k.data_ptr(), ldk, v.data_ptr(), ldv, T,
+                            lens.numel(), offsets.data_ptr(), lens.data_ptr(), _stream(k.device))
+    _check("wq_kv_append", st)
+
+
+def wq_kv_attention(cache: KvCache, q: torch.Tensor, offsets, lens, table, *, scale=None, causal=True, out=None,
+                    lse=None, return_lse=False):
+    """Attention of the rows q bf16 [T, q_heads, D] over the cache (offsets, lens and table as
+    in wq_kv_append, the newest rows last) -> bf16 [T, q_heads, D], and the f32 log-sum-exp
+    [T, q_heads] with return_lse or lse=.  scale: 1 / sqrt(D) by default."""
+    if q.dim() != 3:
+        raise ValueError("q must be bf16 [T, q_heads, D]")
+    d = _kv_desc("wq_kv_attention", cache, offsets, lens, table, q)
+    T, heads, D = q.shape
+    ldq = _kv_rows("q", q, heads, d.head_dim)
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=torch.bfloat16, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    ldo = _kv_rows("out", out, heads, D)
+    if lse is None and return_lse:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+    if lse is not None and (lse.shape != (T, heads) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous f32 [T, q_heads]")
+    _same_device("wq_kv_attention", q, out, *(() if lse is None else (lse,)))
+    ctx, B = context(q.device).handle, lens.numel()
+    need = lib().wq_kv_attention_workspace_bytes(ctx, ctypes.byref(d), T, heads, B)
+    if need < 0:
+        _check("wq_kv_attention", -need)
+    # from torch's allocator, call by call: calls on several streams and captured graphs share nothing
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    st = lib().wq_kv_attention(ctx, ctypes.byref(d), q.data_ptr(), ldq, T, heads, B, offsets.data_ptr(),
+                               lens.data_ptr(), D ** -0.5 if scale is None else float(scale), int(causal),
+                               out.data_ptr(), ldo, _ptr(lse), _ptr(ws), need, _stream(q.device))
+    _check("wq_kv_attention", st)
+    return (out, lse) if return_lse or lse is not None else out
 
 
 def wq_fused_quant_matmul(x, w, w_scale, *, y=None, x_q_out=None, x_scale_out=None, acc_out=None):

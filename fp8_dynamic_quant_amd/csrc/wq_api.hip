@@ -14,6 +14,7 @@
 //    128 x 128 tiles.
 //  * FP8: the 16- or 32-column weight-streaming kernels at T <= 64, 128 x 128 tiles above.
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -344,6 +345,44 @@ int wq_group_quant_mxfp8(wq_ctx* c, const void* x, int64_t T, int64_t G, int64_t
   return status_of(e);
 }
 
+// the argument checks that the 4-bit quantisation and its inverse share
+static int mxfp4_shape(int64_t T, int64_t G, int64_t D) {
+  if (T < 0 || G <= 0 || D <= 0 || D % 32 != 0 || G > 65535 || D > (1 << 20) || T > ((int64_t)1 << 31)) return WQ_ERR_SHAPE;
+  // words, and the kernels' waves of 512 elements, are counted in 32 bits
+  if ((T + 3) / 4 * 4 * G * ((D / 32 + 3) / 4) >= ((int64_t)1 << 31)) return WQ_ERR_SHAPE;
+  return WQ_OK;
+}
+
+int wq_group_quant_mxfp4(wq_ctx* c, const void* x, int64_t T, int64_t G, int64_t D, uint8_t* x_q, int32_t* x_s,
+                         void* stream) {
+  if (!c) return WQ_ERR_NULL;
+  if (int r = mxfp4_shape(T, G, D)) return r;
+  if (T == 0) return WQ_OK;
+  if (!x || !x_q || !x_s) return WQ_ERR_NULL;
+  if (!al16(x) || !al16(x_q) || !al16(x_s)) return WQ_ERR_ALIGN;
+  DeviceGuard g(c->device);
+  hipError_t e = wq::launch_group_quant_mxfp4(static_cast<const uint16_t*>(x), T, (int)G, (int)D, x_q, x_s,
+                                              static_cast<hipStream_t>(stream));
+  if (c->log)
+    std::fprintf(stderr, "[wq] group_quant_mxfp4 T=%lld G=%lld D=%lld\n", (long long)T, (long long)G, (long long)D);
+  return status_of(e);
+}
+
+int wq_group_dequant_mxfp4(wq_ctx* c, const uint8_t* x_q, const int32_t* x_s, int64_t T, int64_t G, int64_t D,
+                           void* y, void* stream) {
+  if (!c) return WQ_ERR_NULL;
+  if (int r = mxfp4_shape(T, G, D)) return r;
+  if (T == 0) return WQ_OK;
+  if (!x_q || !x_s || !y) return WQ_ERR_NULL;
+  if (!al16(x_q) || !al16(x_s) || !al16(y)) return WQ_ERR_ALIGN;
+  DeviceGuard g(c->device);
+  hipError_t e = wq::launch_group_dequant_mxfp4(x_q, x_s, T, (int)G, (int)D, static_cast<uint16_t*>(y),
+                                                static_cast<hipStream_t>(stream));
+  if (c->log)
+    std::fprintf(stderr, "[wq] group_dequant_mxfp4 T=%lld G=%lld D=%lld\n", (long long)T, (long long)G, (long long)D);
+  return status_of(e);
+}
+
 static int int8_matmul(wq_ctx* c, const wq_matmul_desc* d, hipStream_t st) {
   const int64_t M = d->M, N = d->N, K = d->K;
   if (N % 16 != 0 || K % 16 != 0 || K > 131072 || d->lda < K || d->ldy < (d->epilogue == WQ_EPI_SWIGLU_F32 ? N / 2 : N))
@@ -573,6 +612,41 @@ static int fp8_matmul(wq_ctx* c, const wq_matmul_desc* d, hipStream_t st) {
   return status_of(e);
 }
 
+static int mx4_matmul(wq_ctx* c, const wq_matmul_desc* d, hipStream_t st) {
+  const int64_t M = d->M, N = d->N, K = d->K, G = d->batch;
+  if (d->seg_offsets || d->acc_out || d->epilogue != WQ_EPI_BF16) return WQ_ERR_UNSUPPORTED;
+  const bool a8 = d->payload == WQ_PAYLOAD_MXFP8_W4;
+  const int64_t row = a8 ? K : K / 2;  // bytes of an activation row
+  if (N % 16 != 0 || K % 128 != 0 || K > 131072 || G > 65535) return WQ_ERR_SHAPE;
+  if (d->lda < row || d->ldy < N || d->a_batch_stride < 0 || d->y_batch_stride < 0 || d->b_batch_stride < 0)
+    return WQ_ERR_SHAPE;
+  if (d->a_scale_tokens < (M + 3) / 4 * 4) return WQ_ERR_SHAPE;
+  if (G > 1 && d->b_batch_stride < N * (K / 2)) return WQ_ERR_SHAPE;
+  if (!d->a || !d->a_scale || !d->b || !d->b_scale || !d->y) return WQ_ERR_NULL;
+  if (!al16(d->a) || !al16(d->b) || !al16(d->y) || !al16(d->a_scale) || !al16(d->b_scale) || d->lda % 16 != 0 ||
+      d->a_batch_stride % 16 != 0 || (d->ldy * 2) % 16 != 0 || (d->y_batch_stride * 2) % 16 != 0 ||
+      d->b_batch_stride % 16 != 0)
+    return WQ_ERR_ALIGN;
+  wq::Mx4Args t{};
+  t.a = static_cast<const uint8_t*>(d->a);
+  t.lda = d->lda;
+  t.a_batch_stride = d->a_batch_stride;
+  t.a_scale = static_cast<const int32_t*>(d->a_scale);
+  t.a_tokens = d->a_scale_tokens;
+  t.w = static_cast<const uint8_t*>(d->b);
+  t.w_batch_stride = d->b_batch_stride;
+  t.w_scale = reinterpret_cast<const int32_t*>(d->b_scale);
+  t.y = static_cast<uint16_t*>(d->y);
+  t.ldy = d->ldy;
+  t.y_batch_stride = d->y_batch_stride;
+  t.M = (int)M; t.N = (int)N; t.K = (int)K; t.batch = (int)G;
+  hipError_t e = wq::launch_mx4(t, a8, st);
+  if (c->log)
+    std::fprintf(stderr, "[wq] quant_matmul %s M=%lld N=%lld K=%lld groups=%lld\n", a8 ? "mxfp8 x mxfp4" : "mxfp4",
+                 (long long)M, (long long)N, (long long)K, (long long)G);
+  return e == hipErrorInvalidValue ? WQ_ERR_SHAPE : status_of(e);
+}
+
 int wq_quant_matmul(wq_ctx* c, const wq_matmul_desc* d, void* stream) {
   if (!c || !d) return WQ_ERR_NULL;
   if (d->M < 0 || d->N <= 0 || d->K <= 0 || d->batch < 1) return WQ_ERR_SHAPE;
@@ -585,6 +659,7 @@ int wq_quant_matmul(wq_ctx* c, const wq_matmul_desc* d, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (d->payload == WQ_PAYLOAD_INT8) return int8_matmul(c, d, st);
   if (d->payload == WQ_PAYLOAD_FP8_E4M3 || d->payload == WQ_PAYLOAD_MXFP8) return fp8_matmul(c, d, st);
+  if (d->payload == WQ_PAYLOAD_MXFP4 || d->payload == WQ_PAYLOAD_MXFP8_W4) return mx4_matmul(c, d, st);
   return WQ_ERR_SHAPE;
 }
 
@@ -778,6 +853,114 @@ int wq_fused_quant_matmul_packed(wq_ctx* c, const void* x, int64_t M, int64_t K,
   if (c->log)
     std::fprintf(stderr, "[wq] fused_quant_matmul_packed M=%lld N=%lld K=%lld cols/wg=%d rows/wg=%d\n",
                  (long long)M, (long long)N, (long long)K, nt, rr);
+  return status_of(e);
+}
+
+// the cache's sizes and pointers, and the rows' offsets: what both calls check
+static int kv_args(const wq_kv_cache* k, int64_t T, int64_t B, const int64_t* offsets, const int32_t* lens,
+                   wq::KvArgs* out) {
+  if (k->code != WQ_KV_E4M3 && k->code != WQ_KV_INT8) return WQ_ERR_SHAPE;
+  if (k->pages < 1 || k->pages > INT32_MAX || k->heads < 1 || k->heads > 65535 || k->page_tokens < 16 ||
+      k->page_tokens > 256 || k->page_tokens % 16 != 0 || !wq::kv_head_dim_ok(k->head_dim))
+    return WQ_ERR_SHAPE;
+  if (k->max_pages < 1 || k->max_pages > INT32_MAX || k->table_stride < k->max_pages) return WQ_ERR_SHAPE;
+  if (T < 0 || B < 0 || T > ((int64_t)1 << 30) || B > ((int64_t)1 << 24)) return WQ_ERR_SHAPE;
+  if (T == 0 || B == 0) return WQ_OK;
+  if (!k->k || !k->v || !k->k_scale || !k->v_scale || !k->table || !offsets || !lens) return WQ_ERR_NULL;
+  if (!al16(k->k) || !al16(k->v)) return WQ_ERR_ALIGN;
+  out->k = k->k;
+  out->v = k->v;
+  out->k_scale = k->k_scale;
+  out->v_scale = k->v_scale;
+  out->table = k->table;
+  out->table_stride = k->table_stride;
+  out->pages = (int)k->pages;
+  out->H = (int)k->heads;
+  out->P = (int)k->page_tokens;
+  out->D = (int)k->head_dim;
+  out->max_pages = (int)k->max_pages;
+  out->offsets = offsets;
+  out->lens = lens;
+  out->B = (int)B;
+  out->T = T;
+  return WQ_OK;
+}
+
+int wq_kv_append(wq_ctx* c, const wq_kv_cache* k, const void* k_new, int64_t ldk, const void* v_new, int64_t ldv,
+                 int64_t T, int64_t B, const int64_t* offsets, const int32_t* lens, void* stream) {
+  if (!c || !k) return WQ_ERR_NULL;
+  wq::KvArgs a{};
+  if (int r = kv_args(k, T, B, offsets, lens, &a)) return r;
+  if (ldk < k->heads * k->head_dim || ldv < k->heads * k->head_dim) return WQ_ERR_SHAPE;
+  if (T == 0 || B == 0) return WQ_OK;
+  if (!k_new || !v_new) return WQ_ERR_NULL;
+  if (!al16(k_new) || !al16(v_new) || ldk % 8 != 0 || ldv % 8 != 0) return WQ_ERR_ALIGN;
+  DeviceGuard g(c->device);
+  hipError_t e = wq::launch_kv_append(a, k->code == WQ_KV_INT8, static_cast<const uint16_t*>(k_new), ldk,
+                                      static_cast<const uint16_t*>(v_new), ldv, static_cast<hipStream_t>(stream));
+  if (c->log)
+    std::fprintf(stderr, "[wq] kv_append %s T=%lld B=%lld heads=%lld D=%lld page=%lld\n",
+                 k->code == WQ_KV_INT8 ? "int8" : "e4m3", (long long)T, (long long)B, (long long)k->heads,
+                 (long long)k->head_dim, (long long)k->page_tokens);
+  return status_of(e);
+}
+
+// q_heads a multiple of the cache's heads; row tiles are counted in 32 bits
+static bool kv_heads_ok(const wq_kv_cache* k, int64_t q_heads, int64_t T, int64_t B) {
+  return q_heads >= k->heads && q_heads % k->heads == 0 && q_heads <= (1 << 20) &&
+         T * (q_heads / k->heads) / 16 + B < ((int64_t)1 << 31);
+}
+
+int64_t wq_kv_attention_workspace_bytes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B) {
+  if (!c || !k) return -WQ_ERR_NULL;
+  if (k->heads < 1 || k->page_tokens < 16 || k->page_tokens > 256 || k->max_pages < 1 || k->max_pages > INT32_MAX ||
+      !wq::kv_head_dim_ok(k->head_dim) || T < 0 || B < 0 || T > ((int64_t)1 << 30) || B > ((int64_t)1 << 24) ||
+      !kv_heads_ok(k, q_heads, T, B))
+    return -WQ_ERR_SHAPE;
+  if (T == 0 || B == 0) return 0;
+  wq::KvArgs a{};
+  a.H = (int)k->heads;
+  a.P = (int)k->page_tokens;
+  a.D = (int)k->head_dim;
+  a.max_pages = (int)k->max_pages;
+  a.B = (int)B;
+  a.T = T;
+  return (int64_t)wq::kv_attention_workspace(a, (int)(q_heads / k->heads), c->num_cu);
+}
+
+int wq_kv_attention(wq_ctx* c, const wq_kv_cache* k, const void* q, int64_t ldq, int64_t T, int64_t q_heads, int64_t B,
+                    const int64_t* offsets, const int32_t* lens, float scale, int causal, void* out, int64_t ldo,
+                    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!c || !k) return WQ_ERR_NULL;
+  wq::KvAttnArgs a{};
+  if (int r = kv_args(k, T, B, offsets, lens, &a.c)) return r;
+  if (!kv_heads_ok(k, q_heads, T, B)) return WQ_ERR_SHAPE;
+  if (ldq < q_heads * k->head_dim || ldo < q_heads * k->head_dim || !std::isfinite(scale)) return WQ_ERR_SHAPE;
+  if (T == 0 || B == 0) return WQ_OK;
+  if (!q || !out) return WQ_ERR_NULL;
+  if (!al16(q) || !al16(out) || ldq % 8 != 0 || ldo % 8 != 0) return WQ_ERR_ALIGN;
+  a.q = static_cast<const uint16_t*>(q);
+  a.ldq = ldq;
+  a.out = static_cast<uint16_t*>(out);
+  a.ldo = ldo;
+  a.lse = lse;
+  a.scale = scale;
+  a.R = (int)(q_heads / k->heads);
+  a.causal = causal != 0;
+  if (workspace == nullptr) {
+    workspace = c->ws;
+    workspace_bytes = c->ws_bytes;
+  } else if (!al16(workspace)) {
+    return WQ_ERR_ALIGN;
+  }
+  if (workspace_bytes < wq::kv_attention_workspace(a.c, a.R, c->num_cu)) return WQ_ERR_WORKSPACE;
+  DeviceGuard g(c->device);
+  hipError_t e = wq::launch_kv_attention(a, k->code == WQ_KV_INT8, c->num_cu, workspace,
+                                         static_cast<hipStream_t>(stream));
+  if (c->log)
+    std::fprintf(stderr, "[wq] kv_attention %s T=%lld B=%lld heads=%lld/%lld D=%lld page=%lld parts=%d\n",
+                 k->code == WQ_KV_INT8 ? "int8" : "e4m3", (long long)T, (long long)B, (long long)q_heads,
+                 (long long)k->heads, (long long)k->head_dim, (long long)k->page_tokens, wq::kv_attention_splits(a.c, a.R, c->num_cu));
   return status_of(e);
 }
 

@@ -33,6 +33,11 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rn(float f) {
   return u >> 16;
 }
 
+// f32 -> bf16 bits, round to nearest even, any input: a NaN stays one (v_cvt_pk_bf16_f32)
+__device__ __forceinline__ uint32_t f32_to_bf16_nan(float f) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f);
+}
+
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));

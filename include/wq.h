@@ -50,7 +50,15 @@ enum {
 /* input element types */
 enum { WQ_IN_BF16 = 1, WQ_IN_F32 = 2 };
 /* GEMM payload types */
-enum { WQ_PAYLOAD_INT8 = 1, WQ_PAYLOAD_FP8_E4M3 = 2, WQ_PAYLOAD_MXFP8 = 3 };
+enum {
+  WQ_PAYLOAD_INT8 = 1,
+  WQ_PAYLOAD_FP8_E4M3 = 2,
+  WQ_PAYLOAD_MXFP8 = 3,
+  WQ_PAYLOAD_MXFP4 = 4,    /* E2M1 activations on E2M1 weights, 32-element blocks       */
+  WQ_PAYLOAD_MXFP8_W4 = 5  /* E4M3 activations on E2M1 weights, 32-element blocks       */
+};
+/* code types of a paged cache */
+enum { WQ_KV_E4M3 = 1, WQ_KV_INT8 = 2 };
 /* GEMM epilogues */
 enum { WQ_EPI_BF16 = 1, WQ_EPI_SWIGLU_F32 = 2 };
 /* weight layout of wq_matmul_desc.b: plain [batch][N][K], or the fragment order of
@@ -163,6 +171,27 @@ int wq_group_quant_fp8_ue8m0(wq_ctx* ctx, const void* x, int64_t T, int64_t G, i
 int wq_group_quant_mxfp8(wq_ctx* ctx, const void* x, int64_t T, int64_t G, int64_t D,
                          uint8_t* x_q, int32_t* x_s, void* stream);
 
+/* ---- microscaled 4-bit blocks ---------------------------------------------------------
+ * The same blocks of 32 elements in 4 bits: E2M1 (sign, two exponent bits of bias 1, one
+ * fraction bit; magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6), two codes to a byte, the element with
+ * the even index in the low four bits.  x: bf16 [T, G, D] contiguous, D % 32 == 0.
+ *   a = max |x[t, g, 32h .. 32h+31]|,  e = max(-127, smallest e with 2^e >= a / 6)
+ *   code = E2M1(x * 2^-e), nearest-even                       (x_q: uint8 [T, G, D/2])
+ *   byte e + 127 at the place wq_group_quant_mxfp8 gives it (x_s: int32 [G, PH, TA],
+ *   PH = ceil(D / 128)); every other byte of x_s zero.
+ * A block that holds a NaN or an infinity gets byte 255, UE8M0's NaN, and zero codes: what
+ * reads it (the inverse below, the products) gives NaN.
+ * Weights [N, K] are cast by the same call as [T = N, G = 1, D = K]; the casts of G groups
+ * one behind the other are the operand b and its scales of the 4-bit payloads.
+ * TA * G * PH < 2^31 (WQ_ERR_SHAPE otherwise). */
+int wq_group_quant_mxfp4(wq_ctx* ctx, const void* x, int64_t T, int64_t G, int64_t D, uint8_t* x_q, int32_t* x_s,
+                         void* stream);
+
+/* The inverse: y[t, g, d] = code * 2^(byte - 127), bf16 [T, G, D] contiguous (exact: every
+ * value of a finite block is a bf16 number; byte 255 gives NaN). */
+int wq_group_dequant_mxfp4(wq_ctx* ctx, const uint8_t* x_q, const int32_t* x_s, int64_t T, int64_t G, int64_t D,
+                           void* y, void* stream);
+
 /* ---- quantised matmul ---------------------------------------------------------------
  * INT8 (section 一 of the W8A8 article; npu_quant_matmul, and the tuple-reuse path where
  * an upstream producer already gave (x_q, x_scale)):
@@ -194,9 +223,17 @@ int wq_group_quant_mxfp8(wq_ctx* ctx, const void* x, int64_t T, int64_t G, int64
  *   y[m, g, n] = bf16_RN( sum over 32-deep blocks kb of 2^(e_a(m,g,kb))
  *                         * 2^(b_scale[g, n, kb] - 127) * sum_{k in kb} a[m,g,k] * b[g,n,k] );
  *   any M (decode-sized M on the weight-streaming kernel, larger M on the tiled one).
+ * 4-bit weights in 32-element blocks: payload WQ_PAYLOAD_MXFP4 (a = E2M1 pairs of
+ *   wq_group_quant_mxfp4, K/2 bytes a row) or WQ_PAYLOAD_MXFP8_W4 (a = E4M3 codes of
+ *   wq_group_quant_mxfp8, K bytes a row); lda and a_batch_stride in bytes; a_scale = that
+ *   call's storage [G, K/128, TA]; b = E2M1 pairs [G][N][K/2], b_batch_stride in bytes;
+ *   b_scale = int32 words [G][K/128][N], the storage of wq_group_quant_mxfp4 on each group's
+ *   weights (not floats); any M, N % 16 == 0, K % 128 == 0, K <= 131072, G <= 65535;
+ *   y[m, g, n] = bf16_RN( sum over 32-deep blocks of 2^(e_a + e_b) sum_{k in kb} a b ).
+ *   seg_offsets, acc_out, WQ_EPI_SWIGLU_F32 and WQ_LAYOUT_FRAGMENT: WQ_ERR_UNSUPPORTED.
  * acc_out (INT8 dense only, may be NULL): the raw int32 accumulators [M, N], row stride N. */
 typedef struct {
-  int32_t payload;         /* WQ_PAYLOAD_INT8, WQ_PAYLOAD_FP8_E4M3 or WQ_PAYLOAD_MXFP8    */
+  int32_t payload;         /* one of WQ_PAYLOAD_...                                       */
   int32_t epilogue;        /* WQ_EPI_BF16 or WQ_EPI_SWIGLU_F32                            */
   int64_t M, N, K;         /* rows (per batch for strided batches), columns, depth        */
   int64_t batch;           /* 1 = dense; G for FP8 groups; E for segments                 */
@@ -292,6 +329,69 @@ int wq_pack_weight_i8(wq_ctx* ctx, const int8_t* w, int64_t N, int64_t K, int64_
 int wq_fused_quant_matmul_packed(wq_ctx* ctx, const void* x, int64_t M, int64_t K, int64_t ldx,
                                  const int8_t* wp, const float* w_scale, int64_t N, void* y, int64_t ldy,
                                  int8_t* x_q_out, float* x_scale_out, int32_t* acc_out, void* stream);
+
+/* ---- paged 8-bit cache of keys and values, and attention over it -------------------------
+ * A page holds page_tokens consecutive tokens of a sequence, for every head, in 8-bit codes
+ * with one UE8M0 byte for each (page, head) of keys and of values:
+ *   x = code * 2^(byte - 127); code E4M3 (WQ_KV_E4M3) or int8 (WQ_KV_INT8).
+ * Values lie with the tokens innermost (the order the matrix unit contracts them in).
+ * table[b][i] is the page of tokens i * page_tokens .. of sequence b.  A page number outside
+ * [0, pages) is no page: what would be written there is dropped, its tokens are not attended.
+ * Rows belong to sequences by offsets: device int64 [B + 1], non-decreasing from 0; rows
+ * [offsets[b], offsets[b+1]) are the newest tokens of sequence b in order, and lens[b] (device
+ * int32) is its token count with them, so row i of n has position lens[b] - n + i.  A token at
+ * a negative position or behind max_pages * page_tokens is not written and not attended;
+ * rows behind offsets[B] are not read, and their outputs stay as they were. */
+typedef struct {
+  int32_t code;            /* WQ_KV_E4M3 or WQ_KV_INT8                                    */
+  int64_t pages, heads;    /* 1 .. 2^31 - 1 pages, 1 .. 65535 heads                       */
+  int64_t page_tokens;     /* a multiple of 16, 16 .. 256                                 */
+  int64_t head_dim;        /* 64, 128 or 256                                              */
+  void* k;                 /* codes [pages][heads][page_tokens][head_dim]                 */
+  void* v;                 /* codes [pages][heads][head_dim][page_tokens]                 */
+  uint8_t* k_scale;        /* UE8M0 bytes [pages][heads]                                  */
+  uint8_t* v_scale;        /* UE8M0 bytes [pages][heads]                                  */
+  const int32_t* table;    /* device [B][table_stride]                                    */
+  int64_t table_stride;    /* entries between sequences                                   */
+  int64_t max_pages;       /* entries of a sequence, <= table_stride                      */
+} wq_kv_cache;
+
+/* Quantise new rows into the cache.  k_new, v_new: bf16 [T, heads * head_dim], row strides
+ * ldk, ldv (elements).  For each (page, head) that rows fall in, with a = max |x| of them and
+ * e = max(-127, smallest e with 2^e >= a / c), c = 448 (E4M3) or 127 (int8):
+ *   a page whose first slot is among them is begun anew with byte e + 127; in any other the
+ *   byte becomes max(its byte, e + 127), and where it grows, by d, the codes in front of the
+ *   new rows become RN(code * 2^-d);
+ *   the new codes are RN(x * 2^(127 - byte)) (nearest-even).  Slots behind them keep their codes.
+ * A NaN or an infinity among the rows makes the byte 255 (UE8M0's NaN) and their codes zero:
+ * the page's tokens of that head read as NaN until the page is begun anew.
+ * The same call again writes the same bytes.  A page written by the call is in the table of
+ * one sequence only (a shared one is copied first). */
+int wq_kv_append(wq_ctx* ctx, const wq_kv_cache* cache, const void* k_new, int64_t ldk, const void* v_new, int64_t ldv,
+                 int64_t T, int64_t B, const int64_t* offsets, const int32_t* lens, void* stream);
+
+/* Attention of T query rows over the cache: q bf16 [T, q_heads * head_dim], row stride ldq;
+ * q_heads = R * heads, query head i reads cache head i / R.  Row i of n of sequence b sees the
+ * tokens 0 .. lens[b] - n + i (causal != 0) or 0 .. lens[b] - 1:
+ *   s_j = scale * sum_d q_d k_jd,  lse = log sum_j exp(s_j),  out_d = sum_j exp(s_j - lse) v_jd
+ * out: bf16 [T, q_heads * head_dim], row stride ldo (it may not overlap q); lse: f32
+ * [T, q_heads] or NULL.  A row that sees no token gets zeros and lse = -inf.  Codes behind
+ * lens[b] may hold anything; E4M3's NaN patterns in front of it, which wq_kv_append never
+ * writes, may reach rows that do not see them.  The products take the codes exactly (bf16),
+ * sums and softmax statistics are f32, and a weight exp(s - max) is rounded to bf16.
+ * workspace: device memory, 16-byte aligned, of at least wq_kv_attention_workspace_bytes()
+ * for these sizes, that no other call uses until this one is done (the parts of a sequence
+ * that is split over workgroups are joined there); its contents need no initialisation.  NULL:
+ * the context's workspace, with the context's rule of one stream at a time. */
+int wq_kv_attention(wq_ctx* ctx, const wq_kv_cache* cache, const void* q, int64_t ldq, int64_t T, int64_t q_heads,
+                    int64_t B, const int64_t* offsets, const int32_t* lens, float scale, int causal, void* out,
+                    int64_t ldo, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The bytes of workspace that wq_kv_attention takes for these sizes (of the cache: heads,
+ * page_tokens, head_dim and max_pages; no pointer is read), at most 64 MiB; 0 where it needs none; a
+ * negative value is -status.  Host only: no device work. */
+int64_t wq_kv_attention_workspace_bytes(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T, int64_t q_heads,
+                                        int64_t B);
 
 /* ---- expert sort (MoE) ---------------------------------------------------------------
  * "DeepSeek V4 950" section 3.2: sort the (token, slot) pairs by expert id before the

@@ -25,6 +25,8 @@ Modules:
   int8_linear per-token INT8 quant, INT32 GEMM, scale epilogue, fused composition.
   fp8_group   per-token-group FP8 quant, packed UE8M0 writer, grouped FP8 contraction.
   moe         expert sort, RMSNorm+quant, segmented GEMM, SwiGLU+requant.
+  mxfp4       4-bit microscaled blocks: quant, inverse, product.
+  kv_cache    paged 8-bit cache: append, attention.
 """
 
-from . import numerics, int8_linear, fp8_group, moe  # noqa: F401
+from . import numerics, int8_linear, fp8_group, moe, mxfp4, kv_cache  # noqa: F401
