@@ -118,70 +118,4 @@ hipError_t launch_group_dequant_mxfp4(const uint8_t* xq, const int32_t* xs, int6
   return hipGetLastError();
 }
 
-// ---- product -----------------------------------------------------------------------------
-// y[m, g, n] = sum over 32-deep blocks of 2^(ea + eb) sum a b, by
-// v_mfma_scale_f32_16x16x128_f8f6f4: its 128-deep step is one scale word of each operand.
-// Operand layout (measured with one-hot inputs): lane group q (lanes 16q .. 16q+15) holds, of
-// a 4-bit operand, K 32q .. 32q+31 in its first four registers; of an 8-bit operand K 16q ..
-// 16q+15 in the first four and 64+16q .. 64+16q+15 in the last four; the scale operand of lane
-// group s applies to K 32s .. 32s+31 of either.
-
-template <bool A8>
-__device__ __forceinline__ v8i load_a_frag(const uint8_t* row, int kb, int q) {
-  if constexpr (A8) {
-    const v4i lo = *reinterpret_cast<const v4i*>(row + kb * 128 + q * 16);
-    const v4i hi = *reinterpret_cast<const v4i*>(row + kb * 128 + 64 + q * 16);
-    return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  } else {
-    const v4i lo = *reinterpret_cast<const v4i*>(row + kb * 64 + q * 16);
-    return v8i{lo[0], lo[1], lo[2], lo[3], 0, 0, 0, 0};
-  }
-}
-
-__device__ __forceinline__ v8i load_w_frag(const uint8_t* row, int kb, int q) {
-  const v4i lo = *reinterpret_cast<const v4i*>(row + kb * 64 + q * 16);
-  return v8i{lo[0], lo[1], lo[2], lo[3], 0, 0, 0, 0};
-}
-
-// A wave makes 16 rows x 16 columns over all of K, operands straight from memory.
-template <bool A8>
-__global__ __launch_bounds__(256) void k_mx4_plain(Mx4Args p) {
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int nx = (p.N / 16 + 3) / 4;  // workgroups across the columns
-  const int g = blockIdx.y, m0 = (int)(blockIdx.x / nx) * 16, n0 = ((int)(blockIdx.x % nx) * 4 + wv) * 16;
-  if (n0 >= p.N) return;
-  const int cl = lane & 15, q = lane >> 4, KT = p.K >> 7;
-  const int row = min(m0 + cl, p.M - 1);
-  const uint8_t* A = p.a + g * p.a_batch_stride + row * p.lda;
-  const uint8_t* W = p.w + g * p.w_batch_stride + (int64_t)(n0 + cl) * (p.K / 2);
-  const int32_t* SA = p.a_scale + (int64_t)g * KT * p.a_tokens + row;
-  const int32_t* SW = p.w_scale + (int64_t)g * KT * p.N + n0 + cl;
-  v4f acc{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int kb = 0; kb < KT; ++kb) {
-    const v8i a = load_a_frag<A8>(A, kb, q), w = load_w_frag(W, kb, q);
-    const int sa = (SA[kb * p.a_tokens] >> (8 * q)) & 0xFF, sw = (SW[(int64_t)kb * p.N] >> (8 * q)) & 0xFF;
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, w, acc, A8 ? 0 : 4, 4, 0, sa, 0, sw);
-  }
-  // the matrix results are pinned before the per-lane stores: the compiler may otherwise move
-  // a matrix instruction into the branch, where part of its lanes are off
-  asm volatile("" : "+v"(acc));
-  uint16_t* Y = p.y + g * p.y_batch_stride;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = m0 + 4 * q + i;  // output layout: column lane % 16, row 4 (lane / 16) + i
-    if (m < p.M) Y[m * p.ldy + n0 + cl] = (uint16_t)f32_to_bf16_nan(acc[i]);
-  }
-}
-
-hipError_t launch_mx4(const Mx4Args& a, bool a8, hipStream_t st) {
-  const int64_t wgs = (int64_t)((a.N / 16 + 3) / 4) * ((a.M + 15) / 16);
-  if (wgs >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)wgs, (unsigned)a.batch);
-  if (a8)
-    hipLaunchKernelGGL(k_mx4_plain<true>, grid, dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL(k_mx4_plain<false>, grid, dim3(256), 0, st, a);
-  return hipGetLastError();
-}
-
 }  // namespace wq

@@ -618,7 +618,8 @@ static int mx4_matmul(wq_ctx* c, const wq_matmul_desc* d, hipStream_t st) {
   const bool a8 = d->payload == WQ_PAYLOAD_MXFP8_W4;
   const int64_t row = a8 ? K : K / 2;  // bytes of an activation row
   if (N % 16 != 0 || K % 128 != 0 || K > 131072 || G > 65535) return WQ_ERR_SHAPE;
-  if (d->lda < row || d->ldy < N || d->a_batch_stride < 0 || d->y_batch_stride < 0 || d->b_batch_stride < 0)
+  // 128 rows of a tile are addressed by 32-bit offsets
+  if (d->lda < row || d->lda >= (1 << 23) || d->ldy < N || d->a_batch_stride < 0 || d->y_batch_stride < 0 || d->b_batch_stride < 0)
     return WQ_ERR_SHAPE;
   if (d->a_scale_tokens < (M + 3) / 4 * 4) return WQ_ERR_SHAPE;
   if (G > 1 && d->b_batch_stride < N * (K / 2)) return WQ_ERR_SHAPE;
@@ -640,7 +641,7 @@ static int mx4_matmul(wq_ctx* c, const wq_matmul_desc* d, hipStream_t st) {
   t.ldy = d->ldy;
   t.y_batch_stride = d->y_batch_stride;
   t.M = (int)M; t.N = (int)N; t.K = (int)K; t.batch = (int)G;
-  hipError_t e = wq::launch_mx4(t, a8, st);
+  hipError_t e = wq::launch_mx4(t, a8, c->num_cu, st);
   if (c->log)
     std::fprintf(stderr, "[wq] quant_matmul %s M=%lld N=%lld K=%lld groups=%lld\n", a8 ? "mxfp8 x mxfp4" : "mxfp4",
                  (long long)M, (long long)N, (long long)K, (long long)G);

@@ -115,7 +115,7 @@ hipError_t launch_group_quant_mxfp4(const uint16_t* x, int64_t T, int G, int D, 
                                     hipStream_t st);
 hipError_t launch_group_dequant_mxfp4(const uint8_t* xq, const int32_t* xs, int64_t T, int G, int D, uint16_t* y,
                                       hipStream_t st);
-// Product on 4-bit weights (k_mxfp4.hip), N % 16 == 0, K % 128 == 0.
+// Product on 4-bit weights (k_mx4_gemm.hip), N % 16 == 0, K % 128 == 0, lda < 2^23.
 struct Mx4Args {
   const uint8_t* a;        // rows of E2M1 pairs (K/2 bytes) or E4M3 codes (K bytes)
   int64_t lda;             // bytes between rows
@@ -130,7 +130,7 @@ struct Mx4Args {
   int M, N, K, batch;
 };
 // a8: E4M3 activation codes instead of E2M1 pairs
-hipError_t launch_mx4(const Mx4Args& a, bool a8, hipStream_t st);
+hipError_t launch_mx4(const Mx4Args& a, bool a8, int num_cu, hipStream_t st);
 
 // The paged 8-bit cache (k_kv.hip).  A page holds P tokens of every head: k [page][H][P][D],
 // v [page][H][D][P], one UE8M0 byte for each (page, head) of either.

@@ -225,7 +225,7 @@ int wq_group_dequant_mxfp4(wq_ctx* ctx, const uint8_t* x_q, const int32_t* x_s, 
  *   any M (decode-sized M on the weight-streaming kernel, larger M on the tiled one).
  * 4-bit weights in 32-element blocks: payload WQ_PAYLOAD_MXFP4 (a = E2M1 pairs of
  *   wq_group_quant_mxfp4, K/2 bytes a row) or WQ_PAYLOAD_MXFP8_W4 (a = E4M3 codes of
- *   wq_group_quant_mxfp8, K bytes a row); lda and a_batch_stride in bytes; a_scale = that
+ *   wq_group_quant_mxfp8, K bytes a row); lda (< 2^23) and a_batch_stride in bytes; a_scale = that
  *   call's storage [G, K/128, TA]; b = E2M1 pairs [G][N][K/2], b_batch_stride in bytes;
  *   b_scale = int32 words [G][K/128][N], the storage of wq_group_quant_mxfp4 on each group's
  *   weights (not floats); any M, N % 16 == 0, K % 128 == 0, K <= 131072, G <= 65535;

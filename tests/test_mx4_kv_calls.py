@@ -51,7 +51,7 @@ def _desc(**kw):
 
 @pytest.mark.parametrize("kw, want", [
     (dict(M=0), 0), (dict(N=24), SHAPE), (dict(K=192), SHAPE), (dict(K=131200), SHAPE), (dict(batch=65536), SHAPE),
-    (dict(lda=112), SHAPE), (dict(payload=5), SHAPE), (dict(ldy=16), SHAPE), (dict(a_scale_tokens=3), SHAPE),
+    (dict(lda=112), SHAPE), (dict(lda=1 << 23), SHAPE), (dict(payload=5), SHAPE), (dict(ldy=16), SHAPE), (dict(a_scale_tokens=3), SHAPE),
     (dict(batch=2, b_batch_stride=16), SHAPE), (dict(a_batch_stride=-16), SHAPE), (dict(y_batch_stride=-8), SHAPE),
     (dict(a=None), NULL), (dict(a_scale=None), NULL), (dict(b=None), NULL), (dict(b_scale=None), NULL),
     (dict(y=None), NULL), (dict(a=P + 8), ALIGN), (dict(lda=136), ALIGN), (dict(ldy=36), ALIGN), (dict(b_scale=P + 4), ALIGN),
