@@ -177,14 +177,21 @@ def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _on(fn, first, *others):
+    """(context handle, raw current stream) of the device that all the tensors are on.  The calls
+    that decode steps make take this way: the public stream object costs 2 us, these lookups 0.2."""
+    idx = first.get_device()
+    for t in others:
+        if t.get_device() != idx:
+            raise ValueError(f"{fn}: tensors on {first.device} and {t.device}")
+    ctx = _CTX.get(idx)
+    if ctx is None:
+        ctx = context(first.device)
+    return ctx.handle, torch._C._cuda_getCurrentRawStream(idx)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
-
-
-def _same_device(fn, first, *others):
-    for t in others:
-        if t.device != first.device:
-            raise ValueError(f"{fn}: tensors on {first.device} and {t.device}")
 
 
 def _check(fn, st):
@@ -261,21 +268,20 @@ def wq_group_quant_mxfp4(x: torch.Tensor, x_q: torch.Tensor | None = None, stora
     T, G, D = x.shape
     if D % 32:
         raise ValueError("D must be a multiple of 32")
-    _, PH, TA = packed_scale_dims(T, D, 32)
+    PH, TA = (D + 127) // 128, (T + 3) // 4 * 4
     if x_q is None:
-        x_q = torch.empty((T, G, D // 2), dtype=torch.uint8, device=x.device)
+        x_q = x.new_empty((T, G, D // 2), dtype=torch.uint8)
+    elif x_q.shape != (T, G, D // 2) or x_q.dtype != torch.uint8 or not x_q.is_contiguous():
+        raise ValueError("x_q must be contiguous uint8 [T, G, D/2]")
     if storage is None:
-        storage = torch.empty((G, PH, TA), dtype=torch.int32, device=x.device)
-    if x_q.shape != (T, G, D // 2) or x_q.dtype != torch.uint8 or not x_q.is_contiguous() \
-            or storage.shape != (G, PH, TA) or storage.dtype != torch.int32 or not storage.is_contiguous():
-        raise ValueError("x_q must be uint8 [T, G, D/2] and storage int32 [G, PH, TA], both contiguous")
-    _same_device("wq_group_quant_mxfp4", x, x_q, storage)
-    if x.numel() > 0:
-        st = lib().wq_group_quant_mxfp4(context(x.device).handle, x.data_ptr(), T, G, D, x_q.data_ptr(),
-                                        storage.data_ptr(), _stream(x.device))
+        storage = x.new_empty((G, PH, TA), dtype=torch.int32)
+    elif storage.shape != (G, PH, TA) or storage.dtype != torch.int32 or not storage.is_contiguous():
+        raise ValueError("storage must be contiguous int32 [G, PH, TA]")
+    h, stream = _on("wq_group_quant_mxfp4", x, x_q, storage)
+    st = lib().wq_group_quant_mxfp4(h, x.data_ptr(), T, G, D, x_q.data_ptr(), storage.data_ptr(), stream)
+    if st:
         _check("wq_group_quant_mxfp4", st)
-    x_s = storage.transpose(-1, -2)[:, :T, :].transpose(0, 1)
-    return x_q, x_s, storage
+    return x_q, storage.as_strided((T, G, PH), (1, PH * TA, TA)), storage
 
 
 def wq_group_dequant_mxfp4(x_q: torch.Tensor, storage: torch.Tensor, y: torch.Tensor | None = None):
@@ -285,48 +291,53 @@ def wq_group_dequant_mxfp4(x_q: torch.Tensor, storage: torch.Tensor, y: torch.Te
     T, G, D = x_q.shape[0], x_q.shape[1], 2 * x_q.shape[2]
     if D % 32:
         raise ValueError("D must be a multiple of 32")
-    _, PH, TA = packed_scale_dims(T, D, 32)
-    if storage.shape != (G, PH, TA) or storage.dtype != torch.int32 or not storage.is_contiguous():
+    if storage.shape != (G, (D + 127) // 128, (T + 3) // 4 * 4) or storage.dtype != torch.int32 \
+            or not storage.is_contiguous():
         raise ValueError("storage must be contiguous int32 [G, PH, TA]")
     if y is None:
-        y = torch.empty((T, G, D), dtype=torch.bfloat16, device=x_q.device)
+        y = x_q.new_empty((T, G, D), dtype=torch.bfloat16)
     elif y.shape != (T, G, D) or y.dtype != torch.bfloat16 or not y.is_contiguous():
         raise ValueError("y must be contiguous bf16 [T, G, D]")
-    _same_device("wq_group_dequant_mxfp4", x_q, storage, y)
-    if x_q.numel() > 0:
-        st = lib().wq_group_dequant_mxfp4(context(x_q.device).handle, x_q.data_ptr(), storage.data_ptr(), T, G, D,
-                                          y.data_ptr(), _stream(x_q.device))
+    h, stream = _on("wq_group_dequant_mxfp4", x_q, storage, y)
+    st = lib().wq_group_dequant_mxfp4(h, x_q.data_ptr(), storage.data_ptr(), T, G, D, y.data_ptr(), stream)
+    if st:
         _check("wq_group_dequant_mxfp4", st)
     return y
 
 
 def _mx4_matmul(a, a_scale, b, b_scale, G, y):
-    if a.dim() != 3 or b.dim() != 3 or a.dtype != torch.uint8 or b.dtype != torch.uint8 or a.stride(2) != 1 \
-            or b.shape[0] != G or a.shape[1] != G or b.stride(2) != 1 or (b.shape[1] > 1 and b.stride(1) != b.shape[2]):
-        raise ValueError("a must be uint8 [M, G, K/2] or [M, G, K], b uint8 [G, N, K/2], G = fp8_groups")
-    M, N, K = a.shape[0], b.shape[1], 2 * b.shape[2]
-    if a.shape[2] not in (K // 2, K):
-        raise ValueError("a's rows must hold K/2 bytes (E2M1 pairs) or K bytes (E4M3)")
-    for name, s, rows in (("a_scale", a_scale, (M + 3) // 4 * 4), ("b_scale", b_scale, N)):
-        if s.dtype != torch.int32 or s.shape[:2] != (G, (K + 127) // 128) or s.shape[2] < rows or not s.is_contiguous():
-            raise ValueError(f"{name} must be the contiguous int32 storage of its operand's quantisation")
-    if b_scale.shape[2] != N:
-        raise ValueError("b_scale must be [G, K/128, N]")
+    if a.dim() != 3 or b.dim() != 3 or a_scale.dim() != 3 or b_scale.dim() != 3 or a.dtype != torch.uint8 \
+            or b.dtype != torch.uint8 or a_scale.dtype != torch.int32 or b_scale.dtype != torch.int32:
+        raise ValueError("a must be uint8 [M, G, K/2] or [M, G, K], b uint8 [G, N, K/2], their scales int32 storages")
+    M, Ga, row = a.shape
+    Gb, N, half = b.shape
+    K = 2 * half
+    TA = a_scale.shape[2]
+    if Ga != G or Gb != G or (row != half and row != K):
+        raise ValueError("a and b must hold fp8_groups groups of K/2 bytes (E2M1 pairs) or, a, K bytes (E4M3)")
+    sa, sb = a.stride(), b.stride()
+    if sa[2] != 1 or sb[2] != 1 or (N > 1 and sb[1] != half):
+        raise ValueError("a's and b's rows must be dense, b's consecutive")
+    kt = (K + 127) // 128
+    if a_scale.shape != (G, kt, TA) or TA < (M + 3) // 4 * 4 or not a_scale.is_contiguous() or b_scale.shape != (G, kt, N) \
+            or not b_scale.is_contiguous():
+        raise ValueError("a_scale must be contiguous [G, K/128, align4(M) or more] and b_scale [G, K/128, N]")
     if y is None:
-        y = torch.empty((M, G, N), dtype=torch.bfloat16, device=a.device)
-    elif y.shape != (M, G, N) or y.dtype != torch.bfloat16 or y.stride(2) != 1:
-        raise ValueError("y must be bf16 [M, G, N] with unit stride along N")
-    _same_device("wq_quant_matmul", a, a_scale, b, b_scale, y)
-    d = MatmulDesc()
-    d.payload = WQ_PAYLOAD_MXFP8_W4 if a.shape[2] == K else WQ_PAYLOAD_MXFP4
-    d.epilogue, d.M, d.N, d.K, d.batch = WQ_EPI_BF16, M, N, K, G
+        y = a.new_empty((M, G, N), dtype=torch.bfloat16)
+        sy = (G * N, N)
+    else:
+        if y.shape != (M, G, N) or y.dtype != torch.bfloat16 or y.stride(2) != 1:
+            raise ValueError("y must be bf16 [M, G, N] with unit stride along N")
+        sy = y.stride()
+    h, stream = _on("wq_quant_matmul", a, a_scale, b, b_scale, y)
     # a stride of an axis of length one says nothing: the descriptor takes the dense one
-    d.a, d.lda = a.data_ptr(), a.stride(0) if M > 1 else a.shape[2]
-    d.a_batch_stride = a.stride(1) if G > 1 else 0
-    d.a_scale, d.a_scale_tokens = a_scale.data_ptr(), a_scale.shape[2]
-    d.b, d.b_batch_stride, d.b_scale = b.data_ptr(), b.stride(0) if G > 1 else 0, b_scale.data_ptr()
-    d.y, d.ldy, d.y_batch_stride = y.data_ptr(), y.stride(0) if M > 1 else N, y.stride(1) if G > 1 else 0
-    _check("wq_quant_matmul", lib().wq_quant_matmul(context(a.device).handle, ctypes.byref(d), _stream(a.device)))
+    d = MatmulDesc(WQ_PAYLOAD_MXFP8_W4 if row == K else WQ_PAYLOAD_MXFP4, WQ_EPI_BF16, M, N, K, G, None, a.data_ptr(),
+                   sa[0] if M > 1 else row, sa[1] if G > 1 else 0, a_scale.data_ptr(), TA, b.data_ptr(),
+                   sb[0] if G > 1 else 0, b_scale.data_ptr(), y.data_ptr(), sy[0] if M > 1 else N,
+                   sy[1] if G > 1 else 0, None, WQ_LAYOUT_PLAIN, 0)
+    st = lib().wq_quant_matmul(h, ctypes.byref(d), stream)
+    if st:
+        _check("wq_quant_matmul", st)
     return y
 
 
@@ -410,9 +421,9 @@ def kv_cache(pages: int, heads: int, page_tokens: int, head_dim: int, *, dtype=t
                    torch.zeros((pages, heads), dtype=torch.uint8, device=device))
 
 
-def _kv_desc(fn, cache, offsets, lens, table, *rows) -> KvCacheDesc:
+def _kv_desc(cache, offsets, lens, table):
     k, v, ks, vs = cache
-    if k.dim() != 4 or k.dtype not in (torch.uint8, torch.int8) or v.dtype != k.dtype:
+    if k.dim() != 4 or (k.dtype != torch.uint8 and k.dtype != torch.int8) or v.dtype != k.dtype:
         raise ValueError("a cache's codes are uint8 (E4M3) or int8, k [pages, heads, page_tokens, D]")
     pages, heads, page_tokens, D = k.shape
     if v.shape != (pages, heads, D, page_tokens) or ks.shape != (pages, heads) or vs.shape != (pages, heads) \
@@ -423,39 +434,41 @@ def _kv_desc(fn, cache, offsets, lens, table, *rows) -> KvCacheDesc:
     if offsets.dtype != torch.int64 or lens.dtype != torch.int32 or table.dtype != torch.int32:
         raise ValueError("offsets are int64, lens and table int32")
     B = lens.numel()
-    if offsets.shape != (B + 1,) or lens.shape != (B,) or table.dim() != 2 or table.shape[0] != B \
-            or not offsets.is_contiguous() or not lens.is_contiguous() or (table.numel() and table.stride(1) != 1):
+    if lens.dim() != 1 or offsets.shape != (B + 1,) or table.dim() != 2 or not offsets.is_contiguous() \
+            or not lens.is_contiguous():
         raise ValueError("offsets must be [B + 1], lens [B] and table [B, pages of a sequence]")
-    _same_device(fn, k, v, ks, vs, offsets, lens, table, *rows)
-    d = KvCacheDesc()
-    d.code = WQ_KV_INT8 if k.dtype == torch.int8 else WQ_KV_E4M3
-    d.pages, d.heads, d.page_tokens, d.head_dim = pages, heads, page_tokens, D
-    d.k, d.v, d.k_scale, d.v_scale = k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr()
-    d.table, d.max_pages = table.data_ptr(), table.shape[1]
-    d.table_stride = table.stride(0) if B > 1 else table.shape[1]
-    return d
+    Bt, width = table.shape
+    ts = table.stride()
+    if Bt != B or (width > 1 and ts[1] != 1):
+        raise ValueError("table must be [B, pages of a sequence] with dense rows")
+    return KvCacheDesc(WQ_KV_INT8 if k.dtype == torch.int8 else WQ_KV_E4M3, pages, heads, page_tokens, D, k.data_ptr(),
+                       v.data_ptr(), ks.data_ptr(), vs.data_ptr(), table.data_ptr(), ts[0] if B > 1 else width, width), B
 
 
 def _kv_rows(name, x, heads, D):
     """Row stride of bf16 rows [T, heads, D] whose last two axes are dense."""
-    if x.dim() != 3 or x.dtype != torch.bfloat16 or x.shape[1:] != (heads, D) \
-            or (x.numel() and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != D))):
-        raise ValueError(f"{name} must be bf16 [T, {heads}, {D}] with dense rows")
-    return x.stride(0) if x.shape[0] > 1 else heads * D
+    if x.dim() != 3 or x.dtype != torch.bfloat16 or x.shape[1] != heads or x.shape[2] != D:
+        raise ValueError(f"{name} must be bf16 [T, {heads}, {D}]")
+    s = x.stride()
+    if x.shape[0] and (s[2] != 1 or (heads > 1 and s[1] != D)):
+        raise ValueError(f"{name} must have dense rows")
+    return s[0] if x.shape[0] > 1 else heads * D
 
 
 def wq_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, offsets, lens, table) -> None:
     """Quantise the rows k, v bf16 [T, heads, D] into the cache, in place.  offsets int64
     [B + 1]: rows of each sequence; lens int32 [B]: its tokens, these rows among them; table
     int32 [B, pages of a sequence]."""
-    d = _kv_desc("wq_kv_append", cache, offsets, lens, table, k, v)
+    d, B = _kv_desc(cache, offsets, lens, table)
     ldk, ldv = _kv_rows("k", k, d.heads, d.head_dim), _kv_rows("v", v, d.heads, d.head_dim)
     T = k.shape[0]
     if v.shape[0] != T:
         raise ValueError("k and v must have the same number of rows")
-    st = lib().wq_kv_append(context(k.device).handle, ctypes.byref(d), k.data_ptr(), ldk, v.data_ptr(), ldv, T,
-                            lens.numel(), offsets.data_ptr(), lens.data_ptr(), _stream(k.device))
-    _check("wq_kv_append", st)
+    h, stream = _on("wq_kv_append", k, v, *cache, offsets, lens, table)
+    st = lib().wq_kv_append(h, ctypes.byref(d), k.data_ptr(), ldk, v.data_ptr(), ldv, T, B, offsets.data_ptr(),
+                            lens.data_ptr(), stream)
+    if st:
+        _check("wq_kv_append", st)
 
 
 def wq_kv_attention(cache: KvCache, q: torch.Tensor, offsets, lens, table, *, scale=None, causal=True, out=None,
@@ -463,32 +476,35 @@ def wq_kv_attention(cache: KvCache, q: torch.Tensor, offsets, lens, table, *, sc
     """Attention of the rows q bf16 [T, q_heads, D] over the cache (offsets, lens and table as
     in wq_kv_append, the newest rows last) -> bf16 [T, q_heads, D], and the f32 log-sum-exp
     [T, q_heads] with return_lse or lse=.  scale: 1 / sqrt(D) by default."""
+    d, B = _kv_desc(cache, offsets, lens, table)
     if q.dim() != 3:
         raise ValueError("q must be bf16 [T, q_heads, D]")
-    d = _kv_desc("wq_kv_attention", cache, offsets, lens, table, q)
     T, heads, D = q.shape
     ldq = _kv_rows("q", q, heads, d.head_dim)
     if out is None:
-        out = torch.empty((T, heads, D), dtype=torch.bfloat16, device=q.device)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    ldo = _kv_rows("out", out, heads, D)
-    if lse is None and return_lse:
-        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
-    if lse is not None and (lse.shape != (T, heads) or lse.dtype != torch.float32 or not lse.is_contiguous()):
-        raise ValueError("lse must be contiguous f32 [T, q_heads]")
-    _same_device("wq_kv_attention", q, out, *(() if lse is None else (lse,)))
-    ctx, B = context(q.device).handle, lens.numel()
-    need = lib().wq_kv_attention_workspace_bytes(ctx, ctypes.byref(d), T, heads, B)
+        out, ldo = q.new_empty((T, heads, D)), heads * D
+    else:
+        if out.dim() != 3 or out.shape[0] != T:
+            raise ValueError("out must have q's shape")
+        ldo = _kv_rows("out", out, heads, D)
+    if lse is not None:
+        if lse.shape != (T, heads) or lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous f32 [T, q_heads]")
+    elif return_lse:
+        lse = q.new_empty((T, heads), dtype=torch.float32)
+    h, stream = _on("wq_kv_attention", q, *cache, offsets, lens, table, out, *(() if lse is None else (lse,)))
+    by = ctypes.byref(d)
+    need = lib().wq_kv_attention_workspace_bytes(h, by, T, heads, B)
     if need < 0:
         _check("wq_kv_attention", -need)
     # from torch's allocator, call by call: calls on several streams and captured graphs share nothing
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    st = lib().wq_kv_attention(ctx, ctypes.byref(d), q.data_ptr(), ldq, T, heads, B, offsets.data_ptr(),
-                               lens.data_ptr(), D ** -0.5 if scale is None else float(scale), int(causal),
-                               out.data_ptr(), ldo, _ptr(lse), _ptr(ws), need, _stream(q.device))
-    _check("wq_kv_attention", st)
-    return (out, lse) if return_lse or lse is not None else out
+    ws = q.new_empty(need, dtype=torch.uint8) if need else None
+    st = lib().wq_kv_attention(h, by, q.data_ptr(), ldq, T, heads, B, offsets.data_ptr(), lens.data_ptr(),
+                               D ** -0.5 if scale is None else scale, causal, out.data_ptr(), ldo, _ptr(lse), _ptr(ws),
+                               need, stream)
+    if st:
+        _check("wq_kv_attention", st)
+    return (out, lse) if lse is not None else out
 
 
 def wq_fused_quant_matmul(x, w, w_scale, *, y=None, x_q_out=None, x_scale_out=None, acc_out=None):
