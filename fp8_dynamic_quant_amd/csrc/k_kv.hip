@@ -5,6 +5,8 @@
 // values [page][H][D][P]: the matrix instruction contracts q k over D and p v over tokens,
 // and wants eight consecutive terms of a contraction from each lane, so with this layout both
 // come from memory in operand order and nothing is transposed when they are read.
+#include <type_traits>
+
 #include "wq_device.h"
 #include "wq_kernels.h"
 
@@ -17,9 +19,9 @@ typedef unsigned v4u __attribute__((ext_vector_type(4)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-constexpr int kRowTile = 16;   // rows (of one cache head's queries) of a tile
-constexpr int kTokTile = 64;   // tokens of a wave's step
-constexpr int kAttnWaves = 4;
+constexpr int kTokTile = 64;     // tokens of a step
+constexpr int kAttnWaves = 4;    // waves of an attention workgroup
+constexpr int kPlanSeqs = 1024;  // sequences of one split launch (their work is summed up in LDS)
 
 // The sequence of slot `item` when sequence b owns the slots from offsets[b] * mul / div +
 // per * b on (the host knows neither a sequence's rows nor its length, so every sequence gets
@@ -141,10 +143,23 @@ __global__ __launch_bounds__(256) void k_kv_append(KvArgs c, const uint16_t* k_n
 }
 
 // ---- attention -----------------------------------------------------------------------------
+//
+// Lane l of a wave: j = l % 16, g = l / 16.  A wave takes 16-row tiles of one sequence and cache
+// head (a row is new token * R + query head of the group, so the R heads that share the keys share
+// their reads) and steps of 64 tokens, in 16-token groups g = 0 .. 3, each inside one page.
+//  * s^T = k q^T in four 16-token instructions t: the lane that supplies k row i takes token
+//    16 (i / 4) + 4 t + i % 4, so that the results, rows 4 g + r of column j, are tokens
+//    16 g + 4 t + r of row j: lane group g ends with the 16 consecutive tokens of its group.
+//  * o^T += v^T p^T: the lane supplies p of exactly those 16 tokens, from its own registers, and v
+//    of the same 16 tokens, 16 consecutive bytes of a value row.  Nothing crosses lanes but the
+//    running maximum.
+//  * the scales are one number for the lane's 16 tokens: the keys' multiplies s, the values' goes
+//    into the widening of v (E4M3) or multiplies p (int8).
 
-// eight codes -> eight bf16, exact (E4M3 has 4 significant bits, int8 at most 7)
+// eight codes -> eight bf16, exact (E4M3 has 4 significant bits, int8 at most 7); E4M3 times
+// `scale`, a power of two
 template <bool I8>
-__device__ __forceinline__ v8bf widen8(uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ v8bf widen8(uint32_t lo, uint32_t hi, float scale) {
   v4u o;
   if constexpr (I8) {
     const uint32_t w[2] = {lo, hi};
@@ -155,10 +170,10 @@ __device__ __forceinline__ v8bf widen8(uint32_t lo, uint32_t hi) {
       o[i] = __builtin_amdgcn_perm(f1, f0, 0x07060302u);  // the high halves: exact
     }
   } else {
-    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
-    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
-    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
-    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false));
+    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true));
+    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false));
+    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true));
   }
   return __builtin_bit_cast(v8bf, o);
 }
@@ -168,222 +183,710 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
   return byte == 255u ? __uint_as_float(0x7FC00000u) : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
 }
 
-// max / sum over the four lane groups that share a row (lanes l, l + 16, l + 32, l + 48)
+// max / sum over the four lane groups that share a row (lanes j, j + 16, j + 32, j + 48): the swaps
+// of both registers' halves leave the two halves of v in two registers
 __device__ __forceinline__ float groups_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
+  const v2u a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const v2u b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float groups_sum(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
+  const v2u a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const v2u b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// A workgroup takes 16 rows of one sequence and cache head (row = new token * R + query head
-// of the group) and one of `splits` parts of the keys they see; its four waves take 64-token
-// steps in turn, each with its own running maximum and sum, joined at the end in LDS.
-//
-// Lane l: j = l % 16, g = l / 16.  A step's tokens are 16-token groups g = 0 .. 3, each inside
-// one page (P % 16 == 0).
-//  * s^T = k q^T in four 16-token instructions t: the lane that supplies k row i takes token
-//    16 (i / 4) + 4 t + i % 4, so that the results, rows 4 g + r of column j, are tokens
-//    16 g + 4 t + r of row j: lane group g ends with the 16 consecutive tokens of its group.
-//  * o^T += v^T p^T: the lane supplies p of exactly those 16 tokens, from its own registers,
-//    and v of the same 16 tokens: 16 consecutive bytes of a value row.  No exchange of lanes.
-//  * the scales are one number for the lane's tokens: keys' multiplies s, values' multiplies p.
-template <int D, bool I8>
-__global__ __launch_bounds__(64 * kAttnWaves) void k_kv_attention(KvAttnArgs a) {
-  constexpr int ND = D / 16, NC = D / 64;
-  __shared__ float o_lds[kAttnWaves][kRowTile][D + 4];
-  __shared__ float m_lds[kAttnWaves][kRowTile], l_lds[kAttnWaves][kRowTile];
-  const KvArgs& c = a.c;
+// a value that every lane of the wave has, as one scalar
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+
+// One sequence as the rows of a cache head see it, in scalars.
+struct Seq {
+  int64_t row0;      // its first row
+  int64_t nrows;     // rows * R
+  int len;           // tokens (as given)
+  int rows;
+  uint32_t seen;     // tokens that the table can hold, >= 0
+  const int32_t* table;
+};
+__device__ __forceinline__ Seq seq_of(const KvAttnArgs& a, int b, int64_t row0, int64_t rows) {
+  Seq s;
+  b = uniform(b);
+  s.row0 = uniform64(row0);
+  s.rows = uniform((int)rows);
+  s.nrows = (int64_t)s.rows * a.R;
+  s.len = uniform(a.c.lens[b]);
+  s.seen = (uint32_t)min((int64_t)max(s.len, 0), (int64_t)a.c.max_pages * a.c.P);
+  s.table = a.c.table + b * a.c.table_stride;
+  return s;
+}
+// tokens 0 .. limit - 1 are what a row of new token i sees
+__device__ __forceinline__ uint32_t limit_of(const KvAttnArgs& a, const Seq& s, int i) {
+  return a.causal ? (uint32_t)min((int64_t)max((int64_t)s.len - s.rows + i + 1, (int64_t)0), (int64_t)s.seen) : s.seen;
+}
+// number / divisor by the divisor's rounded-up reciprocal (exact below 2^28 for divisors to 16)
+__device__ __forceinline__ uint32_t by_page(uint32_t group, uint32_t per, uint32_t recip) {
+  return per == 1 ? group : __umulhi(group, recip);
+}
+
+// slots of the lane's 16 that hold tokens: from the sequence's end on they hold anything
+__device__ __forceinline__ int there_slots(const Seq& s, bool there, uint32_t gt) {
+  return !there || gt >= s.seen ? 0 : (int)min(s.seen - gt, 16u);
+}
+__device__ __forceinline__ v4u keep_bytes(v4u v, int n) {  // the first n bytes, the others zero
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int keep = n - 4 * w;
+    v[w] = keep >= 4 ? v[w] : keep <= 0 ? 0u : v[w] & ((1u << (8 * keep)) - 1u);
+  }
+  return v;
+}
+
+// RT row tiles of a wave over steps [lo, hi) with stride TW, keys and values straight from memory
+// in operand order.  The values of a step load while its scores are made, the keys of the next one
+// during its softmax and products, page numbers two steps ahead.
+template <int D, bool I8, int RT>
+struct Rows {
+  static constexpr int ND = D / 16, NC = D / 64;
+  v8bf qf[RT][NC][2];
+  v4f o[RT][ND];
+  float mx[RT], sum[RT];  // running maximum (in log2 units) and this lane group's part of the sum
+  uint32_t limit[RT];
+
+  // r0: the first row; rows past the sequence's last repeat it (and are not stored)
+  __device__ __forceinline__ void begin(const KvAttnArgs& a, const Seq& s, int h, int64_t r0, int j, int g) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int rc = (int)min(r0 + 16 * rt + j, s.nrows - 1);
+      const int i = rc / a.R, head = h * a.R + rc % a.R;
+      limit[rt] = limit_of(a, s, i);
+      const uint16_t* q = a.q + (s.row0 + i) * a.ldq + (int64_t)head * D + 16 * g;
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          v4u w = *reinterpret_cast<const v4u*>(q + 64 * cc + 8 * m);
+          if (a.scale < 0.0f) w ^= 0x80008000u;  // the sign goes into q, so that scores scale by |scale|
+          qf[rt][cc][m] = __builtin_bit_cast(v8bf, w);
+        }
+      mx[rt] = -INFINITY;
+      sum[rt] = 0.0f;
+#pragma unroll
+      for (int i2 = 0; i2 < ND; ++i2) o[rt][i2] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  }
+
+  // scores of the lane's 16 tokens from gt on -> weights, the running maximum and sum
+  template <bool MASK>
+  __device__ __forceinline__ void weights(v4f (&sc)[RT][4], v8bf (&pf)[RT][2], float ks, float vs, bool there, uint32_t gt) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (MASK) sc[rt][t][r] = there && gt + 4 * t + r < limit[rt] ? sc[rt][t][r] * ks : -INFINITY;
+          top = fmaxf(top, sc[rt][t][r]);
+        }
+      if constexpr (!MASK) top *= ks;
+      top = groups_max(top);
+      if (__any(top > mx[rt])) {
+        const float mn = fmaxf(mx[rt], top);
+        const float alpha = __builtin_amdgcn_exp2f(mx[rt] - (mn == -INFINITY ? 0.0f : mn));
+        mx[rt] = mn;
+        sum[rt] *= alpha;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) o[rt][i] *= alpha;
+      }
+      const float base = mx[rt] == -INFINITY ? 0.0f : mx[rt];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float e = __builtin_amdgcn_exp2f(MASK ? sc[rt][t][r] - base : __builtin_fmaf(sc[rt][t][r], ks, -base));
+          sum[rt] += e;
+          // rounded to bf16, with an int8 page's scale on it (a power of two: no further
+          // rounding); a masked token's weight is zero whatever its page's scale holds
+          float w = e;
+          if constexpr (MASK) w = sc[rt][t][r] == -INFINITY ? 0.0f : e * vs;
+          else if constexpr (I8) w = e * vs;
+          pf[rt][t >> 1][(t & 1) * 4 + r] = (__bf16)w;
+        }
+    }
+  }
+
+  __device__ __forceinline__ void run(const KvAttnArgs& a, const Seq& s, int h, uint32_t lo, uint32_t hi, uint32_t TW, int j,
+                                      int g) {
+    if (lo >= hi) return;
+    const KvArgs& c = a.c;
+    const uint32_t per = (uint32_t)c.P >> 4, recip = c.page_recip, H = (uint32_t)c.H;
+    const float to_log2 = fabsf(a.scale) * 1.44269504088896340736f;
+    const uint32_t page_bytes = (uint32_t)c.P * D;
+    const uint8_t* K = static_cast<const uint8_t*>(c.k) + (uint32_t)h * page_bytes;
+    const uint8_t* V = static_cast<const uint8_t*>(c.v) + (uint32_t)h * page_bytes;
+    const int64_t page_step = (int64_t)H * page_bytes;
+    const int kg = j >> 2;  // the token group that this lane reads keys of
+    uint32_t first = limit[0];  // the least limit of the wave's rows: the first row's
+    first = __builtin_amdgcn_readfirstlane((int)first);
+    struct Page {
+      uint32_t at, slot;
+      bool there;
+    };
+    auto number = [&](uint32_t step, uint32_t grp) -> int {  // the table's entry
+      const uint32_t tg = 4 * step + grp;
+      return 16 * tg < s.seen ? s.table[by_page(tg, per, recip)] : -1;
+    };
+    // a group past the end, or a page number that is none, reads page 0 and is masked
+    auto place = [&](uint32_t step, uint32_t grp, int page) -> Page {
+      const uint32_t tg = 4 * step + grp;
+      const bool there = (uint32_t)page < (uint32_t)c.pages;
+      return Page{there ? (uint32_t)page : 0u, (tg - by_page(tg, per, recip) * per) * 16, there};
+    };
+    v4u kk[4][NC];
+    auto load_k = [&](const Page& p) {
+      const uint8_t* kp = K + p.at * page_step + (p.slot + (j & 3)) * D + 16 * g;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) kk[t][cc] = *reinterpret_cast<const v4u*>(kp + 4 * t * D + 64 * cc);
+    };
+    Page pv = place(lo, g, number(lo, g));
+    load_k(place(lo, kg, number(lo, kg)));
+    uint32_t kb = c.k_scale[(int64_t)pv.at * H + h];
+    uint32_t nstep = min(lo + TW, hi - 1);  // the last step's "next" is a repeat, loaded and not used
+    int nk = number(nstep, kg), nv = number(nstep, g);
+    for (uint32_t step = lo; step < hi; step += TW) {
+      const uint32_t tok0 = step * kTokTile, gt = tok0 + 16 * g;
+      const uint8_t* vp = V + pv.at * page_step + (uint32_t)j * c.P + pv.slot;
+      const uint32_t vb = c.v_scale[(int64_t)pv.at * H + h];
+      v4u vv[ND];
+#pragma unroll
+      for (int i = 0; i < ND; ++i) vv[i] = *reinterpret_cast<const v4u*>(vp + 16 * i * c.P);
+      // ---- scores
+      v4f sc[RT][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) sc[rt][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const v8bf kf = widen8<I8>(kk[t][cc][2 * m], kk[t][cc][2 * m + 1], 1.0f);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) sc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[rt][cc][m], sc[rt][t], 0, 0, 0);
+          }
+      }
+      const float ks = scale_of(kb) * to_log2;
+      // ---- the next step's keys
+      const Page npv = place(nstep, g, nv);
+      load_k(place(nstep, kg, nk));
+      kb = c.k_scale[(int64_t)npv.at * H + h];
+      nstep = min(nstep + TW, hi - 1);
+      nk = number(nstep, kg);
+      nv = number(nstep, g);
+      // ---- weights and values
+      const float vs = scale_of(vb);
+      auto finish = [&](auto masked) __attribute__((always_inline)) {
+        constexpr bool MASK = decltype(masked)::value;
+        v8bf pf[RT][2];
+        this->template weights<MASK>(sc, pf, ks, vs, pv.there, gt);
+#pragma unroll
+        for (int i = 0; i < ND; ++i) {
+          if constexpr (MASK) vv[i] = keep_bytes(vv[i], there_slots(s, pv.there, gt));
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const v8bf vf = widen8<I8>(vv[i][2 * m], vv[i][2 * m + 1], MASK ? 1.0f : vs);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) o[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][m], o[rt][i], 0, 0, 0);
+          }
+        }
+      };
+      // every token of the step is there for every row, and its values' scales are numbers
+      if (tok0 + kTokTile <= first && __all(pv.there && vb != 255u)) finish(std::false_type{});
+      else finish(std::true_type{});
+      pv = npv;
+    }
+  }
+};
+
+// The same for the four waves of a workgroup, 64 RT rows that read the same keys: a step's keys
+// (64 token rows of D bytes) and values (D rows of 64 tokens) go global -> LDS by DMA, S - 1 steps
+// ahead in a ring, each byte read once by the workgroup.  Chunks of 16 bytes are XORed so that the
+// sixteen rows that are read at one chunk meet sixteen different bank groups: a key read takes
+// tokens 16 a + 4 t + b (a, b = 0 .. 3), a value read sixteen consecutive rows of 64 bytes.
+// Wave w sends the keys of token group w, and of the values every fourth run of 16 rows; page
+// numbers are read through the scalar cache, so that no vector load but the DMA is in flight and
+// its count tells when a step has landed.
+template <int D, bool I8, int RT, int S>
+struct SharedRows {
+  using R = Rows<D, I8, RT>;
+  static constexpr int ND = D / 16, NC = D / 64;
+  static constexpr int kTile = 64 * D, kStage = 2 * kTile + 256;  // keys, values, scale bytes (a word each)
+  static constexpr int kDma = 2 * NC + 1;
+  static constexpr int kBytes = S * kStage;
+  static __device__ __forceinline__ int k_swz(int token) {
+    return NC == 1 ? (token >> 4) & 3 : NC == 2 ? ((token >> 4) & 3) * 2 + ((token >> 1) & 1) : ((token >> 4) & 3) * 4 + (token & 3);
+  }
+  static __device__ __forceinline__ int v_swz(int d) { return (d >> 2) & 3; }
+
+  // every wave of the workgroup calls this with the same lo, hi; a wave whose rows see only steps
+  // below `most` skips the others' arithmetic
+  static __device__ __forceinline__ void run(R& w, const KvAttnArgs& a, const Seq& s, int h, uint32_t lo, uint32_t hi,
+                                             uint32_t most, uint8_t* smem, int wv, int lane) {
+    if (lo >= hi) return;
+    const KvArgs& c = a.c;
+    const int j = lane & 15, g = lane >> 4;
+    const uint32_t per = (uint32_t)c.P >> 4, recip = c.page_recip, H = (uint32_t)c.H;
+    const float to_log2 = fabsf(a.scale) * 1.44269504088896340736f;
+    const uint32_t page_bytes = (uint32_t)c.P * D;
+    const uint8_t* K = static_cast<const uint8_t*>(c.k) + (uint32_t)h * page_bytes;
+    const uint8_t* V = static_cast<const uint8_t*>(c.v) + (uint32_t)h * page_bytes;
+    const int64_t page_step = (int64_t)H * page_bytes;
+    const uint32_t first = __builtin_amdgcn_readfirstlane((int)w.limit[0]);
+    const auto* table = (const __attribute__((address_space(4))) int32_t*)s.table;
+    // page of token group lane % 4 of a step, -1 where there is none
+    auto page_of = [&](uint32_t tg) __attribute__((always_inline)) -> int {
+      const bool in = 16 * tg < s.seen;
+      const int n = uniform(table[in ? by_page(tg, per, recip) : 0u]);
+      return in && (uint32_t)n < (uint32_t)c.pages ? n : -1;
+    };
+    auto pages_of = [&](uint32_t step) __attribute__((always_inline)) -> int {
+      const int p0 = page_of(4 * step), p1 = page_of(4 * step + 1), p2 = page_of(4 * step + 2), p3 = page_of(4 * step + 3);
+      const int lo2 = lane & 1 ? p1 : p0, hi2 = lane & 1 ? p3 : p2;
+      return lane & 2 ? hi2 : lo2;
+    };
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_u8)smem;
+    // this lane's places: keys, position wv * NC * 64 + lane of the tile is (token, chunk); values,
+    // row wv * 16 + lane / 4 (then 64 rows on), chunk lane % 4
+    const int vg = (lane & 3) ^ ((lane >> 4) & 3);  // the token group of the lane's value chunk
+    auto issue = [&](uint32_t step, int page, int stage) __attribute__((always_inline)) {
+      const uint32_t st = lds0 + stage * kStage;
+      auto slot_of = [&](uint32_t x) {
+        const uint32_t tg = 4 * step + x;
+        return (tg - by_page(tg, per, recip) * per) * 16;
+      };
+      const int held = max(page, 0);  // a group without a page reads page 0 and is masked
+      const uint8_t* kb = K + __builtin_amdgcn_readlane(held, wv) * page_step + slot_of(wv) * D;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int pos = (wv * NC + i) * 64 + lane, tok = pos / (D / 16), ch = (pos % (D / 16)) ^ k_swz(tok);
+        dma16_at(kb + ((tok & 15) * D + ch * 16), st + (wv * NC + i) * 1024);
+      }
+      // the page of token group (lane % 4) ^ (lane / 16): the quads of row r of 16 lanes swapped by r
+      int vp = held;
+      vp = __builtin_amdgcn_update_dpp(vp, held, 0xB1, 0x2, 0xF, false);
+      vp = __builtin_amdgcn_update_dpp(vp, held, 0x4E, 0x4, 0xF, false);
+      vp = __builtin_amdgcn_update_dpp(vp, held, 0x1B, 0x8, 0xF, false);
+      const uint8_t* vb = V + vp * page_step + (uint32_t)(wv * 16 + (lane >> 2)) * c.P + slot_of(vg);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) dma16_at(vb + (int64_t)(64 * i) * c.P, st + kTile + (wv + 4 * i) * 1024);
+      // scale bytes: word x of the stage's last 256 bytes is the keys' of token group x, word 4 + x
+      // the values' (each wave writes the same)
+      dma1_at((lane & 4 ? c.v_scale : c.k_scale) + (int64_t)held * H + h, st + 2 * kTile);
+    };
+    static_assert(S == 2 || S == 3, "page numbers of three steps");
+    int p0 = pages_of(lo), p1 = pages_of(min(lo + 1, hi - 1)), p2 = S == 3 ? pages_of(min(lo + 2, hi - 1)) : 0;
+    issue(lo, p0, 0);
+    if (S == 3 && lo + 1 < hi) issue(lo + 1, p1, 1);
+    int stage = 0;
+    for (uint32_t step = lo; step < hi; ++step) {
+      if (S > 2 && step + S - 2 < hi) wait_vm<kDma*(S - 2)>();
+      else wait_vm<0>();
+      lds_barrier();  // the step has landed for all, and the one before it has been read by all
+      if (step + S - 1 < hi) issue(step + S - 1, S == 3 ? p2 : p1, stage == 0 ? S - 1 : stage - 1);
+      const uint32_t none = (uint32_t)__ballot(p0 < 0) & 15u;
+      p0 = p1;
+      if (S == 3) p1 = p2;
+      (S == 3 ? p2 : p1) = pages_of(min(step + S, hi - 1));
+      const uint8_t* sk = smem + stage * kStage;
+      const uint8_t* sv = sk + kTile;
+      const uint32_t* sb = reinterpret_cast<const uint32_t*>(sv + kTile);
+      stage = stage + 1 == S ? 0 : stage + 1;
+      if (step >= most) continue;  // uniform in the wave
+      // operands are read one ahead of their use; the barriers keep the compiler from reading many
+      // ahead, for which there are no registers
+      v4f sc[RT][4];
+      auto key = [&](int x) __attribute__((always_inline)) {
+        const int tok = 16 * (j >> 2) + 4 * (x / NC) + (j & 3), ch = 4 * (x % NC) + g;
+        return *reinterpret_cast<const v4u*>(sk + tok * D + ((ch ^ k_swz(tok)) << 4));
+      };
+      v4u kk = key(0);
+#pragma unroll
+      for (int x = 0; x < 4 * NC; ++x) {
+        const int t = x / NC, cc = x % NC;
+        const v4u next = x + 1 < 4 * NC ? key(x + 1) : kk;
+        if (cc == 0)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) sc[rt][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const v8bf kf = widen8<I8>(kk[2 * m], kk[2 * m + 1], 1.0f);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) sc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, w.qf[rt][cc][m], sc[rt][t], 0, 0, 0);
+        }
+        kk = next;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const uint32_t vbyte = sb[4 + g];
+      const float ks = scale_of(sb[g]) * to_log2, vs = scale_of(vbyte);
+      const uint32_t tok0 = step * kTokTile, gt = tok0 + 16 * g;
+      const bool there = !(none >> g & 1u);
+      auto finish = [&](auto masked) __attribute__((always_inline)) {
+        constexpr bool MASK = decltype(masked)::value;
+        v8bf pf[RT][2];
+        auto value = [&](int i) __attribute__((always_inline)) {
+          return *reinterpret_cast<const v4u*>(sv + (16 * i + j) * 64 + ((g ^ v_swz(j)) << 4));
+        };
+        v4u vv = value(0);
+        w.template weights<MASK>(sc, pf, ks, vs, there, gt);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < ND; ++i) {
+          const v4u next = i + 1 < ND ? value(i + 1) : vv;
+          if constexpr (MASK) vv = keep_bytes(vv, there_slots(s, there, gt));
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const v8bf vf = widen8<I8>(vv[2 * m], vv[2 * m + 1], MASK ? 1.0f : vs);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) w.o[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][m], w.o[rt][i], 0, 0, 0);
+          }
+          vv = next;
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      if (tok0 + kTokTile <= first && none == 0 && __all(vbyte != 255u)) finish(std::false_type{});
+      else finish(std::true_type{});
+    }
+    lds_barrier();  // the ring may be filled again
+  }
+};
+
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
+}
+
+// A wave's own rows, whole: lane (j, g) holds of row j the elements 16 i + 4 g .. + 3
+template <int D, bool I8, int RT>
+__device__ __forceinline__ void store_rows(const KvAttnArgs& a, const Seq& s, Rows<D, I8, RT>& w, int h, int64_t r0, int j,
+                                           int g) {
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const float l = groups_sum(w.sum[rt]);
+    const int64_t rr = r0 + 16 * rt + j;
+    if (rr >= s.nrows) continue;
+    const int i = (int)rr / a.R, head = h * a.R + (int)rr % a.R;
+    const float inv = w.mx[rt] == -INFINITY ? 0.0f : 1.0f / l;
+    uint16_t* out = a.out + (s.row0 + i) * a.ldo + (int64_t)head * D + 4 * g;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      const v4f v = w.o[rt][d] * inv;
+      *reinterpret_cast<v2u*>(out + 16 * d) = v2u{f32_to_bf16_nan(v[0]) | f32_to_bf16_nan(v[1]) << 16,
+                                                  f32_to_bf16_nan(v[2]) | f32_to_bf16_nan(v[3]) << 16};
+    }
+    if (a.lse && g == 0) a.lse[(s.row0 + i) * (int64_t)(a.c.H * a.R) + head] = log_sum(w.mx[rt], l);
+  }
+}
+
+// Many rows: a workgroup takes 64 RT rows of one sequence and cache head over all their keys.  A
+// sequence's last rows, which see most, come first.
+template <int D, bool I8, int RT, int S>
+__global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_rows(KvAttnArgs a) {
+  using W = SharedRows<D, I8, RT, S>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int h = blockIdx.y, split = blockIdx.z, R = a.R;
-  const SeqSlot s = find_slot(c, blockIdx.x, R, kRowTile, 1);
-  const int64_t r0 = s.j * kRowTile, nrows = s.rows * R;
-  if (r0 >= nrows) return;
-  const int64_t len = c.lens[s.b];
-  const int64_t seen = min(max(len, (int64_t)0), (int64_t)c.max_pages * c.P);  // tokens that the table can hold
-  // rows behind the last read the last and see no key
-  const int64_t rr = r0 + j, rc = min(rr, nrows - 1);
-  const int64_t tok = s.row0 + rc / R;
-  const int head = h * R + (int)(rc % R);
-  auto limit_of = [&](int64_t row) -> int64_t {
-    return a.causal ? min(max(len - s.rows + row / R + 1, (int64_t)0), seen) : seen;
+  constexpr int kRows = 16 * RT * kAttnWaves;
+  const int h = blockIdx.x % a.c.H;
+  const SeqSlot sl = find_slot(a.c, blockIdx.x / a.c.H, a.R, kRows, 1);
+  const Seq s = seq_of(a, sl.b, sl.row0, max(sl.rows, (int64_t)0));
+  const int64_t tiles = (s.nrows + kRows - 1) / kRows;
+  if (sl.j >= tiles) return;
+  const int64_t t0 = (tiles - 1 - sl.j) * kRows, r0 = t0 + wv * 16 * RT;
+  auto steps_to = [&](int64_t row) {
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)((limit_of(a, s, (int)(row / a.R)) + kTokTile - 1) / kTokTile));
   };
-  const int64_t limit = rr < nrows ? limit_of(rc) : 0;
-  const int64_t last = limit_of(min(r0 + kRowTile, nrows) - 1);   // the tile's longest row
-  const int64_t steps = (last + kTokTile - 1) / kTokTile;
-  const int64_t t_lo = steps * split / a.splits, t_hi = steps * (split + 1) / a.splits;
+  Rows<D, I8, RT> w;
+  w.begin(a, s, h, r0, j, g);
+  W::run(w, a, s, h, 0, steps_to(min(t0 + kRows, s.nrows) - 1),
+         r0 < s.nrows ? steps_to(min(r0 + 16 * RT, s.nrows) - 1) : 0, smem, wv, lane);
+  store_rows(a, s, w, h, r0, j, g);
+}
 
-  v8bf qf[NC][2];
-  {
-    const uint16_t* q = a.q + tok * a.ldq + (int64_t)head * D + 16 * g;
-#pragma unroll
-    for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-      for (int m = 0; m < 2; ++m) qf[cc][m] = *reinterpret_cast<const v8bf*>(q + 64 * cc + 8 * m);
-  }
-  const float to_log2 = a.scale * 1.44269504088896340736f;
-  const int32_t* table = c.table + s.b * c.table_stride;
-  const int64_t page_bytes = (int64_t)c.P * D;
-  float mx = -INFINITY, sum = 0.0f;
-  v4f o[ND];
-#pragma unroll
-  for (int i = 0; i < ND; ++i) o[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-
-  for (int64_t step = t_lo + wv; step < t_hi; step += kAttnWaves) {
-    const int64_t tok0 = step * kTokTile;
-    // this lane group's page; a token group past the end, or a page number outside the cache,
-    // reads page 0 and is masked
-    const int64_t gt = tok0 + 16 * g;
-    int page = gt < seen ? table[gt / c.P] : -1;
-    const bool there = page >= 0 && page < c.pages;
-    page = there ? page : 0;
-    const int slot = (int)(gt % c.P);
-    const int64_t base = ((int64_t)page * c.H + h) * page_bytes;
-    const int64_t kv_at = (int64_t)page * c.H + h;
-    const float ks = scale_of(c.k_scale[kv_at]) * to_log2;
-    const float vs = scale_of(c.v_scale[kv_at]);
-    // the page and slot of the token group that this lane reads keys of
-    const int kg = j >> 2;
-    const int64_t kbase = ((int64_t)__shfl(page, kg * 16, 64) * c.H + h) * page_bytes;
-    const int kslot = (int)((tok0 + 16 * kg) % c.P) + (j & 3);
-    const uint8_t* kp = static_cast<const uint8_t*>(c.k) + kbase + (int64_t)kslot * D + 16 * g;
-    v4f sc[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      sc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int cc = 0; cc < NC; ++cc) {
-        const v4u kk = *reinterpret_cast<const v4u*>(kp + 4 * t * D + 64 * cc);
-        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<I8>(kk[0], kk[1]), qf[cc][0], sc[t], 0, 0, 0);
-        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<I8>(kk[2], kk[3]), qf[cc][1], sc[t], 0, 0, 0);
-      }
+// Few rows: the work, tokens' steps of all (sequence, head, row tile) items in a row, is cut into
+// equal runs, one for each workgroup, whatever the lengths.  An item that lies in one run is stored;
+// of one that is cut the parts go to the workspace, and k_kv_join adds them.
+struct Plan {
+  int64_t units;  // steps in all
+  int runs;       // workgroups that take some
+};
+// Sums of the sequences' work in LDS: pre[b] = row tiles * steps of the sequences before b (for one
+// head).  Every thread of 256 takes part.
+template <int kRows>
+__device__ __forceinline__ Plan make_plan(const KvAttnArgs& a, int64_t* pre, int64_t* carry) {
+  const KvArgs& c = a.c;
+  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < c.B; b0 += 256) {
+    const int b = b0 + t;
+    int64_t v = 0;
+    if (b < c.B) {
+      const int64_t rows = max(seq_offset(c, b + 1) - seq_offset(c, b), (int64_t)0);
+      const int64_t seen = min((int64_t)max(c.lens[b], 0), (int64_t)c.max_pages * c.P);
+      // a sequence without tokens still has rows to store: one step
+      v = (rows * a.R + kRows - 1) / kRows * max((seen + kTokTile - 1) / kTokTile, (int64_t)1);
     }
-    // scores in units of log2, masked
-    float top = -INFINITY;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float v = sc[t][r] * ks;
-        sc[t][r] = there && gt + 4 * t + r < limit ? v : -INFINITY;
-        top = fmaxf(top, sc[t][r]);
-      }
-    top = groups_max(top);
-    const float mn = fmaxf(mx, top);
-    const float base_m = mn == -INFINITY ? 0.0f : mn;
-    const float alpha = __builtin_amdgcn_exp2f(mx - base_m);
-    mx = mn;
-    float part = 0.0f;
-    v8bf pf[2];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float e = __builtin_amdgcn_exp2f(sc[t][r] - base_m);
-        part += e;
-        // rounded to bf16 with the values' scale on it (a power of two: no further rounding);
-        // a masked token's weight is zero whatever its page's scale holds
-        pf[t >> 1][(t & 1) * 4 + r] = (__bf16)(sc[t][r] == -INFINITY ? 0.0f : e * vs);
-      }
-    sum = sum * alpha + part;
-    const uint8_t* vp = static_cast<const uint8_t*>(c.v) + base + (int64_t)j * c.P + slot;
-    const int64_t rest = seen - gt;  // the group's slots from `rest` on hold anything: read as zero
-    const int valid = !there || rest <= 0 ? 0 : rest >= 16 ? 16 : (int)rest;
-#pragma unroll
-    for (int i = 0; i < ND; ++i) {
-      v4u vv = *reinterpret_cast<const v4u*>(vp + (int64_t)16 * i * c.P);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int keep = valid - 4 * w;
-        vv[w] = keep >= 4 ? vv[w] : keep <= 0 ? 0u : vv[w] & ((1u << (8 * keep)) - 1u);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) o[i][r] *= alpha;
-      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<I8>(vv[0], vv[1]), pf[0], o[i], 0, 0, 0);
-      o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<I8>(vv[2], vv[3]), pf[1], o[i], 0, 0, 0);
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t u = __shfl_up(v, o, 64);
+      if (lane >= o) v += u;
     }
+    if (lane == 63) carry[wv] = v;
+    __syncthreads();
+    int64_t base = before;
+    for (int w = 0; w < wv; ++w) base += carry[w];
+    if (b < c.B) pre[b + 1] = base + v;
+    before += carry[0] + carry[1] + carry[2] + carry[3];
+    __syncthreads();
   }
-  sum = groups_sum(sum);
-#pragma unroll
-  for (int i = 0; i < ND; ++i) *reinterpret_cast<v4f*>(&o_lds[wv][j][16 * i + 4 * g]) = o[i];
-  if (g == 0) {
-    m_lds[wv][j] = mx;
-    l_lds[wv][j] = sum;
-  }
+  if (t == 0) pre[0] = 0;
   __syncthreads();
-  // join the waves: thread -> (row, 16-th of D)
-  const int row = threadIdx.x >> 4, dq = (threadIdx.x & 15) * (D / 16);
-  if (r0 + row >= nrows) return;
-  float M = m_lds[0][row];
-#pragma unroll
-  for (int w = 1; w < kAttnWaves; ++w) M = fmaxf(M, m_lds[w][row]);
-  const float Mb = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f, wgt[kAttnWaves];
-#pragma unroll
-  for (int w = 0; w < kAttnWaves; ++w) {
-    wgt[w] = __builtin_amdgcn_exp2f(m_lds[w][row] - Mb);
-    L += wgt[w] * l_lds[w][row];
+  Plan p;
+  p.units = before * c.H;
+  // a run is worth a step for each wave
+  p.runs = (int)min((int64_t)a.runs, (p.units + a.least - 1) / a.least);
+  return p;
+}
+// run w takes units [start(w), start(w + 1))
+__device__ __forceinline__ int64_t run_start(const Plan& p, int w) { return p.units * w / p.runs; }
+struct Item {
+  int b, h, tile;
+  uint32_t steps, step;  // of the item; the unit's step in it
+};
+__device__ __forceinline__ Item item_of(const KvAttnArgs& a, const int64_t* pre, int64_t u, int krows) {
+  const KvArgs& c = a.c;
+  int lo = 0, hi = c.B - 1;
+  while (lo < hi) {  // the last sequence that begins at or before u (of equal ones the one with work)
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] * c.H <= u) lo = mid;
+    else hi = mid - 1;
   }
-  float acc[D / 16];
+  Item it;
+  lo = uniform(lo);
+  it.b = lo;
+  const int64_t seen = min((int64_t)max(c.lens[lo], 0), (int64_t)c.max_pages * c.P);
+  it.steps = (uint32_t)uniform((int)max((seen + kTokTile - 1) / kTokTile, (int64_t)1));
+  const int64_t in = u - pre[lo] * c.H;
+  const int64_t item = in / it.steps;
+  it.step = (uint32_t)uniform((int)(in - item * it.steps));
+  const int tiles = (int)((pre[lo + 1] - pre[lo]) / it.steps);
+  it.h = uniform((int)(item / tiles));
+  it.tile = uniform((int)(item % tiles));
+  return it;
+}
+
+// What both kinds of run do with an item: its sequence and rows, and where its part goes
+struct Run {
+  Item it;
+  uint32_t n;    // steps of it
+  bool whole;
+  int64_t slot;  // first row of its part in the workspace
+};
+__device__ __forceinline__ Run next_run(const KvAttnArgs& a, const int64_t* pre, int64_t u, int64_t end, int part, int krows) {
+  Run r;
+  r.it = item_of(a, pre, u, krows);
+  r.n = (uint32_t)uniform((int)min((int64_t)(r.it.steps - r.it.step), end - u));
+  r.whole = r.n == r.it.steps;
+  r.slot = ((int64_t)blockIdx.x * 2 + part) * krows;
+  return r;
+}
+
+// 64-row tiles, each wave 16 rows of its own, keys shared through LDS
+template <int D, bool I8, int S>
+__global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs64(KvAttnArgs a) {
+  using W = SharedRows<D, I8, 1, S>;
+  constexpr int kRows = 64;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ int64_t pre[kPlanSeqs + 1], carry[4];
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const Plan plan = make_plan<kRows>(a, pre, carry);
+  if ((int)blockIdx.x >= plan.runs) return;
+  int64_t u = run_start(plan, blockIdx.x);
+  const int64_t end = run_start(plan, blockIdx.x + 1);
+  for (int part = 0; u < end; part = 1) {
+    const Run r = next_run(a, pre, u, end, part, kRows);
+    u += r.n;
+    const int64_t row0 = seq_offset(a.c, r.it.b);
+    const Seq s = seq_of(a, r.it.b, row0, seq_offset(a.c, r.it.b + 1) - row0);
+    const int64_t t0 = (int64_t)r.it.tile * kRows, r0 = t0 + wv * 16;
+    auto steps_to = [&](int64_t row) {
+      return (uint32_t)__builtin_amdgcn_readfirstlane((int)((limit_of(a, s, (int)(row / a.R)) + kTokTile - 1) / kTokTile));
+    };
+    Rows<D, I8, 1> w;
+    w.begin(a, s, r.it.h, r0, j, g);
+    W::run(w, a, s, r.it.h, r.it.step, min(r.it.step + r.n, steps_to(min(t0 + kRows, s.nrows) - 1)),
+           r0 < s.nrows ? steps_to(min(r0 + 16, s.nrows) - 1) : 0, smem, wv, lane);
+    if (r.whole) {
+      store_rows(a, s, w, r.it.h, r0, j, g);
+    } else {
+      const float l = groups_sum(w.sum[0]);
+      float* to = a.part + (r.slot + wv * 16 + j) * D + 4 * g;
 #pragma unroll
-  for (int d = 0; d < D / 16; ++d) {
-    acc[d] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) acc[d] += wgt[w] * o_lds[w][row][dq + d];
-  }
-  const int64_t orow = r0 + row;
-  if (a.splits == 1) {
-    const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
-    uint16_t* out = a.out + (s.row0 + orow / R) * a.ldo + (int64_t)(h * R + orow % R) * D + dq;
-#pragma unroll
-    for (int d = 0; d < D / 16; ++d) out[d] = (uint16_t)f32_to_bf16_nan(acc[d] * inv);
-    if (a.lse && dq == 0)
-      a.lse[(s.row0 + orow / R) * (int64_t)(c.H * R) + h * R + orow % R] =
-          M == -INFINITY ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994530942f;
-  } else {
-    const int64_t at = (((int64_t)blockIdx.x * c.H + h) * a.splits + split) * kRowTile + row;
-    float* part = a.part + at * D + dq;
-#pragma unroll
-    for (int d = 0; d < D / 16; ++d) part[d] = acc[d];
-    if (dq == 0) a.stat[at] = float2{M, L};
+      for (int i = 0; i < D / 16; ++i) *reinterpret_cast<v4f*>(to + 16 * i) = w.o[0][i];
+      if (g == 0) a.stat[r.slot + wv * 16 + j] = float2{w.mx[0], l};
+    }
   }
 }
 
-// The parts of one row tile, joined in order: one workgroup for each (row tile, cache head).
+// 16-row tiles: the waves share the rows and take steps in turn, and are joined in LDS
+template <int D, bool I8>
+__global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void k_kv_attention_runs16(KvAttnArgs a) {
+  constexpr int kRows = 16;
+  __shared__ float o_lds[kAttnWaves][kRows][D + 4];
+  __shared__ float m_lds[kAttnWaves][kRows], l_lds[kAttnWaves][kRows];
+  __shared__ int64_t pre[kPlanSeqs + 1], carry[4];
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const Plan plan = make_plan<kRows>(a, pre, carry);
+  if ((int)blockIdx.x >= plan.runs) return;
+  int64_t u = run_start(plan, blockIdx.x);
+  const int64_t end = run_start(plan, blockIdx.x + 1);
+  for (int part = 0; u < end; part = 1) {
+    const Run r = next_run(a, pre, u, end, part, kRows);
+    u += r.n;
+    const int64_t row0 = seq_offset(a.c, r.it.b);
+    const Seq s = seq_of(a, r.it.b, row0, seq_offset(a.c, r.it.b + 1) - row0);
+    const int64_t r0 = (int64_t)r.it.tile * kRows;
+    const uint32_t most = __builtin_amdgcn_readfirstlane(
+        (int)((limit_of(a, s, (int)((min(r0 + kRows, s.nrows) - 1) / a.R)) + kTokTile - 1) / kTokTile));
+    Rows<D, I8, 1> w;
+    w.begin(a, s, r.it.h, r0, j, g);
+    w.run(a, s, r.it.h, r.it.step + wv, min(r.it.step + r.n, most), kAttnWaves, j, g);
+    const float l = groups_sum(w.sum[0]);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) *reinterpret_cast<v4f*>(&o_lds[wv][j][16 * i + 4 * g]) = w.o[0][i];
+    if (g == 0) {
+      m_lds[wv][j] = w.mx[0];
+      l_lds[wv][j] = l;
+    }
+    __syncthreads();
+    // join the waves: 16 threads a row, four elements at a time
+    const int row = threadIdx.x >> 4, q4 = (threadIdx.x & 15) * 4;
+    const int64_t rr = r0 + row;
+    if (rr < s.nrows) {
+      float M = m_lds[0][row];
+#pragma unroll
+      for (int x = 1; x < kAttnWaves; ++x) M = fmaxf(M, m_lds[x][row]);
+      const float Mb = M == -INFINITY ? 0.0f : M;
+      float L = 0.0f, wgt[kAttnWaves];
+#pragma unroll
+      for (int x = 0; x < kAttnWaves; ++x) {
+        wgt[x] = __builtin_amdgcn_exp2f(m_lds[x][row] - Mb);
+        L += wgt[x] * l_lds[x][row];
+      }
+      const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
+      const int i = (int)rr / a.R, head = r.it.h * a.R + (int)rr % a.R;
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d) {
+        v4f v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int x = 0; x < kAttnWaves; ++x) v += wgt[x] * *reinterpret_cast<const v4f*>(&o_lds[x][row][64 * d + q4]);
+        if (r.whole) {
+          v *= inv;
+          *reinterpret_cast<v2u*>(a.out + (s.row0 + i) * a.ldo + (int64_t)head * D + 64 * d + q4) =
+              v2u{f32_to_bf16_nan(v[0]) | f32_to_bf16_nan(v[1]) << 16, f32_to_bf16_nan(v[2]) | f32_to_bf16_nan(v[3]) << 16};
+        } else {
+          *reinterpret_cast<v4f*>(a.part + (r.slot + row) * D + 64 * d + q4) = v;
+        }
+      }
+      if (q4 == 0) {
+        if (!r.whole) a.stat[r.slot + row] = float2{M, L};
+        else if (a.lse) a.lse[(s.row0 + i) * (int64_t)(a.c.H * a.R) + head] = log_sum(M, L);
+      }
+    }
+    __syncthreads();  // the next item's waves write where this one's were read
+  }
+}
+
+// The items that runs cut, joined part by part in order.  Run w > 0 that begins inside an item,
+// the first to do so, stands for it; one workgroup for each (run, row of the tile): the threads'
+// quarters take every fourth part, and are added in order.
 template <int D>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
+  __shared__ int64_t pre[kPlanSeqs + 1], carry[4];
+  __shared__ float o_lds[4][D], m_lds[4], l_lds[4];
+  const int krows = a.tile_rows, row = blockIdx.y;
+  const Plan plan = krows == 16 ? make_plan<16>(a, pre, carry) : make_plan<64>(a, pre, carry);
+  const int run = blockIdx.x + 1;
+  if (run >= plan.runs) return;
+  const int64_t u = run_start(plan, run);
+  const Item it = item_of(a, pre, u, krows);
+  const int64_t i0 = u - it.step, i1 = i0 + it.steps;
+  if (it.step == 0 || run_start(plan, run - 1) > i0) return;
   const KvArgs& c = a.c;
-  const int h = blockIdx.y, R = a.R;
-  const SeqSlot s = find_slot(c, blockIdx.x, R, kRowTile, 1);
-  const int64_t r0 = s.j * kRowTile, nrows = s.rows * R;
-  const int row = threadIdx.x >> 4, dq = (threadIdx.x & 15) * (D / 16);
-  if (r0 + row >= nrows) return;
-  const int64_t at = ((int64_t)blockIdx.x * c.H + h) * a.splits * kRowTile + row;
-  float M = -INFINITY;
-  for (int i = 0; i < a.splits; ++i) M = fmaxf(M, a.stat[at + (int64_t)i * kRowTile].x);
-  const float Mb = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f, acc[D / 16];
-#pragma unroll
-  for (int d = 0; d < D / 16; ++d) acc[d] = 0.0f;
-  for (int i = 0; i < a.splits; ++i) {
-    const float2 st = a.stat[at + (int64_t)i * kRowTile];
-    const float w = __builtin_amdgcn_exp2f(st.x - Mb);
-    L += w * st.y;
-    const float* part = a.part + (at + (int64_t)i * kRowTile) * D + dq;
-#pragma unroll
-    for (int d = 0; d < D / 16; ++d) acc[d] += w * part[d];
+  const int64_t row0 = seq_offset(c, it.b), nrows = (seq_offset(c, it.b + 1) - row0) * a.R;
+  const int64_t rr = (int64_t)it.tile * krows + row;
+  if (rr >= nrows) return;
+  // runs run - 1 .. last - 1 hold its parts: the first one's is its second if the item begins inside
+  int last = run;
+  {
+    int lo = run, hi = plan.runs - 1;  // the last run that begins before i1
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (run_start(plan, mid) < i1) lo = mid;
+      else hi = mid - 1;
+    }
+    last = lo + 1;
   }
-  const int64_t orow = r0 + row;
-  const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
-  uint16_t* out = a.out + (s.row0 + orow / R) * a.ldo + (int64_t)(h * R + orow % R) * D + dq;
+  const int first_slot = 2 * (run - 1) + (run_start(plan, run - 1) < i0 ? 1 : 0);
+  auto slot_of = [&](int p) -> int64_t { return (int64_t)(p == 0 ? first_slot : 2 * (run - 1 + p)) * krows + row; };
+  const int parts = last - run + 1, q = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  constexpr int E = D / 64;  // elements of a lane
+  float M = -INFINITY, L = 0.0f, acc[E];
 #pragma unroll
-  for (int d = 0; d < D / 16; ++d) out[d] = (uint16_t)f32_to_bf16_nan(acc[d] * inv);
-  if (a.lse && dq == 0)
-    a.lse[(s.row0 + orow / R) * (int64_t)(c.H * R) + h * R + orow % R] =
-        M == -INFINITY ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994530942f;
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+  for (int p = q; p < parts; p += 4) {
+    const float2 st = a.stat[slot_of(p)];
+    const float* from = a.part + slot_of(p) * D + lane * E;
+    const float mn = fmaxf(M, st.x), mb = mn == -INFINITY ? 0.0f : mn;
+    const float w0 = __builtin_amdgcn_exp2f(M - mb), w1 = __builtin_amdgcn_exp2f(st.x - mb);
+    M = mn;
+    L = L * w0 + st.y * w1;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * w0 + from[e] * w1;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) o_lds[q][lane * E + e] = acc[e];
+  if (lane == 0) {
+    m_lds[q] = M;
+    l_lds[q] = L;
+  }
+  __syncthreads();
+  M = fmaxf(fmaxf(m_lds[0], m_lds[1]), fmaxf(m_lds[2], m_lds[3]));
+  const float Mb = M == -INFINITY ? 0.0f : M;
+  L = 0.0f;
+  float wgt[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    wgt[x] = __builtin_amdgcn_exp2f(m_lds[x] - Mb);
+    L += wgt[x] * l_lds[x];
+  }
+  const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
+  const int i = (int)rr / a.R, head = it.h * a.R + (int)rr % a.R;
+  uint16_t* out = a.out + (row0 + i) * a.ldo + (int64_t)head * D;
+  for (int d = threadIdx.x; d < D; d += 256) {
+    float v = 0.0f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v += wgt[x] * o_lds[x][d];
+    out[d] = (uint16_t)f32_to_bf16_nan(v * inv);
+  }
+  if (a.lse && threadIdx.x == 0) a.lse[(row0 + i) * (int64_t)(c.H * a.R) + head] = log_sum(M, L);
 }
 
 }  // namespace
@@ -400,40 +903,94 @@ hipError_t launch_kv_append(const KvArgs& c, bool i8, const uint16_t* k_new, int
 
 bool kv_head_dim_ok(int64_t D) { return D == 64 || D == 128 || D == 256; }
 
-template <int D>
-static hipError_t attention_of(const KvAttnArgs& a, bool i8, unsigned tiles, hipStream_t st) {
-  const dim3 grid(tiles, (unsigned)a.c.H, (unsigned)a.splits), block(64 * kAttnWaves);
-  if (i8)
-    hipLaunchKernelGGL((k_kv_attention<D, true>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((k_kv_attention<D, false>), grid, block, 0, st, a);
-  if (a.splits > 1) hipLaunchKernelGGL(k_kv_join<D>, dim3(tiles, (unsigned)a.c.H), dim3(256), 0, st, a);
+namespace {
+
+constexpr size_t kJoinBytes = 64u << 20;
+
+// How a call runs: row tiles of `rows` rows, whole (many rows), or in equal runs of the work.
+struct Shape {
+  bool whole;
+  int rows, runs, least;
+  bool join;
+};
+
+int rows_of_whole(int D) { return D == 256 ? 64 : 128; }
+
+Shape shape_of(const KvArgs& c, int R, int num_cu) {
+  Shape s{};
+  const int big = rows_of_whole(c.D);
+  // whole row tiles once they fill the chip twice over
+  if (c.T * R / big * c.H >= 2 * num_cu) {
+    s.whole = true;
+    s.rows = big;
+    return s;
+  }
+  const int64_t avg = (c.T * R + c.B - 1) / c.B;
+  s.rows = avg <= 16 ? 16 : 64;
+  const int B = (int)min((int64_t)c.B, (int64_t)kPlanSeqs);
+  const int64_t cap = ((int64_t)c.max_pages * c.P + kTokTile - 1) / kTokTile;  // steps of the longest sequence
+  s.least = s.rows == 16 ? 4 * kAttnWaves : 4;
+  const int64_t items = (c.T * R / s.rows + B) * c.H;
+  s.runs = (int)min((int64_t)2 * num_cu, max((items * cap + s.least - 1) / s.least, (int64_t)1));
+  s.runs = (int)min((int64_t)s.runs, (int64_t)(kJoinBytes / ((size_t)2 * s.rows * (c.D * 4 + 8))));
+  s.join = s.runs > 1;
+  return s;
+}
+
+template <int D, bool I8>
+hipError_t attention_of(KvAttnArgs a, const Shape& s, hipStream_t st) {
+  const dim3 block(64 * kAttnWaves);
+  constexpr int S = D == 256 ? 2 : 3;
+  if (s.whole) {
+    constexpr int RT = D == 256 ? 1 : 2;
+    const int64_t tiles = a.c.T * a.R / (16 * RT * kAttnWaves) + a.c.B;
+    constexpr int lds = SharedRows<D, I8, RT, S>::kBytes;
+    hipError_t e = set_lds_limit(reinterpret_cast<const void*>(k_kv_attention_rows<D, I8, RT, S>), lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_kv_attention_rows<D, I8, RT, S>), dim3((unsigned)(tiles * a.c.H)), block, lds, st, a);
+    return hipGetLastError();
+  }
+  const KvAttnArgs all = a;
+  for (int b = 0; b < all.c.B; b += kPlanSeqs) {  // the launches of one stream use the workspace in turn
+    a.c.B = min(all.c.B - b, kPlanSeqs);
+    a.c.offsets = all.c.offsets + b;
+    a.c.lens = all.c.lens + b;
+    a.c.table = all.c.table + b * all.c.table_stride;
+    if (s.rows == 16) {
+      hipLaunchKernelGGL((k_kv_attention_runs16<D, I8>), dim3((unsigned)s.runs), block, 0, st, a);
+    } else {
+      constexpr int lds = SharedRows<D, I8, 1, S>::kBytes;
+      hipError_t e = set_lds_limit(reinterpret_cast<const void*>(k_kv_attention_runs64<D, I8, S>), lds);
+      if (e != hipSuccess) return e;
+      hipLaunchKernelGGL((k_kv_attention_runs64<D, I8, S>), dim3((unsigned)s.runs), block, lds, st, a);
+    }
+    if (s.join) hipLaunchKernelGGL(k_kv_join<D>, dim3((unsigned)(s.runs - 1), (unsigned)s.rows), dim3(256), 0, st, a);
+  }
   return hipGetLastError();
 }
 
-static int64_t row_tiles(const KvArgs& c, int R) { return c.T * R / kRowTile + c.B; }
-
-// Parts of the keys: enough workgroups for the chip, while the longest sequence that the table
-// can hold keeps a step for each wave of a part.
-int kv_attention_splits(const KvArgs& c, int R, int num_cu) {
-  const int64_t wgs = row_tiles(c, R) * c.H;
-  const int64_t most = ((int64_t)c.max_pages * c.P + kTokTile * kAttnWaves - 1) / (kTokTile * kAttnWaves);
-  return (int)max((int64_t)1, min((2 * (int64_t)num_cu + wgs - 1) / wgs, min(most, (int64_t)65535)));
-}
+}  // namespace
 
 size_t kv_attention_workspace(const KvArgs& c, int R, int num_cu) {
-  const int splits = kv_attention_splits(c, R, num_cu);
-  return splits == 1 ? 0 : (size_t)(row_tiles(c, R) * c.H * kRowTile * splits) * (c.D * 4 + 8);
+  const Shape s = shape_of(c, R, num_cu);
+  return s.join ? (size_t)2 * s.runs * s.rows * (c.D * 4 + 8) : 0;
+}
+
+const char* kv_attention_kind(const KvArgs& c, int R, int num_cu) {
+  const Shape s = shape_of(c, R, num_cu);
+  return s.whole ? "row tiles" : s.join ? "runs and a join" : "one run";
 }
 
 hipError_t launch_kv_attention(KvAttnArgs a, bool i8, int num_cu, void* ws, hipStream_t st) {
-  const int64_t tiles = row_tiles(a.c, a.R);
-  a.splits = kv_attention_splits(a.c, a.R, num_cu);
+  const Shape s = shape_of(a.c, a.R, num_cu);
+  a.runs = s.runs;
+  a.least = s.least;
+  a.tile_rows = s.rows;
   a.part = static_cast<float*>(ws);
-  a.stat = a.splits > 1 ? reinterpret_cast<float2*>(a.part + tiles * a.c.H * kRowTile * a.splits * a.c.D) : nullptr;
-  if (a.c.D == 64) return attention_of<64>(a, i8, (unsigned)tiles, st);
-  if (a.c.D == 128) return attention_of<128>(a, i8, (unsigned)tiles, st);
-  return attention_of<256>(a, i8, (unsigned)tiles, st);
+  a.stat = s.join ? reinterpret_cast<float2*>(a.part + (size_t)2 * s.runs * s.rows * a.c.D) : nullptr;
+  if (a.c.D == 64) return i8 ? attention_of<64, true>(a, s, st) : attention_of<64, false>(a, s, st);
+  if (a.c.D == 128) return i8 ? attention_of<128, true>(a, s, st) : attention_of<128, false>(a, s, st);
+  return i8 ? attention_of<256, true>(a, s, st) : attention_of<256, false>(a, s, st);
 }
 
 }  // namespace wq

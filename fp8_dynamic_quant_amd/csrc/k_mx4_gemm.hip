@@ -19,7 +19,6 @@ namespace {
 
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
 typedef unsigned v4u __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) uint8_t* lds_ptr_b;
 
 __device__ __forceinline__ v8i regs4(const v4i lo) { return v8i{lo[0], lo[1], lo[2], lo[3], 0, 0, 0, 0}; }
 __device__ __forceinline__ v8i regs8(const v4i lo, const v4i hi) {
@@ -131,24 +130,6 @@ __device__ __forceinline__ int chunk_swz(int row) { return B == 64 ? (row >> 2) 
 template <int B>
 __device__ __forceinline__ int lds_at(int row, int c) { return row * B + ((c ^ chunk_swz<B>(row)) << 4); }
 
-// One DMA instruction of 64 lanes x 16 (or 4) bytes to LDS byte address `la` on: a wave-uniform
-// base and a lane offset.  Written out, with its LDS address in M0: given the builtin, the
-// compiler lets LDS reads that it cannot tell from the target wait for every DMA in flight.
-// The kernel orders them itself (vmcnt, then a barrier).  Nothing is loaded into registers.
-// Six wait states stand in front of the load: a base just written by the VALU needs five, M0 one.
-__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t la) {
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(la) : "memory", "m0");
-#pragma clang diagnostic pop
-}
-__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t la) {
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(la) : "memory", "m0");
-#pragma clang diagnostic pop
-}
-
 template <bool A8, int WM, int WN, int S>
 struct Ring {
   static constexpr int kBM = 64 * WM, kBN = 64 * WN;
@@ -160,9 +141,6 @@ struct Ring {
   static constexpr int kOut = kBM * kBN * 2;           // the bf16 tile, staged in the ring's place
   static constexpr int kBytes = S * kStage > kOut ? S * kStage : kOut;
 };
-
-template <int N>
-__device__ __forceinline__ void wait_vm() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
 template <bool A8, int WM, int WN, int S>
 __global__ __launch_bounds__(256, 2) void k_mx4_tile(Mx4Args p, int tiles_m, int tiles_n, int per_xcd) {
@@ -204,7 +182,7 @@ __global__ __launch_bounds__(256, 2) void k_mx4_tile(Mx4Args p, int tiles_m, int
     const int d = (wv + 4 * i) % kWordDmas, r = d * 64 + lane;
     soff[i] = (uint32_t)(d < WM ? min(r, M - 1 - m0) : min(r - R::kBM, N - 1 - n0)) * 4u;
   }
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_b)smem;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_u8)smem;
   auto issue = [&](int kt, int stage) __attribute__((always_inline)) {
     const uint32_t st = lds0 + stage * R::kStage;
     const uint8_t* a = A + (int64_t)kt * R::kARow;

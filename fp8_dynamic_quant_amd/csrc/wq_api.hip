@@ -880,6 +880,7 @@ static int kv_args(const wq_kv_cache* k, int64_t T, int64_t B, const int64_t* of
   out->P = (int)k->page_tokens;
   out->D = (int)k->head_dim;
   out->max_pages = (int)k->max_pages;
+  out->page_recip = (uint32_t)((((uint64_t)1 << 32) + out->P / 16 - 1) / (out->P / 16));  // (0 at P = 16, where it is not used)
   out->offsets = offsets;
   out->lens = lens;
   out->B = (int)B;
@@ -909,7 +910,7 @@ int wq_kv_append(wq_ctx* c, const wq_kv_cache* k, const void* k_new, int64_t ldk
 // q_heads a multiple of the cache's heads; row tiles are counted in 32 bits
 static bool kv_heads_ok(const wq_kv_cache* k, int64_t q_heads, int64_t T, int64_t B) {
   return q_heads >= k->heads && q_heads % k->heads == 0 && q_heads <= (1 << 20) &&
-         T * (q_heads / k->heads) / 16 + B < ((int64_t)1 << 31);
+         (T * (q_heads / k->heads) / 16 + B) * k->heads < ((int64_t)1 << 31);
 }
 
 int64_t wq_kv_attention_workspace_bytes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B) {
@@ -959,9 +960,9 @@ int wq_kv_attention(wq_ctx* c, const wq_kv_cache* k, const void* q, int64_t ldq,
   hipError_t e = wq::launch_kv_attention(a, k->code == WQ_KV_INT8, c->num_cu, workspace,
                                          static_cast<hipStream_t>(stream));
   if (c->log)
-    std::fprintf(stderr, "[wq] kv_attention %s T=%lld B=%lld heads=%lld/%lld D=%lld page=%lld parts=%d\n",
+    std::fprintf(stderr, "[wq] kv_attention %s T=%lld B=%lld heads=%lld/%lld D=%lld page=%lld: %s\n",
                  k->code == WQ_KV_INT8 ? "int8" : "e4m3", (long long)T, (long long)B, (long long)q_heads,
-                 (long long)k->heads, (long long)k->head_dim, (long long)k->page_tokens, wq::kv_attention_splits(a.c, a.R, c->num_cu));
+                 (long long)k->heads, (long long)k->head_dim, (long long)k->page_tokens, wq::kv_attention_kind(a.c, a.R, c->num_cu));
   return status_of(e);
 }
 

@@ -142,6 +142,7 @@ struct KvArgs {
   const int32_t* table;     // [B][table_stride], the first max_pages entries of a row used
   int64_t table_stride;
   int pages, H, P, D, max_pages;
+  uint32_t page_recip;      // ceil(2^32 / (P / 16)): token groups of 16 to pages without a division
   const int64_t* offsets;   // [B + 1]: rows of each sequence
   const int32_t* lens;      // [B]: tokens of each sequence, the new rows among them
   int B;
@@ -159,13 +160,16 @@ struct KvAttnArgs {
   float scale;
   int R;                    // query heads of each cache head
   int causal;
-  int splits;               // parts of a sequence's keys, joined by a second launch
-  float* part;              // splits > 1: [row tile][H][splits][16][D] unnormalised sums
-  float2* stat;             // splits > 1: [row tile][H][splits][16] running maximum (log2) and sum
+  // set by the launcher: workgroups that share the work, its least share in steps, the rows of a
+  // tile, and for items that are cut the parts' unnormalised sums [runs][2][tile_rows][D], running
+  // maxima (log2) and sums [runs][2][tile_rows]
+  int runs, least, tile_rows;
+  float* part;
+  float2* stat;
 };
 bool kv_head_dim_ok(int64_t D);
-// how many parts a call of these sizes cuts the keys into, and the bytes that joining them takes
-int kv_attention_splits(const KvArgs& c, int R, int num_cu);
+// how a call of these sizes runs, and the bytes that joining cut items takes
+const char* kv_attention_kind(const KvArgs& c, int R, int num_cu);
 size_t kv_attention_workspace(const KvArgs& c, int R, int num_cu);
 hipError_t launch_kv_attention(KvAttnArgs a, bool i8, int num_cu, void* ws, hipStream_t st);
 
