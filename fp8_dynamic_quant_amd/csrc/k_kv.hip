@@ -21,7 +21,8 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kTokTile = 64;     // tokens of a step
 constexpr int kAttnWaves = 4;    // waves of an attention workgroup
-constexpr int kPlanSeqs = 1024;  // sequences of one split launch (their work is summed up in LDS)
+constexpr int kPlanSeqs = 1024;  // sequences of one launch of runs (their work is summed up in LDS)
+constexpr int kMaxRuns = 1024;   // workgroups of one
 
 // The sequence of slot `item` when sequence b owns the slots from offsets[b] * mul / div +
 // per * b on (the host knows neither a sequence's rows nor its length, so every sequence gets
@@ -228,9 +229,10 @@ __device__ __forceinline__ Seq seq_of(const KvAttnArgs& a, int b, int64_t row0, 
 __device__ __forceinline__ uint32_t limit_of(const KvAttnArgs& a, const Seq& s, int i) {
   return a.causal ? (uint32_t)min((int64_t)max((int64_t)s.len - s.rows + i + 1, (int64_t)0), (int64_t)s.seen) : s.seen;
 }
-// number / divisor by the divisor's rounded-up reciprocal (exact below 2^28 for divisors to 16)
-__device__ __forceinline__ uint32_t by_page(uint32_t group, uint32_t per, uint32_t recip) {
-  return per == 1 ? group : __umulhi(group, recip);
+// page of a token group: group / per by per's rounded-up reciprocal (exact below 2^28 for per to
+// 16); at per = 1 the reciprocal is 0 and `one` all ones
+__device__ __forceinline__ uint32_t by_page(uint32_t group, uint32_t recip, uint32_t one) {
+  return __umulhi(group, recip) + (group & one);
 }
 
 // slots of the lane's 16 that hold tokens: from the sequence's end on they hold anything
@@ -247,8 +249,8 @@ __device__ __forceinline__ v4u keep_bytes(v4u v, int n) {  // the first n bytes,
 }
 
 // RT row tiles of a wave over steps [lo, hi) with stride TW, keys and values straight from memory
-// in operand order.  The values of a step load while its scores are made, the keys of the next one
-// during its softmax and products, page numbers two steps ahead.
+// in operand order.  The next step's keys load as soon as this one's scores are made, its values as
+// soon as this one's are used, so that each has a whole step's time; page numbers load two ahead.
 template <int D, bool I8, int RT>
 struct Rows {
   static constexpr int ND = D / 16, NC = D / 64;
@@ -324,7 +326,7 @@ struct Rows {
                                       int g) {
     if (lo >= hi) return;
     const KvArgs& c = a.c;
-    const uint32_t per = (uint32_t)c.P >> 4, recip = c.page_recip, H = (uint32_t)c.H;
+    const uint32_t per = (uint32_t)c.P >> 4, recip = c.page_recip, one = per == 1 ? ~0u : 0u, H = (uint32_t)c.H;
     const float to_log2 = fabsf(a.scale) * 1.44269504088896340736f;
     const uint32_t page_bytes = (uint32_t)c.P * D;
     const uint8_t* K = static_cast<const uint8_t*>(c.k) + (uint32_t)h * page_bytes;
@@ -339,13 +341,13 @@ struct Rows {
     };
     auto number = [&](uint32_t step, uint32_t grp) -> int {  // the table's entry
       const uint32_t tg = 4 * step + grp;
-      return 16 * tg < s.seen ? s.table[by_page(tg, per, recip)] : -1;
+      return 16 * tg < s.seen ? s.table[by_page(tg, recip, one)] : -1;
     };
     // a group past the end, or a page number that is none, reads page 0 and is masked
     auto place = [&](uint32_t step, uint32_t grp, int page) -> Page {
       const uint32_t tg = 4 * step + grp;
       const bool there = (uint32_t)page < (uint32_t)c.pages;
-      return Page{there ? (uint32_t)page : 0u, (tg - by_page(tg, per, recip) * per) * 16, there};
+      return Page{there ? (uint32_t)page : 0u, (tg - by_page(tg, recip, one) * per) * 16, there};
     };
     v4u kk[4][NC];
     auto load_k = [&](const Page& p) {
@@ -357,16 +359,19 @@ struct Rows {
     };
     Page pv = place(lo, g, number(lo, g));
     load_k(place(lo, kg, number(lo, kg)));
-    uint32_t kb = c.k_scale[(int64_t)pv.at * H + h];
+    uint32_t kb = c.k_scale[(int64_t)pv.at * H + h], vb;
+    v4u vv[ND];
+    auto load_v = [&](const Page& p) {
+      const uint8_t* vp = V + p.at * page_step + (uint32_t)j * c.P + p.slot;
+      vb = c.v_scale[(int64_t)p.at * H + h];
+#pragma unroll
+      for (int i = 0; i < ND; ++i) vv[i] = *reinterpret_cast<const v4u*>(vp + 16 * i * c.P);
+    };
+    load_v(pv);
     uint32_t nstep = min(lo + TW, hi - 1);  // the last step's "next" is a repeat, loaded and not used
     int nk = number(nstep, kg), nv = number(nstep, g);
     for (uint32_t step = lo; step < hi; step += TW) {
       const uint32_t tok0 = step * kTokTile, gt = tok0 + 16 * g;
-      const uint8_t* vp = V + pv.at * page_step + (uint32_t)j * c.P + pv.slot;
-      const uint32_t vb = c.v_scale[(int64_t)pv.at * H + h];
-      v4u vv[ND];
-#pragma unroll
-      for (int i = 0; i < ND; ++i) vv[i] = *reinterpret_cast<const v4u*>(vp + 16 * i * c.P);
       // ---- scores
       v4f sc[RT][4];
 #pragma unroll
@@ -410,7 +415,9 @@ struct Rows {
       // every token of the step is there for every row, and its values' scales are numbers
       if (tok0 + kTokTile <= first && __all(pv.there && vb != 255u)) finish(std::false_type{});
       else finish(std::true_type{});
+      // ---- the next step's values
       pv = npv;
+      load_v(pv);
     }
   }
 };
@@ -442,7 +449,7 @@ struct SharedRows {
     if (lo >= hi) return;
     const KvArgs& c = a.c;
     const int j = lane & 15, g = lane >> 4;
-    const uint32_t per = (uint32_t)c.P >> 4, recip = c.page_recip, H = (uint32_t)c.H;
+    const uint32_t per = (uint32_t)c.P >> 4, recip = c.page_recip, one = per == 1 ? ~0u : 0u, H = (uint32_t)c.H;
     const float to_log2 = fabsf(a.scale) * 1.44269504088896340736f;
     const uint32_t page_bytes = (uint32_t)c.P * D;
     const uint8_t* K = static_cast<const uint8_t*>(c.k) + (uint32_t)h * page_bytes;
@@ -453,7 +460,7 @@ struct SharedRows {
     // page of token group lane % 4 of a step, -1 where there is none
     auto page_of = [&](uint32_t tg) __attribute__((always_inline)) -> int {
       const bool in = 16 * tg < s.seen;
-      const int n = uniform(table[in ? by_page(tg, per, recip) : 0u]);
+      const int n = uniform(table[in ? by_page(tg, recip, one) : 0u]);
       return in && (uint32_t)n < (uint32_t)c.pages ? n : -1;
     };
     auto pages_of = [&](uint32_t step) __attribute__((always_inline)) -> int {
@@ -469,7 +476,7 @@ struct SharedRows {
       const uint32_t st = lds0 + stage * kStage;
       auto slot_of = [&](uint32_t x) {
         const uint32_t tg = 4 * step + x;
-        return (tg - by_page(tg, per, recip) * per) * 16;
+        return (tg - by_page(tg, recip, one) * per) * 16;
       };
       const int held = max(page, 0);  // a group without a page reads page 0 and is masked
       const uint8_t* kb = K + __builtin_amdgcn_readlane(held, wv) * page_step + slot_of(wv) * D;
@@ -620,90 +627,138 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_rows(KvAttn
 
 // Few rows: the work, tokens' steps of all (sequence, head, row tile) items in a row, is cut into
 // equal runs, one for each workgroup, whatever the lengths.  An item that lies in one run is stored;
-// of one that is cut the parts go to the workspace, and k_kv_join adds them.
+// of one that is cut the parts go to the workspace, and k_kv_join adds them.  Where a table holds
+// few tokens a unit of the work is a whole item, and nothing is cut.
 struct Plan {
-  int64_t units;  // steps in all
+  int64_t units;  // steps (or items) in all
   int runs;       // workgroups that take some
 };
-// Sums of the sequences' work in LDS: pre[b] = row tiles * steps of the sequences before b (for one
-// head).  Every thread of 256 takes part.
+struct PlanLds {
+  int64_t pre[kPlanSeqs + 1];  // work of the sequences before b, for one head
+  int row0[kPlanSeqs + 1];     // their rows
+  int len[kPlanSeqs];
+  int64_t carry[kAttnWaves];
+};
+__device__ __forceinline__ uint32_t steps_of(const KvArgs& c, int len) {
+  const int64_t seen = min((int64_t)max(len, 0), (int64_t)c.max_pages * c.P);
+  return (uint32_t)max((seen + kTokTile - 1) / kTokTile, (int64_t)1);  // rows that see nothing are stored too
+}
+// Every thread of the workgroup takes part.
 template <int kRows>
-__device__ __forceinline__ Plan make_plan(const KvAttnArgs& a, int64_t* pre, int64_t* carry) {
+__device__ __forceinline__ Plan make_plan(const KvAttnArgs& a, PlanLds& l) {
   const KvArgs& c = a.c;
   const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+  constexpr int kThreads = 64 * kAttnWaves;
   int64_t before = 0;
-  for (int b0 = 0; b0 < c.B; b0 += 256) {
+  for (int b0 = 0; b0 < c.B; b0 += kThreads) {
     const int b = b0 + t;
     int64_t v = 0;
     if (b < c.B) {
-      const int64_t rows = max(seq_offset(c, b + 1) - seq_offset(c, b), (int64_t)0);
-      const int64_t seen = min((int64_t)max(c.lens[b], 0), (int64_t)c.max_pages * c.P);
-      // a sequence without tokens still has rows to store: one step
-      v = (rows * a.R + kRows - 1) / kRows * max((seen + kTokTile - 1) / kTokTile, (int64_t)1);
+      const int64_t lo = seq_offset(c, b), rows = max(seq_offset(c, b + 1) - lo, (int64_t)0);
+      const int len = c.lens[b];
+      v = (rows * a.R + kRows - 1) / kRows * (a.cut ? steps_of(c, len) : 1);
+      l.row0[b] = (int)lo;
+      l.len[b] = len;
+      if (b == c.B - 1) l.row0[c.B] = (int)(lo + rows);
     }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int64_t u = __shfl_up(v, o, 64);
       if (lane >= o) v += u;
     }
-    if (lane == 63) carry[wv] = v;
+    if (lane == 63) l.carry[wv] = v;
     __syncthreads();
     int64_t base = before;
-    for (int w = 0; w < wv; ++w) base += carry[w];
-    if (b < c.B) pre[b + 1] = base + v;
-    before += carry[0] + carry[1] + carry[2] + carry[3];
+    for (int w = 0; w < wv; ++w) base += l.carry[w];
+    if (b < c.B) l.pre[b + 1] = base + v;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) before += l.carry[w];
     __syncthreads();
   }
-  if (t == 0) pre[0] = 0;
+  if (t == 0) l.pre[0] = 0;
   __syncthreads();
   Plan p;
   p.units = before * c.H;
-  // a run is worth a step for each wave
   p.runs = (int)min((int64_t)a.runs, (p.units + a.least - 1) / a.least);
   return p;
 }
+// n / d for non-negative n: 64-bit divisions take hundreds of cycles, and are hardly ever needed
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  return ((uint64_t)n | (uint64_t)d) >> 32 == 0 ? (int64_t)((uint32_t)n / (uint32_t)d) : n / d;
+}
 // run w takes units [start(w), start(w + 1))
-__device__ __forceinline__ int64_t run_start(const Plan& p, int w) { return p.units * w / p.runs; }
+__device__ __forceinline__ int64_t run_start(const Plan& p, int w) { return quotient(p.units * w, p.runs); }
 struct Item {
   int b, h, tile;
   uint32_t steps, step;  // of the item; the unit's step in it
 };
-__device__ __forceinline__ Item item_of(const KvAttnArgs& a, const int64_t* pre, int64_t u, int krows) {
+__device__ __forceinline__ Item item_of(const KvAttnArgs& a, const PlanLds& l, int64_t u) {
   const KvArgs& c = a.c;
   int lo = 0, hi = c.B - 1;
   while (lo < hi) {  // the last sequence that begins at or before u (of equal ones the one with work)
     const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] * c.H <= u) lo = mid;
+    if (l.pre[mid] * c.H <= u) lo = mid;
     else hi = mid - 1;
   }
   Item it;
   lo = uniform(lo);
   it.b = lo;
-  const int64_t seen = min((int64_t)max(c.lens[lo], 0), (int64_t)c.max_pages * c.P);
-  it.steps = (uint32_t)uniform((int)max((seen + kTokTile - 1) / kTokTile, (int64_t)1));
-  const int64_t in = u - pre[lo] * c.H;
-  const int64_t item = in / it.steps;
-  it.step = (uint32_t)uniform((int)(in - item * it.steps));
-  const int tiles = (int)((pre[lo + 1] - pre[lo]) / it.steps);
-  it.h = uniform((int)(item / tiles));
-  it.tile = uniform((int)(item % tiles));
+  it.steps = (uint32_t)uniform((int)steps_of(c, l.len[lo]));
+  const uint32_t per = a.cut ? it.steps : 1;
+  const int64_t in = u - l.pre[lo] * c.H;
+  const int64_t item = quotient(in, per);
+  it.step = (uint32_t)uniform((int)(in - item * per));
+  const int64_t tiles = quotient(l.pre[lo + 1] - l.pre[lo], per);
+  it.h = uniform((int)quotient(item, tiles));
+  it.tile = uniform((int)(item - it.h * tiles));
   return it;
 }
+__device__ __forceinline__ Seq seq_of(const KvAttnArgs& a, const PlanLds& l, int b) {
+  Seq s;
+  s.row0 = uniform(l.row0[b]);
+  s.rows = uniform(l.row0[b + 1]) - (int)s.row0;
+  s.nrows = (int64_t)s.rows * a.R;
+  s.len = uniform(l.len[b]);
+  s.seen = (uint32_t)min((int64_t)max(s.len, 0), (int64_t)a.c.max_pages * a.c.P);
+  s.table = a.c.table + b * a.c.table_stride;
+  return s;
+}
 
-// What both kinds of run do with an item: its sequence and rows, and where its part goes
+// A run's share of an item, and where its part goes
 struct Run {
   Item it;
   uint32_t n;    // steps of it
   bool whole;
   int64_t slot;  // first row of its part in the workspace
 };
-__device__ __forceinline__ Run next_run(const KvAttnArgs& a, const int64_t* pre, int64_t u, int64_t end, int part, int krows) {
+__device__ __forceinline__ Run next_run(const KvAttnArgs& a, const PlanLds& l, int64_t u, int64_t end, int part, int krows) {
   Run r;
-  r.it = item_of(a, pre, u, krows);
-  r.n = (uint32_t)uniform((int)min((int64_t)(r.it.steps - r.it.step), end - u));
+  r.it = item_of(a, l, u);
+  r.n = a.cut ? (uint32_t)uniform((int)min((int64_t)(r.it.steps - r.it.step), end - u)) : r.it.steps;
   r.whole = r.n == r.it.steps;
   r.slot = ((int64_t)blockIdx.x * 2 + part) * krows;
   return r;
+}
+// What k_kv_join needs of the item that run w begins inside, if it is the first run to do so
+// (parts = 0 otherwise): it stands for the item.
+__device__ __forceinline__ void tell_join(const KvAttnArgs& a, const Plan& p, const PlanLds& l, int w) {
+  if (threadIdx.x != 0 || a.joins == nullptr) return;
+  KvJoin d{};
+  if (w > 0 && w < p.runs) {
+    const int64_t u = run_start(p, w);
+    const Item it = item_of(a, l, u);
+    const int64_t i0 = u - it.step, i1 = i0 + it.steps, start = run_start(p, w - 1);
+    if (it.step > 0 && start <= i0) {
+      const int last = (int)quotient(i1 * p.runs - 1, p.units);  // the last run that begins before i1
+      d.parts = last - w + 2;
+      d.first_slot = 2 * (w - 1) + (start < i0 ? 1 : 0);  // its second part if the item begins inside it
+      d.h = it.h;
+      d.tile = it.tile;
+      d.row0 = l.row0[it.b];
+      d.rows = l.row0[it.b + 1] - d.row0;
+    }
+  }
+  a.joins[w] = d;
 }
 
 // 64-row tiles, each wave 16 rows of its own, keys shared through LDS
@@ -712,18 +767,18 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs64(KvAt
   using W = SharedRows<D, I8, 1, S>;
   constexpr int kRows = 64;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ int64_t pre[kPlanSeqs + 1], carry[4];
+  __shared__ PlanLds plan_lds;
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const Plan plan = make_plan<kRows>(a, pre, carry);
+  const Plan plan = make_plan<kRows>(a, plan_lds);
+  if (a.cut) tell_join(a, plan, plan_lds, blockIdx.x);
   if ((int)blockIdx.x >= plan.runs) return;
   int64_t u = run_start(plan, blockIdx.x);
   const int64_t end = run_start(plan, blockIdx.x + 1);
   for (int part = 0; u < end; part = 1) {
-    const Run r = next_run(a, pre, u, end, part, kRows);
-    u += r.n;
-    const int64_t row0 = seq_offset(a.c, r.it.b);
-    const Seq s = seq_of(a, r.it.b, row0, seq_offset(a.c, r.it.b + 1) - row0);
+    const Run r = next_run(a, plan_lds, u, end, part, kRows);
+    u += a.cut ? r.n : 1;
+    const Seq s = seq_of(a, plan_lds, r.it.b);
     const int64_t t0 = (int64_t)r.it.tile * kRows, r0 = t0 + wv * 16;
     auto steps_to = [&](int64_t row) {
       return (uint32_t)__builtin_amdgcn_readfirstlane((int)((limit_of(a, s, (int)(row / a.R)) + kTokTile - 1) / kTokTile));
@@ -746,22 +801,22 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs64(KvAt
 
 // 16-row tiles: the waves share the rows and take steps in turn, and are joined in LDS
 template <int D, bool I8>
-__global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void k_kv_attention_runs16(KvAttnArgs a) {
+__global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs16(KvAttnArgs a) {
   constexpr int kRows = 16;
   __shared__ float o_lds[kAttnWaves][kRows][D + 4];
   __shared__ float m_lds[kAttnWaves][kRows], l_lds[kAttnWaves][kRows];
-  __shared__ int64_t pre[kPlanSeqs + 1], carry[4];
+  __shared__ PlanLds plan_lds;
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const Plan plan = make_plan<kRows>(a, pre, carry);
+  const Plan plan = make_plan<kRows>(a, plan_lds);
+  if (a.cut) tell_join(a, plan, plan_lds, blockIdx.x);
   if ((int)blockIdx.x >= plan.runs) return;
   int64_t u = run_start(plan, blockIdx.x);
   const int64_t end = run_start(plan, blockIdx.x + 1);
   for (int part = 0; u < end; part = 1) {
-    const Run r = next_run(a, pre, u, end, part, kRows);
-    u += r.n;
-    const int64_t row0 = seq_offset(a.c, r.it.b);
-    const Seq s = seq_of(a, r.it.b, row0, seq_offset(a.c, r.it.b + 1) - row0);
+    const Run r = next_run(a, plan_lds, u, end, part, kRows);
+    u += a.cut ? r.n : 1;
+    const Seq s = seq_of(a, plan_lds, r.it.b);
     const int64_t r0 = (int64_t)r.it.tile * kRows;
     const uint32_t most = __builtin_amdgcn_readfirstlane(
         (int)((limit_of(a, s, (int)((min(r0 + kRows, s.nrows) - 1) / a.R)) + kTokTile - 1) / kTokTile));
@@ -814,79 +869,77 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void k_kv_attent
   }
 }
 
-// The items that runs cut, joined part by part in order.  Run w > 0 that begins inside an item,
-// the first to do so, stands for it; one workgroup for each (run, row of the tile): the threads'
-// quarters take every fourth part, and are added in order.
-template <int D>
-__global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
-  __shared__ int64_t pre[kPlanSeqs + 1], carry[4];
-  __shared__ float o_lds[4][D], m_lds[4], l_lds[4];
-  const int krows = a.tile_rows, row = blockIdx.y;
-  const Plan plan = krows == 16 ? make_plan<16>(a, pre, carry) : make_plan<64>(a, pre, carry);
-  const int run = blockIdx.x + 1;
-  if (run >= plan.runs) return;
-  const int64_t u = run_start(plan, run);
-  const Item it = item_of(a, pre, u, krows);
-  const int64_t i0 = u - it.step, i1 = i0 + it.steps;
-  if (it.step == 0 || run_start(plan, run - 1) > i0) return;
-  const KvArgs& c = a.c;
-  const int64_t row0 = seq_offset(c, it.b), nrows = (seq_offset(c, it.b + 1) - row0) * a.R;
-  const int64_t rr = (int64_t)it.tile * krows + row;
-  if (rr >= nrows) return;
-  // runs run - 1 .. last - 1 hold its parts: the first one's is its second if the item begins inside
-  int last = run;
-  {
-    int lo = run, hi = plan.runs - 1;  // the last run that begins before i1
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (run_start(plan, mid) < i1) lo = mid;
-      else hi = mid - 1;
-    }
-    last = lo + 1;
+// The items that runs cut: one workgroup for each (run that stands for one, row of the tile).  W
+// waves take every W-th part, with the weights of all parts in LDS first, and are added in order.
+template <int D, int W>
+__global__ __launch_bounds__(64 * W) void k_kv_join(KvAttnArgs a) {
+  constexpr int kAhead = 8, E = D / 64;  // parts in flight; elements of a lane
+  __shared__ float wgt[kMaxRuns + 1], o_lds[W][D], red[W];
+  const KvJoin d = a.joins[blockIdx.x + 1];
+  const int row = blockIdx.y, run = blockIdx.x + 1;
+  const int64_t rr = (int64_t)d.tile * a.tile_rows + row;
+  if (d.parts == 0 || rr >= (int64_t)d.rows * a.R) return;
+  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+  auto slot_of = [&](int p) -> int64_t { return (int64_t)(p == 0 ? d.first_slot : 2 * (run - 1 + p)) * a.tile_rows + row; };
+  float M = -INFINITY;
+  for (int p = t; p < d.parts; p += 64 * W) {
+    const float m = a.stat[slot_of(p)].x;
+    wgt[p] = m;
+    M = fmaxf(M, m);
   }
-  const int first_slot = 2 * (run - 1) + (run_start(plan, run - 1) < i0 ? 1 : 0);
-  auto slot_of = [&](int p) -> int64_t { return (int64_t)(p == 0 ? first_slot : 2 * (run - 1 + p)) * krows + row; };
-  const int parts = last - run + 1, q = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  constexpr int E = D / 64;  // elements of a lane
-  float M = -INFINITY, L = 0.0f, acc[E];
+  M = wave_max(M);
+  if constexpr (W > 1) {
+    if (lane == 0) red[wv] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) M = fmaxf(M, red[w]);
+    __syncthreads();
+  }
+  const float Mb = M == -INFINITY ? 0.0f : M;
+  float L = 0.0f;
+  for (int p = t; p < d.parts; p += 64 * W) {
+    const float x = __builtin_amdgcn_exp2f(wgt[p] - Mb);
+    wgt[p] = x;
+    L += x * a.stat[slot_of(p)].y;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) L += __shfl_xor(L, o, 64);
+  if (lane == 0) red[wv] = L;
+  __syncthreads();
+  L = 0.0f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) L += red[w];
+  float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-  for (int p = q; p < parts; p += 4) {
-    const float2 st = a.stat[slot_of(p)];
-    const float* from = a.part + slot_of(p) * D + lane * E;
-    const float mn = fmaxf(M, st.x), mb = mn == -INFINITY ? 0.0f : mn;
-    const float w0 = __builtin_amdgcn_exp2f(M - mb), w1 = __builtin_amdgcn_exp2f(st.x - mb);
-    M = mn;
-    L = L * w0 + st.y * w1;
+  for (int p0 = wv; p0 < d.parts; p0 += W * kAhead) {
+    float v[kAhead][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * w0 + from[e] * w1;
-  }
+    for (int x = 0; x < kAhead; ++x) {
+      const float* from = a.part + slot_of(min(p0 + x * W, d.parts - 1)) * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) o_lds[q][lane * E + e] = acc[e];
-  if (lane == 0) {
-    m_lds[q] = M;
-    l_lds[q] = L;
-  }
-  __syncthreads();
-  M = fmaxf(fmaxf(m_lds[0], m_lds[1]), fmaxf(m_lds[2], m_lds[3]));
-  const float Mb = M == -INFINITY ? 0.0f : M;
-  L = 0.0f;
-  float wgt[4];
+      for (int e = 0; e < E; ++e) v[x][e] = from[e];
+    }
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    wgt[x] = __builtin_amdgcn_exp2f(m_lds[x] - Mb);
-    L += wgt[x] * l_lds[x];
+    for (int x = 0; x < kAhead; ++x)
+      if (p0 + x * W < d.parts) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += wgt[p0 + x * W] * v[x][e];
+      }
   }
   const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
-  const int i = (int)rr / a.R, head = it.h * a.R + (int)rr % a.R;
-  uint16_t* out = a.out + (row0 + i) * a.ldo + (int64_t)head * D;
-  for (int d = threadIdx.x; d < D; d += 256) {
-    float v = 0.0f;
+  const int i = (int)rr / a.R, head = d.h * a.R + (int)rr % a.R;
+  uint16_t* out = a.out + ((int64_t)d.row0 + i) * a.ldo + (int64_t)head * D;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) v += wgt[x] * o_lds[x][d];
-    out[d] = (uint16_t)f32_to_bf16_nan(v * inv);
+  for (int e = 0; e < E; ++e) o_lds[wv][lane * E + e] = acc[e];
+  __syncthreads();
+  for (int x = t; x < D; x += 64 * W) {
+    float v = o_lds[0][x];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += o_lds[w][x];
+    out[x] = (uint16_t)f32_to_bf16_nan(v * inv);
   }
-  if (a.lse && threadIdx.x == 0) a.lse[(row0 + i) * (int64_t)(c.H * a.R) + head] = log_sum(M, L);
+  if (a.lse && t == 0) a.lse[((int64_t)d.row0 + i) * (a.c.H * a.R) + head] = log_sum(M, L);
 }
 
 }  // namespace
@@ -910,8 +963,8 @@ constexpr size_t kJoinBytes = 64u << 20;
 // How a call runs: row tiles of `rows` rows, whole (many rows), or in equal runs of the work.
 struct Shape {
   bool whole;
-  int rows, runs, least;
-  bool join;
+  int rows, runs, least, cut;
+  bool wide_join;
 };
 
 int rows_of_whole(int D) { return D == 256 ? 64 : 128; }
@@ -926,14 +979,20 @@ Shape shape_of(const KvArgs& c, int R, int num_cu) {
     return s;
   }
   const int64_t avg = (c.T * R + c.B - 1) / c.B;
-  s.rows = avg <= 16 ? 16 : 64;
-  const int B = (int)min((int64_t)c.B, (int64_t)kPlanSeqs);
+  s.rows = avg <= 16 && c.D < 256 ? 16 : 64;
+  const int64_t B = min((int64_t)c.B, (int64_t)kPlanSeqs);
   const int64_t cap = ((int64_t)c.max_pages * c.P + kTokTile - 1) / kTokTile;  // steps of the longest sequence
-  s.least = s.rows == 16 ? 4 * kAttnWaves : 4;
   const int64_t items = (c.T * R / s.rows + B) * c.H;
-  s.runs = (int)min((int64_t)2 * num_cu, max((items * cap + s.least - 1) / s.least, (int64_t)1));
-  s.runs = (int)min((int64_t)s.runs, (int64_t)(kJoinBytes / ((size_t)2 * s.rows * (c.D * 4 + 8))));
-  s.join = s.runs > 1;
+  // a sequence of few steps is not worth cutting: a run is an item then
+  s.cut = cap > (s.rows == 16 ? 4 * kAttnWaves : 8);
+  s.least = !s.cut ? 1 : s.rows == 16 ? 2 * kAttnWaves : 4;
+  const int most = (int)min((int64_t)min(kMaxRuns, 2 * num_cu), (int64_t)(kJoinBytes / ((size_t)2 * s.rows * (c.D * 4 + 8) + sizeof(KvJoin))));
+  if (!s.cut) {
+    s.runs = (int)min(items, (int64_t)1 << 30);
+  } else {
+    s.runs = (int)min((int64_t)most, (items * cap + s.least - 1) / s.least);
+    s.wide_join = items * 8 < s.runs;  // many parts to an item
+  }
   return s;
 }
 
@@ -957,14 +1016,21 @@ hipError_t attention_of(KvAttnArgs a, const Shape& s, hipStream_t st) {
     a.c.lens = all.c.lens + b;
     a.c.table = all.c.table + b * all.c.table_stride;
     if (s.rows == 16) {
-      hipLaunchKernelGGL((k_kv_attention_runs16<D, I8>), dim3((unsigned)s.runs), block, 0, st, a);
+      // (a head of 256 elements does not fit the registers that leave two waves to a SIMD)
+      if constexpr (D < 256) hipLaunchKernelGGL((k_kv_attention_runs16<D, I8>), dim3((unsigned)s.runs), block, 0, st, a);
     } else {
       constexpr int lds = SharedRows<D, I8, 1, S>::kBytes;
       hipError_t e = set_lds_limit(reinterpret_cast<const void*>(k_kv_attention_runs64<D, I8, S>), lds);
       if (e != hipSuccess) return e;
       hipLaunchKernelGGL((k_kv_attention_runs64<D, I8, S>), dim3((unsigned)s.runs), block, lds, st, a);
     }
-    if (s.join) hipLaunchKernelGGL(k_kv_join<D>, dim3((unsigned)(s.runs - 1), (unsigned)s.rows), dim3(256), 0, st, a);
+    if (s.cut && s.runs > 1) {
+      const dim3 grid((unsigned)(s.runs - 1), (unsigned)s.rows);
+      if (s.wide_join)
+        hipLaunchKernelGGL((k_kv_join<D, 4>), grid, dim3(256), 0, st, a);
+      else
+        hipLaunchKernelGGL((k_kv_join<D, 1>), grid, dim3(64), 0, st, a);
+    }
   }
   return hipGetLastError();
 }
@@ -973,21 +1039,26 @@ hipError_t attention_of(KvAttnArgs a, const Shape& s, hipStream_t st) {
 
 size_t kv_attention_workspace(const KvArgs& c, int R, int num_cu) {
   const Shape s = shape_of(c, R, num_cu);
-  return s.join ? (size_t)2 * s.runs * s.rows * (c.D * 4 + 8) : 0;
+  return s.cut ? (size_t)s.runs * ((size_t)2 * s.rows * (c.D * 4 + 8) + sizeof(KvJoin)) : 0;
 }
 
 const char* kv_attention_kind(const KvArgs& c, int R, int num_cu) {
   const Shape s = shape_of(c, R, num_cu);
-  return s.whole ? "row tiles" : s.join ? "runs and a join" : "one run";
+  return s.whole ? "row tiles" : s.cut ? "equal runs" : "items";
 }
 
 hipError_t launch_kv_attention(KvAttnArgs a, bool i8, int num_cu, void* ws, hipStream_t st) {
   const Shape s = shape_of(a.c, a.R, num_cu);
   a.runs = s.runs;
   a.least = s.least;
+  a.cut = s.cut;
   a.tile_rows = s.rows;
-  a.part = static_cast<float*>(ws);
-  a.stat = s.join ? reinterpret_cast<float2*>(a.part + (size_t)2 * s.runs * s.rows * a.c.D) : nullptr;
+  if (s.cut) {
+    const size_t slots = (size_t)2 * s.runs * s.rows;
+    a.part = static_cast<float*>(ws);
+    a.stat = reinterpret_cast<float2*>(a.part + slots * a.c.D);
+    a.joins = reinterpret_cast<KvJoin*>(a.stat + slots);
+  }
   if (a.c.D == 64) return i8 ? attention_of<64, true>(a, s, st) : attention_of<64, false>(a, s, st);
   if (a.c.D == 128) return i8 ? attention_of<128, true>(a, s, st) : attention_of<128, false>(a, s, st);
   return i8 ? attention_of<256, true>(a, s, st) : attention_of<256, false>(a, s, st);

@@ -150,6 +150,10 @@ struct KvArgs {
 };
 hipError_t launch_kv_append(const KvArgs& c, bool i8, const uint16_t* k_new, int64_t ldk, const uint16_t* v_new,
                             int64_t ldv, hipStream_t st);
+// an item that several workgroups share (k_kv_join): its parts' slots, and the rows it is of
+struct KvJoin {
+  int parts, first_slot, h, tile, row0, rows, spare[2];
+};
 struct KvAttnArgs {
   KvArgs c;
   const uint16_t* q;        // bf16 [T][Hq * D], row stride ldq
@@ -160,12 +164,13 @@ struct KvAttnArgs {
   float scale;
   int R;                    // query heads of each cache head
   int causal;
-  // set by the launcher: workgroups that share the work, its least share in steps, the rows of a
-  // tile, and for items that are cut the parts' unnormalised sums [runs][2][tile_rows][D], running
-  // maxima (log2) and sums [runs][2][tile_rows]
-  int runs, least, tile_rows;
+  // set by the launcher: workgroups that share the work, its least share in steps, whether items
+  // are cut, the rows of a tile, and for items that are cut the parts' unnormalised sums
+  // [runs][2][tile_rows][D], running maxima (log2) and sums [runs][2][tile_rows], and [runs] joins
+  int runs, least, cut, tile_rows;
   float* part;
   float2* stat;
+  KvJoin* joins;
 };
 bool kv_head_dim_ok(int64_t D);
 // how a call of these sizes runs, and the bytes that joining cut items takes
