@@ -260,25 +260,27 @@ struct Rows {
   uint32_t limit[RT];
 
   // r0: the first row; rows past the sequence's last repeat it (and are not stored)
-  __device__ __forceinline__ void begin(const KvAttnArgs& a, const Seq& s, int h, int64_t r0, int j, int g) {
+  __device__ __forceinline__ void limits(const KvAttnArgs& a, const Seq& s, int64_t r0, int j) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int rc = (int)min(r0 + 16 * rt + j, s.nrows - 1);
-      const int i = rc / a.R, head = h * a.R + rc % a.R;
-      limit[rt] = limit_of(a, s, i);
-      const uint16_t* q = a.q + (s.row0 + i) * a.ldq + (int64_t)head * D + 16 * g;
-#pragma unroll
-      for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          v4u w = *reinterpret_cast<const v4u*>(q + 64 * cc + 8 * m);
-          if (a.scale < 0.0f) w ^= 0x80008000u;  // the sign goes into q, so that scores scale by |scale|
-          qf[rt][cc][m] = __builtin_bit_cast(v8bf, w);
-        }
+      limit[rt] = limit_of(a, s, (int)min(r0 + 16 * rt + j, s.nrows - 1) / a.R);
       mx[rt] = -INFINITY;
       sum[rt] = 0.0f;
 #pragma unroll
-      for (int i2 = 0; i2 < ND; ++i2) o[rt][i2] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < ND; ++i) o[rt][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  }
+  __device__ __forceinline__ void load_q(const KvAttnArgs& a, const Seq& s, int h, int64_t r0, int j, int g) {
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;  // the sign goes into q: scores scale by |scale|
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int rc = (int)min(r0 + 16 * rt + j, s.nrows - 1);
+      const uint16_t* q = a.q + (s.row0 + rc / a.R) * a.ldq + (int64_t)(h * a.R + rc % a.R) * D + 16 * g;
+#pragma unroll
+      for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          qf[rt][cc][m] = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(q + 64 * cc + 8 * m) ^ flip);
     }
   }
 
@@ -287,12 +289,13 @@ struct Rows {
   __device__ __forceinline__ void weights(v4f (&sc)[RT][4], v8bf (&pf)[RT][2], float ks, float vs, bool there, uint32_t gt) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
+      const int left = there ? (int)min(limit[rt], 0x7FFFFFFFu) - (int)min(gt, 0x7FFFFFFFu) : 0;  // tokens from gt on that the row sees
       float top = -INFINITY;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          if constexpr (MASK) sc[rt][t][r] = there && gt + 4 * t + r < limit[rt] ? sc[rt][t][r] * ks : -INFINITY;
+          if constexpr (MASK) sc[rt][t][r] = 4 * t + r < left ? sc[rt][t][r] * ks : -INFINITY;
           top = fmaxf(top, sc[rt][t][r]);
         }
       if constexpr (!MASK) top *= ks;
@@ -322,9 +325,11 @@ struct Rows {
     }
   }
 
-  __device__ __forceinline__ void run(const KvAttnArgs& a, const Seq& s, int h, uint32_t lo, uint32_t hi, uint32_t TW, int j,
-                                      int g) {
+  __device__ __forceinline__ void run(const KvAttnArgs& a, const Seq& s, int h, int64_t r0, uint32_t lo, uint32_t hi,
+                                      uint32_t TW, int j, int g) {
+    limits(a, s, r0, j);
     if (lo >= hi) return;
+    auto begin_rows = [&]() __attribute__((always_inline)) { load_q(a, s, h, r0, j, g); };
     const KvArgs& c = a.c;
     const uint32_t per = (uint32_t)c.P >> 4, recip = c.page_recip, one = per == 1 ? ~0u : 0u, H = (uint32_t)c.H;
     const float to_log2 = fabsf(a.scale) * 1.44269504088896340736f;
@@ -333,8 +338,6 @@ struct Rows {
     const uint8_t* V = static_cast<const uint8_t*>(c.v) + (uint32_t)h * page_bytes;
     const int64_t page_step = (int64_t)H * page_bytes;
     const int kg = j >> 2;  // the token group that this lane reads keys of
-    uint32_t first = limit[0];  // the least limit of the wave's rows: the first row's
-    first = __builtin_amdgcn_readfirstlane((int)first);
     struct Page {
       uint32_t at, slot;
       bool there;
@@ -357,8 +360,10 @@ struct Rows {
 #pragma unroll
         for (int cc = 0; cc < NC; ++cc) kk[t][cc] = *reinterpret_cast<const v4u*>(kp + 4 * t * D + 64 * cc);
     };
-    Page pv = place(lo, g, number(lo, g));
-    load_k(place(lo, kg, number(lo, kg)));
+    const int n0 = number(lo, g), n1 = number(lo, kg);
+    begin_rows();  // (the rows' own loads behind the page numbers', which are waited for first)
+    Page pv = place(lo, g, n0);
+    load_k(place(lo, kg, n1));
     uint32_t kb = c.k_scale[(int64_t)pv.at * H + h], vb;
     v4u vv[ND];
     auto load_v = [&](const Page& p) {
@@ -397,24 +402,21 @@ struct Rows {
       nv = number(nstep, g);
       // ---- weights and values
       const float vs = scale_of(vb);
-      auto finish = [&](auto masked) __attribute__((always_inline)) {
-        constexpr bool MASK = decltype(masked)::value;
-        v8bf pf[RT][2];
-        this->template weights<MASK>(sc, pf, ks, vs, pv.there, gt);
+      // (always masked: a second copy of this code without the masks is slower to fetch than it saves)
+      v8bf pf[RT][2];
+      weights<true>(sc, pf, ks, vs, pv.there, gt);
+      if (tok0 + kTokTile > s.seen || !__all(pv.there)) {
 #pragma unroll
-        for (int i = 0; i < ND; ++i) {
-          if constexpr (MASK) vv[i] = keep_bytes(vv[i], there_slots(s, pv.there, gt));
+        for (int i = 0; i < ND; ++i) vv[i] = keep_bytes(vv[i], there_slots(s, pv.there, gt));
+      }
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const v8bf vf = widen8<I8>(vv[i][2 * m], vv[i][2 * m + 1], MASK ? 1.0f : vs);
+      for (int i = 0; i < ND; ++i)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) o[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][m], o[rt][i], 0, 0, 0);
-          }
+        for (int m = 0; m < 2; ++m) {
+          const v8bf vf = widen8<I8>(vv[i][2 * m], vv[i][2 * m + 1], 1.0f);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) o[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][m], o[rt][i], 0, 0, 0);
         }
-      };
-      // every token of the step is there for every row, and its values' scales are numbers
-      if (tok0 + kTokTile <= first && __all(pv.there && vb != 255u)) finish(std::false_type{});
-      else finish(std::true_type{});
       // ---- the next step's values
       pv = npv;
       load_v(pv);
@@ -619,30 +621,43 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_rows(KvAttn
     return (uint32_t)__builtin_amdgcn_readfirstlane((int)((limit_of(a, s, (int)(row / a.R)) + kTokTile - 1) / kTokTile));
   };
   Rows<D, I8, RT> w;
-  w.begin(a, s, h, r0, j, g);
+  w.limits(a, s, r0, j);
+  w.load_q(a, s, h, r0, j, g);
   W::run(w, a, s, h, 0, steps_to(min(t0 + kRows, s.nrows) - 1),
          r0 < s.nrows ? steps_to(min(r0 + 16 * RT, s.nrows) - 1) : 0, smem, wv, lane);
   store_rows(a, s, w, h, r0, j, g);
 }
 
-// Few rows: the work, tokens' steps of all (sequence, head, row tile) items in a row, is cut into
-// equal runs, one for each workgroup, whatever the lengths.  An item that lies in one run is stored;
-// of one that is cut the parts go to the workspace, and k_kv_join adds them.  Where a table holds
-// few tokens a unit of the work is a whole item, and nothing is cut.
+// Few rows: the work, the 64-token steps of all (sequence, head, row tile) items in a row, is cut
+// into equal runs, one for each workgroup, whatever the lengths.  An item also counts `fixed` steps
+// for its beginning and end (without them the workgroups that got many short sequences came in
+// last: 64 sequences of 700 to 8192 tokens, the median done after 99 us, the last after 138); a cut
+// inside those lies in front of the item.  An item that lies in one run is stored; of one that is
+// cut the parts go to the workspace, and k_kv_join adds them.  Where a table holds few tokens a run
+// is one item, and nothing is cut.
 struct Plan {
-  int64_t units;  // steps (or items) in all
+  int64_t units;  // steps, the fixed ones among them, or items
+  int64_t per;    // of a run
   int runs;       // workgroups that take some
 };
 struct PlanLds {
-  int64_t pre[kPlanSeqs + 1];  // work of the sequences before b, for one head
+  int64_t pre[kPlanSeqs + 1];  // units of the sequences before b, for one head
   int row0[kPlanSeqs + 1];     // their rows
   int len[kPlanSeqs];
   int64_t carry[kAttnWaves];
 };
+// n / d for 0 <= n < 2^52 (what the call accepts stays below), d > 0; integer divisions of 64 bits
+// are hundreds of instructions
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  int64_t q = (int64_t)((double)n / (double)d);
+  const int64_t r = n - q * d;
+  return r < 0 ? q - 1 : r >= d ? q + 1 : q;
+}
 __device__ __forceinline__ uint32_t steps_of(const KvArgs& c, int len) {
   const int64_t seen = min((int64_t)max(len, 0), (int64_t)c.max_pages * c.P);
   return (uint32_t)max((seen + kTokTile - 1) / kTokTile, (int64_t)1);  // rows that see nothing are stored too
 }
+__device__ __forceinline__ uint32_t units_of(const KvAttnArgs& a, uint32_t steps) { return a.cut ? steps + a.fixed : 1; }
 // Every thread of the workgroup takes part.
 template <int kRows>
 __device__ __forceinline__ Plan make_plan(const KvAttnArgs& a, PlanLds& l) {
@@ -656,15 +671,17 @@ __device__ __forceinline__ Plan make_plan(const KvAttnArgs& a, PlanLds& l) {
     if (b < c.B) {
       const int64_t lo = seq_offset(c, b), rows = max(seq_offset(c, b + 1) - lo, (int64_t)0);
       const int len = c.lens[b];
-      v = (rows * a.R + kRows - 1) / kRows * (a.cut ? steps_of(c, len) : 1);
+      v = (rows * a.R + kRows - 1) / kRows * units_of(a, steps_of(c, len));
       l.row0[b] = (int)lo;
       l.len[b] = len;
       if (b == c.B - 1) l.row0[c.B] = (int)(lo + rows);
     }
+    if (b0 + wv * 64 < c.B) {
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t u = __shfl_up(v, o, 64);
-      if (lane >= o) v += u;
+      for (int o = 1; o < 64; o <<= 1) {
+        const int64_t u = __shfl_up(v, o, 64);
+        if (lane >= o) v += u;
+      }
     }
     if (lane == 63) l.carry[wv] = v;
     __syncthreads();
@@ -673,24 +690,19 @@ __device__ __forceinline__ Plan make_plan(const KvAttnArgs& a, PlanLds& l) {
     if (b < c.B) l.pre[b + 1] = base + v;
 #pragma unroll
     for (int w = 0; w < kAttnWaves; ++w) before += l.carry[w];
+    if (b == 0) l.pre[0] = 0;
     __syncthreads();
   }
-  if (t == 0) l.pre[0] = 0;
-  __syncthreads();
   Plan p;
   p.units = before * c.H;
-  p.runs = (int)min((int64_t)a.runs, (p.units + a.least - 1) / a.least);
+  p.per = max(quotient(p.units + a.runs - 1, a.runs), (int64_t)a.least);
+  p.runs = (int)quotient(p.units + p.per - 1, p.per);
   return p;
 }
-// n / d for non-negative n: 64-bit divisions take hundreds of cycles, and are hardly ever needed
-__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
-  return ((uint64_t)n | (uint64_t)d) >> 32 == 0 ? (int64_t)((uint32_t)n / (uint32_t)d) : n / d;
-}
-// run w takes units [start(w), start(w + 1))
-__device__ __forceinline__ int64_t run_start(const Plan& p, int w) { return quotient(p.units * w, p.runs); }
 struct Item {
   int b, h, tile;
-  uint32_t steps, step;  // of the item; the unit's step in it
+  uint32_t steps, step;  // of the item; where the unit is in it
+  int64_t i0;            // its first unit
 };
 __device__ __forceinline__ Item item_of(const KvAttnArgs& a, const PlanLds& l, int64_t u) {
   const KvArgs& c = a.c;
@@ -704,11 +716,13 @@ __device__ __forceinline__ Item item_of(const KvAttnArgs& a, const PlanLds& l, i
   lo = uniform(lo);
   it.b = lo;
   it.steps = (uint32_t)uniform((int)steps_of(c, l.len[lo]));
-  const uint32_t per = a.cut ? it.steps : 1;
-  const int64_t in = u - l.pre[lo] * c.H;
-  const int64_t item = quotient(in, per);
-  it.step = (uint32_t)uniform((int)(in - item * per));
-  const int64_t tiles = quotient(l.pre[lo + 1] - l.pre[lo], per);
+  const uint32_t units = units_of(a, it.steps);
+  const int64_t first = l.pre[lo] * c.H;
+  const int64_t item = quotient(u - first, units);
+  it.i0 = first + item * units;
+  const int64_t in = u - it.i0;
+  it.step = a.cut && in > a.fixed ? (uint32_t)uniform((int)(in - a.fixed)) : 0u;
+  const int64_t tiles = quotient(l.pre[lo + 1] - l.pre[lo], units);
   it.h = uniform((int)quotient(item, tiles));
   it.tile = uniform((int)(item - it.h * tiles));
   return it;
@@ -723,18 +737,18 @@ __device__ __forceinline__ Seq seq_of(const KvAttnArgs& a, const PlanLds& l, int
   s.table = a.c.table + b * a.c.table_stride;
   return s;
 }
-
 // A run's share of an item, and where its part goes
 struct Run {
   Item it;
-  uint32_t n;    // steps of it
+  uint32_t n;    // steps of it: 0 behind the run's last
   bool whole;
   int64_t slot;  // first row of its part in the workspace
 };
 __device__ __forceinline__ Run next_run(const KvAttnArgs& a, const PlanLds& l, int64_t u, int64_t end, int part, int krows) {
   Run r;
   r.it = item_of(a, l, u);
-  r.n = a.cut ? (uint32_t)uniform((int)min((int64_t)(r.it.steps - r.it.step), end - u)) : r.it.steps;
+  const int64_t to = a.cut ? min(max(end - r.it.i0 - a.fixed, (int64_t)0), (int64_t)r.it.steps) : (int64_t)r.it.steps;
+  r.n = (uint32_t)uniform((int)max(to - (int64_t)r.it.step, (int64_t)0));
   r.whole = r.n == r.it.steps;
   r.slot = ((int64_t)blockIdx.x * 2 + part) * krows;
   return r;
@@ -742,16 +756,15 @@ __device__ __forceinline__ Run next_run(const KvAttnArgs& a, const PlanLds& l, i
 // What k_kv_join needs of the item that run w begins inside, if it is the first run to do so
 // (parts = 0 otherwise): it stands for the item.
 __device__ __forceinline__ void tell_join(const KvAttnArgs& a, const Plan& p, const PlanLds& l, int w) {
-  if (threadIdx.x != 0 || a.joins == nullptr) return;
+  if (threadIdx.x != 0) return;
   KvJoin d{};
   if (w > 0 && w < p.runs) {
-    const int64_t u = run_start(p, w);
-    const Item it = item_of(a, l, u);
-    const int64_t i0 = u - it.step, i1 = i0 + it.steps, start = run_start(p, w - 1);
-    if (it.step > 0 && start <= i0) {
-      const int last = (int)quotient(i1 * p.runs - 1, p.units);  // the last run that begins before i1
+    const Item it = item_of(a, l, w * p.per);
+    const int64_t before = (w - 1) * p.per;
+    if (it.step > 0 && before <= it.i0 + a.fixed) {
+      const int last = (int)quotient(it.i0 + a.fixed + it.steps - 1, p.per);  // the last run that begins in it
       d.parts = last - w + 2;
-      d.first_slot = 2 * (w - 1) + (start < i0 ? 1 : 0);  // its second part if the item begins inside it
+      d.first_slot = 2 * (w - 1) + (before < it.i0 ? 1 : 0);  // its second part if the item begins inside it
       d.h = it.h;
       d.tile = it.tile;
       d.row0 = l.row0[it.b];
@@ -773,18 +786,20 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs64(KvAt
   const Plan plan = make_plan<kRows>(a, plan_lds);
   if (a.cut) tell_join(a, plan, plan_lds, blockIdx.x);
   if ((int)blockIdx.x >= plan.runs) return;
-  int64_t u = run_start(plan, blockIdx.x);
-  const int64_t end = run_start(plan, blockIdx.x + 1);
+  int64_t u = blockIdx.x * plan.per;
+  const int64_t end = min(u + plan.per, plan.units);
   for (int part = 0; u < end; part = 1) {
     const Run r = next_run(a, plan_lds, u, end, part, kRows);
-    u += a.cut ? r.n : 1;
+    if (r.n == 0) break;
+    u = r.it.i0 + units_of(a, r.it.steps);
     const Seq s = seq_of(a, plan_lds, r.it.b);
     const int64_t t0 = (int64_t)r.it.tile * kRows, r0 = t0 + wv * 16;
     auto steps_to = [&](int64_t row) {
       return (uint32_t)__builtin_amdgcn_readfirstlane((int)((limit_of(a, s, (int)(row / a.R)) + kTokTile - 1) / kTokTile));
     };
     Rows<D, I8, 1> w;
-    w.begin(a, s, r.it.h, r0, j, g);
+    w.limits(a, s, r0, j);
+    w.load_q(a, s, r.it.h, r0, j, g);
     W::run(w, a, s, r.it.h, r.it.step, min(r.it.step + r.n, steps_to(min(t0 + kRows, s.nrows) - 1)),
            r0 < s.nrows ? steps_to(min(r0 + 16, s.nrows) - 1) : 0, smem, wv, lane);
     if (r.whole) {
@@ -811,18 +826,18 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs16(KvAt
   const Plan plan = make_plan<kRows>(a, plan_lds);
   if (a.cut) tell_join(a, plan, plan_lds, blockIdx.x);
   if ((int)blockIdx.x >= plan.runs) return;
-  int64_t u = run_start(plan, blockIdx.x);
-  const int64_t end = run_start(plan, blockIdx.x + 1);
+  int64_t u = blockIdx.x * plan.per;
+  const int64_t end = min(u + plan.per, plan.units);
   for (int part = 0; u < end; part = 1) {
     const Run r = next_run(a, plan_lds, u, end, part, kRows);
-    u += a.cut ? r.n : 1;
+    if (r.n == 0) break;
+    u = r.it.i0 + units_of(a, r.it.steps);
     const Seq s = seq_of(a, plan_lds, r.it.b);
     const int64_t r0 = (int64_t)r.it.tile * kRows;
     const uint32_t most = __builtin_amdgcn_readfirstlane(
         (int)((limit_of(a, s, (int)((min(r0 + kRows, s.nrows) - 1) / a.R)) + kTokTile - 1) / kTokTile));
     Rows<D, I8, 1> w;
-    w.begin(a, s, r.it.h, r0, j, g);
-    w.run(a, s, r.it.h, r.it.step + wv, min(r.it.step + r.n, most), kAttnWaves, j, g);
+    w.run(a, s, r.it.h, r0, r.it.step + wv, min(r.it.step + r.n, most), kAttnWaves, j, g);
     const float l = groups_sum(w.sum[0]);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) *reinterpret_cast<v4f*>(&o_lds[wv][j][16 * i + 4 * g]) = w.o[0][i];
@@ -831,8 +846,10 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs16(KvAt
       l_lds[wv][j] = l;
     }
     __syncthreads();
-    // join the waves: 16 threads a row, four elements at a time
-    const int row = threadIdx.x >> 4, q4 = (threadIdx.x & 15) * 4;
+    // join the waves: 16 threads a row, D / 16 elements each
+    constexpr int E = D / 16;
+    typedef float vE __attribute__((ext_vector_type(E)));
+    const int row = threadIdx.x >> 4, q4 = (threadIdx.x & 15) * E;
     const int64_t rr = r0 + row;
     if (rr < s.nrows) {
       float M = m_lds[0][row];
@@ -847,18 +864,17 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs16(KvAt
       }
       const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
       const int i = (int)rr / a.R, head = r.it.h * a.R + (int)rr % a.R;
+      vE v = 0.0f;
 #pragma unroll
-      for (int d = 0; d < D / 64; ++d) {
-        v4f v{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int x = 0; x < kAttnWaves; ++x) v += wgt[x] * *reinterpret_cast<const vE*>(&o_lds[x][row][q4]);
+      if (r.whole) {
+        v *= inv;
+        uint16_t* out = a.out + (s.row0 + i) * a.ldo + (int64_t)head * D + q4;
 #pragma unroll
-        for (int x = 0; x < kAttnWaves; ++x) v += wgt[x] * *reinterpret_cast<const v4f*>(&o_lds[x][row][64 * d + q4]);
-        if (r.whole) {
-          v *= inv;
-          *reinterpret_cast<v2u*>(a.out + (s.row0 + i) * a.ldo + (int64_t)head * D + 64 * d + q4) =
-              v2u{f32_to_bf16_nan(v[0]) | f32_to_bf16_nan(v[1]) << 16, f32_to_bf16_nan(v[2]) | f32_to_bf16_nan(v[3]) << 16};
-        } else {
-          *reinterpret_cast<v4f*>(a.part + (r.slot + row) * D + 64 * d + q4) = v;
-        }
+        for (int e = 0; e < E; e += 2)
+          *reinterpret_cast<uint32_t*>(out + e) = f32_to_bf16_nan(v[e]) | f32_to_bf16_nan(v[e + 1]) << 16;
+      } else {
+        *reinterpret_cast<vE*>(a.part + (r.slot + row) * D + q4) = v;
       }
       if (q4 == 0) {
         if (!r.whole) a.stat[r.slot + row] = float2{M, L};
@@ -963,7 +979,7 @@ constexpr size_t kJoinBytes = 64u << 20;
 // How a call runs: row tiles of `rows` rows, whole (many rows), or in equal runs of the work.
 struct Shape {
   bool whole;
-  int rows, runs, least, cut;
+  int rows, runs, least, cut, fixed;
   bool wide_join;
 };
 
@@ -986,11 +1002,12 @@ Shape shape_of(const KvArgs& c, int R, int num_cu) {
   // a sequence of few steps is not worth cutting: a run is an item then
   s.cut = cap > (s.rows == 16 ? 4 * kAttnWaves : 8);
   s.least = !s.cut ? 1 : s.rows == 16 ? 2 * kAttnWaves : 4;
+  s.fixed = s.rows == 16 ? 2 * kAttnWaves : 4;
   const int most = (int)min((int64_t)min(kMaxRuns, 2 * num_cu), (int64_t)(kJoinBytes / ((size_t)2 * s.rows * (c.D * 4 + 8) + sizeof(KvJoin))));
   if (!s.cut) {
     s.runs = (int)min(items, (int64_t)1 << 30);
   } else {
-    s.runs = (int)min((int64_t)most, (items * cap + s.least - 1) / s.least);
+    s.runs = (int)min((int64_t)most, (items * (cap + s.fixed) + s.least - 1) / s.least);
     s.wide_join = items * 8 < s.runs;  // many parts to an item
   }
   return s;
@@ -1017,7 +1034,8 @@ hipError_t attention_of(KvAttnArgs a, const Shape& s, hipStream_t st) {
     a.c.table = all.c.table + b * all.c.table_stride;
     if (s.rows == 16) {
       // (a head of 256 elements does not fit the registers that leave two waves to a SIMD)
-      if constexpr (D < 256) hipLaunchKernelGGL((k_kv_attention_runs16<D, I8>), dim3((unsigned)s.runs), block, 0, st, a);
+      if constexpr (D < 256)
+        hipLaunchKernelGGL((k_kv_attention_runs16<D, I8>), dim3((unsigned)s.runs), dim3(64 * kAttnWaves), 0, st, a);
     } else {
       constexpr int lds = SharedRows<D, I8, 1, S>::kBytes;
       hipError_t e = set_lds_limit(reinterpret_cast<const void*>(k_kv_attention_runs64<D, I8, S>), lds);
@@ -1052,6 +1070,7 @@ hipError_t launch_kv_attention(KvAttnArgs a, bool i8, int num_cu, void* ws, hipS
   a.runs = s.runs;
   a.least = s.least;
   a.cut = s.cut;
+  a.fixed = s.fixed;
   a.tile_rows = s.rows;
   if (s.cut) {
     const size_t slots = (size_t)2 * s.runs * s.rows;

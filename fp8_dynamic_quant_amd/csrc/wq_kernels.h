@@ -165,9 +165,9 @@ struct KvAttnArgs {
   int R;                    // query heads of each cache head
   int causal;
   // set by the launcher: workgroups that share the work, its least share in steps, whether items
-  // are cut, the rows of a tile, and for items that are cut the parts' unnormalised sums
+  // are cut, the steps that an item counts besides its own, the rows of a tile, and for items that are cut the parts' unnormalised sums
   // [runs][2][tile_rows][D], running maxima (log2) and sums [runs][2][tile_rows], and [runs] joins
-  int runs, least, cut, tile_rows;
+  int runs, least, cut, fixed, tile_rows;
   float* part;
   float2* stat;
   KvJoin* joins;

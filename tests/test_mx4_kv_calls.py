@@ -234,3 +234,66 @@ def test_offsets_that_hold_anything_stay_in_bounds(seed):
         assert 0 <= b < B
         for r in range(j * tile, min((j + 1) * tile, rows * R)):
             assert r >= 0 and 0 <= row0 + r // R < T
+
+
+# ---- equal runs of attention's work, restated -----------------------------------------------------
+
+
+def attention_runs(ns, lens, heads, R, krows, most, least, fixed, cut, capacity):
+    """What each workgroup computes, and which parts each join adds: {item: [(step, n, slot)]},
+    {item: [slot]}."""
+    steps = [max(-(-min(max(x, 0), capacity) // 64), 1) for x in lens]
+    units_of = lambda s: s + fixed if cut else 1  # noqa: E731
+    pre = np.concatenate(([0], np.cumsum([-(-n * R // krows) * units_of(s) for n, s in zip(ns, steps)]))).tolist()
+    units = pre[-1] * heads
+    per = max(-(-units // most), least)
+    runs = -(-units // per)
+
+    def item_of(u):
+        b = max(i for i in range(len(ns)) if pre[i] * heads <= u)
+        n = units_of(steps[b])
+        item = (u - pre[b] * heads) // n
+        i0 = pre[b] * heads + item * n
+        tiles = (pre[b + 1] - pre[b]) // n
+        return (b, item // tiles, item % tiles), steps[b], (max(u - i0 - fixed, 0) if cut else 0), i0
+
+    done, joins = {}, {}
+    for w in range(runs):
+        u, end, part = w * per, min((w + 1) * per, units), 0
+        while u < end:
+            it, s, step, i0 = item_of(u)
+            n = (min(max(end - i0 - fixed, 0), s) if cut else s) - step
+            if n <= 0:
+                break
+            done.setdefault(it, []).append((step, n, 2 * w + min(part, 1)))
+            u, part = i0 + units_of(s), part + 1
+        if cut and w > 0:
+            it, s, step, i0 = item_of(w * per)
+            before = (w - 1) * per
+            if step > 0 and before <= i0 + fixed:
+                last = (i0 + fixed + s - 1) // per
+                joins[it] = [2 * (w - 1) + (before < i0)] + [2 * (w - 1 + p) for p in range(1, last - w + 2)]
+    assert runs <= most
+    return done, joins
+
+
+@pytest.mark.parametrize("seed", range(80))
+def test_runs_cover_every_item_once(seed):
+    g = np.random.default_rng(300 + seed)
+    B, heads, R, krows = int(g.integers(1, 10)), int(g.integers(1, 6)), int(g.choice([1, 4, 5, 16])), int(g.choice([16, 64]))
+    ns = (g.integers(0, 20, B) * (g.random(B) < 0.8)).tolist()
+    if sum(ns) == 0:
+        ns[0] = 1
+    lens, cut = g.integers(-3, 4000, B).tolist(), bool(g.random() < 0.8)
+    tiles = sum(-(-n * R // krows) for n in ns)
+    most = int(g.integers(1, 200)) if cut else tiles * heads
+    done, joins = attention_runs(ns, lens, heads, R, krows, most, int(g.choice([4, 8])) if cut else 1, int(g.choice([0, 4, 8])), cut,
+                                 int(g.choice([64, 1000, 10000])))
+    assert len(done) == tiles * heads
+    for it, parts in done.items():
+        at = 0
+        for step, n, _ in parts:
+            assert step == at
+            at += n
+        assert len(parts) == 1 or joins.pop(it) == [slot for _, _, slot in parts]
+    assert not joins
