@@ -179,9 +179,10 @@ __device__ __forceinline__ v8bf widen8(uint32_t lo, uint32_t hi, float scale) {
   return __builtin_bit_cast(v8bf, o);
 }
 
-// 2^(byte - 127); byte 255 is NaN, byte 0 the subnormal 2^-127
+// 2^(byte - 127), byte 0 the subnormal 2^-127; byte 255 is NaN
 __device__ __forceinline__ float scale_of(uint32_t byte) {
-  return byte == 255u ? __uint_as_float(0x7FC00000u) : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+  const float f = ldexpf(1.0f, (int)byte - 127);
+  return byte == 255u ? __uint_as_float(0x7FC00000u) : f;
 }
 
 // max / sum over the four lane groups that share a row (lanes j, j + 16, j + 32, j + 48): the swaps
@@ -430,15 +431,16 @@ struct Rows {
 // sixteen rows that are read at one chunk meet sixteen different bank groups: a key read takes
 // tokens 16 a + 4 t + b (a, b = 0 .. 3), a value read sixteen consecutive rows of 64 bytes.
 // Wave w sends the keys of token group w, and of the values every fourth run of 16 rows; page
-// numbers are read through the scalar cache, so that no vector load but the DMA is in flight and
-// its count tells when a step has landed.
+// numbers come by DMA too, so that no other vector load is in flight and the count of DMAs tells
+// when a step has landed.
 template <int D, bool I8, int RT, int S>
 struct SharedRows {
   using R = Rows<D, I8, RT>;
   static constexpr int ND = D / 16, NC = D / 64;
   static constexpr int kTile = 64 * D, kStage = 2 * kTile + 256;  // keys, values, scale bytes (a word each)
-  static constexpr int kDma = 2 * NC + 1;
-  static constexpr int kBytes = S * kStage;
+  static constexpr int kDma = 2 * NC + 2;
+  static constexpr int kPages = S * kStage;  // page numbers of eight steps, a word a lane
+  static constexpr int kBytes = kPages + 8 * 256;
   static __device__ __forceinline__ int k_swz(int token) {
     return NC == 1 ? (token >> 4) & 3 : NC == 2 ? ((token >> 4) & 3) * 2 + ((token >> 1) & 1) : ((token >> 4) & 3) * 4 + (token & 3);
   }
@@ -456,63 +458,68 @@ struct SharedRows {
     const uint32_t page_bytes = (uint32_t)c.P * D;
     const uint8_t* K = static_cast<const uint8_t*>(c.k) + (uint32_t)h * page_bytes;
     const uint8_t* V = static_cast<const uint8_t*>(c.v) + (uint32_t)h * page_bytes;
-    const int64_t page_step = (int64_t)H * page_bytes;
+    const uint32_t page_step = H * page_bytes;  // < 2^32: 65535 heads of 256 x 256
     const uint32_t first = __builtin_amdgcn_readfirstlane((int)w.limit[0]);
-    const auto* table = (const __attribute__((address_space(4))) int32_t*)s.table;
-    // page of token group lane % 4 of a step, -1 where there is none
-    auto page_of = [&](uint32_t tg) __attribute__((always_inline)) -> int {
-      const bool in = 16 * tg < s.seen;
-      const int n = uniform(table[in ? by_page(tg, recip, one) : 0u]);
-      return in && (uint32_t)n < (uint32_t)c.pages ? n : -1;
-    };
-    auto pages_of = [&](uint32_t step) __attribute__((always_inline)) -> int {
-      const int p0 = page_of(4 * step), p1 = page_of(4 * step + 1), p2 = page_of(4 * step + 2), p3 = page_of(4 * step + 3);
-      const int lo2 = lane & 1 ? p1 : p0, hi2 = lane & 1 ? p3 : p2;
-      return lane & 2 ? hi2 : lo2;
-    };
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_u8)smem;
-    // this lane's places: keys, position wv * NC * 64 + lane of the tile is (token, chunk); values,
-    // row wv * 16 + lane / 4 (then 64 rows on), chunk lane % 4
-    const int vg = (lane & 3) ^ ((lane >> 4) & 3);  // the token group of the lane's value chunk
+    // This lane's places.  Keys: position wv * NC * 64 + lane of the tile is (token, chunk).  Values:
+    // row wv * 16 + lane / 4 (then 64 rows on), chunk lane % 4, which holds token group vg.  Page
+    // numbers are held for token group vg (lanes 0 .. 3: groups 0 .. 3).
+    const uint32_t vg = (uint32_t)((lane & 3) ^ ((lane >> 4) & 3));
+    auto entry = [&](uint32_t step) __attribute__((always_inline)) {  // of the table; past the end the first
+      const uint32_t tg = 4 * step + vg;
+      return s.table + (16 * tg < s.seen ? by_page(tg, recip, one) : 0u);
+    };
+    // page of token group vg of a step, -1 where there is none
+    auto checked = [&](uint32_t step, int page) __attribute__((always_inline)) {
+      return 16 * (4 * step + vg) < s.seen && (uint32_t)page < (uint32_t)c.pages ? page : -1;
+    };
+    auto slot_of = [&](uint32_t tg) __attribute__((always_inline)) { return (tg - by_page(tg, recip, one) * per) * 16; };
+    uint32_t koff[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int pos = (wv * NC + i) * 64 + lane, tok = pos / (D / 16), ch = (pos % (D / 16)) ^ k_swz(tok);
+      koff[i] = (uint32_t)((tok & 15) * D + ch * 16);
+    }
+    const uint8_t* vrow = V + (uint32_t)(wv * 16 + (lane >> 2)) * c.P;
+    const uint8_t* scales = (lane & 4 ? c.v_scale : c.k_scale) + h;
     auto issue = [&](uint32_t step, int page, int stage) __attribute__((always_inline)) {
       const uint32_t st = lds0 + stage * kStage;
-      auto slot_of = [&](uint32_t x) {
-        const uint32_t tg = 4 * step + x;
-        return (tg - by_page(tg, recip, one) * per) * 16;
-      };
-      const int held = max(page, 0);  // a group without a page reads page 0 and is masked
-      const uint8_t* kb = K + __builtin_amdgcn_readlane(held, wv) * page_step + slot_of(wv) * D;
+      const uint32_t held = (uint32_t)max(page, 0);  // a group without a page reads page 0 and is masked
+      const uint8_t* kb = K + (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)held, wv) * page_step + slot_of(4 * step + wv) * D;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int pos = (wv * NC + i) * 64 + lane, tok = pos / (D / 16), ch = (pos % (D / 16)) ^ k_swz(tok);
-        dma16_at(kb + ((tok & 15) * D + ch * 16), st + (wv * NC + i) * 1024);
-      }
-      // the page of token group (lane % 4) ^ (lane / 16): the quads of row r of 16 lanes swapped by r
-      int vp = held;
-      vp = __builtin_amdgcn_update_dpp(vp, held, 0xB1, 0x2, 0xF, false);
-      vp = __builtin_amdgcn_update_dpp(vp, held, 0x4E, 0x4, 0xF, false);
-      vp = __builtin_amdgcn_update_dpp(vp, held, 0x1B, 0x8, 0xF, false);
-      const uint8_t* vb = V + vp * page_step + (uint32_t)(wv * 16 + (lane >> 2)) * c.P + slot_of(vg);
+      for (int i = 0; i < NC; ++i) dma16_at(kb + koff[i], st + (wv * NC + i) * 1024);
+      const uint8_t* vb = vrow + (uint64_t)held * page_step + slot_of(4 * step + vg);
 #pragma unroll
-      for (int i = 0; i < NC; ++i) dma16_at(vb + (int64_t)(64 * i) * c.P, st + kTile + (wv + 4 * i) * 1024);
+      for (int i = 0; i < NC; ++i) dma16_at(vb + (uint32_t)(64 * i * c.P), st + kTile + (wv + 4 * i) * 1024);
       // scale bytes: word x of the stage's last 256 bytes is the keys' of token group x, word 4 + x
       // the values' (each wave writes the same)
-      dma1_at((lane & 4 ? c.v_scale : c.k_scale) + (int64_t)held * H + h, st + 2 * kTile);
+      dma1_at(scales + (uint64_t)held * H, st + 2 * kTile);
+    };
+    auto send_page = [&](uint32_t step) __attribute__((always_inline)) {
+      dma4_at(entry(min(step, hi - 1)), lds0 + kPages + (step & 7) * 256);
     };
     static_assert(S == 2 || S == 3, "page numbers of three steps");
-    int p0 = pages_of(lo), p1 = pages_of(min(lo + 1, hi - 1)), p2 = S == 3 ? pages_of(min(lo + 2, hi - 1)) : 0;
+    // p0, p1(, p2): pages of this step and the next; step + S - 1's are read when its data are sent,
+    // two steps after they were sent for themselves
+    int p0 = checked(lo, *entry(lo)), p1 = checked(lo + 1, *entry(min(lo + 1, hi - 1)));
+    int p2 = S == 3 ? checked(lo + 2, *entry(min(lo + 2, hi - 1))) : 0;
+    send_page(lo + S);
     issue(lo, p0, 0);
     if (S == 3 && lo + 1 < hi) issue(lo + 1, p1, 1);
     int stage = 0;
     for (uint32_t step = lo; step < hi; ++step) {
-      if (S > 2 && step + S - 2 < hi) wait_vm<kDma*(S - 2)>();
+      if (S > 2 && step + S - 2 < hi && step > lo) wait_vm<kDma*(S - 2)>();
       else wait_vm<0>();
       lds_barrier();  // the step has landed for all, and the one before it has been read by all
+      if (step > lo) {
+        const int got = *reinterpret_cast<const int*>(smem + kPages + ((step + S - 1) & 7) * 256 + lane * 4);
+        (S == 3 ? p2 : p1) = checked(step + S - 1, got);
+      }
+      send_page(step + S + 1);
       if (step + S - 1 < hi) issue(step + S - 1, S == 3 ? p2 : p1, stage == 0 ? S - 1 : stage - 1);
       const uint32_t none = (uint32_t)__ballot(p0 < 0) & 15u;
       p0 = p1;
       if (S == 3) p1 = p2;
-      (S == 3 ? p2 : p1) = pages_of(min(step + S, hi - 1));
       const uint8_t* sk = smem + stage * kStage;
       const uint8_t* sv = sk + kTile;
       const uint32_t* sb = reinterpret_cast<const uint32_t*>(sv + kTile);
@@ -572,6 +579,7 @@ struct SharedRows {
       if (tok0 + kTokTile <= first && none == 0 && __all(vbyte != 255u)) finish(std::false_type{});
       else finish(std::true_type{});
     }
+    wait_vm<0>();   // no page number is still on its way
     lds_barrier();  // the ring may be filled again
   }
 };

@@ -27,7 +27,7 @@ typedef __attribute__((address_space(3))) uint8_t* lds_ptr_u8;
 
 // One DMA instruction of 64 lanes to LDS byte address `la` on, 16 bytes a lane (dma16), a dword
 // (dma4) or a byte widened to a dword (dma1_at), from a wave-uniform base and a lane offset or
-// from an address a lane.  Written out, with its LDS address in M0: given the builtin, the
+// (.._at) from an address a lane.  Written out, with its LDS address in M0: given the builtin, the
 // compiler lets LDS reads that it cannot tell from the target wait for every DMA in flight.  The
 // kernels order them themselves (vmcnt, then a barrier).  Nothing is loaded into registers.  Six
 // wait states stand in front of the load: a base just written by the VALU needs five, M0 one.
@@ -41,6 +41,9 @@ __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t la
 }
 __device__ __forceinline__ void dma16_at(const void* at, uint32_t la) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at), "s"(la) : "memory", "m0");
+}
+__device__ __forceinline__ void dma4_at(const void* at, uint32_t la) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dword %0, off" ::"v"(at), "s"(la) : "memory", "m0");
 }
 __device__ __forceinline__ void dma1_at(const void* at, uint32_t la) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_ubyte %0, off" ::"v"(at), "s"(la) : "memory", "m0");
