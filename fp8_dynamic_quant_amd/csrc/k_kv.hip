@@ -249,6 +249,11 @@ __device__ __forceinline__ v4u keep_bytes(v4u v, int n) {  // the first n bytes,
   return v;
 }
 
+// |scale| log2(e), with which scores become powers of two (1 for a zero scale, at which q is zero)
+__device__ __forceinline__ float log2_scale(const KvAttnArgs& a) {
+  return a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.44269504088896340736f;
+}
+
 // RT row tiles of a wave over steps [lo, hi) with stride TW, keys and values straight from memory
 // in operand order.  The next step's keys load as soon as this one's scores are made, its values as
 // soon as this one's are used, so that each has a whole step's time; page numbers load two ahead.
@@ -272,7 +277,8 @@ struct Rows {
     }
   }
   __device__ __forceinline__ void load_q(const KvAttnArgs& a, const Seq& s, int h, int64_t r0, int j, int g) {
-    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;  // the sign goes into q: scores scale by |scale|
+    // the sign goes into q, and a zero, so that scores scale by a positive number (log2_scale)
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, keep = a.scale == 0.0f ? 0u : ~0u;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int rc = (int)min(r0 + 16 * rt + j, s.nrows - 1);
@@ -281,26 +287,33 @@ struct Rows {
       for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
         for (int m = 0; m < 2; ++m)
-          qf[rt][cc][m] = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(q + 64 * cc + 8 * m) ^ flip);
+          qf[rt][cc][m] = __builtin_bit_cast(v8bf, (*reinterpret_cast<const v4u*>(q + 64 * cc + 8 * m) ^ flip) & keep);
     }
   }
 
-  // scores of the lane's 16 tokens from gt on -> weights, the running maximum and sum
-  template <bool MASK>
-  __device__ __forceinline__ void weights(v4f (&sc)[RT][4], v8bf (&pf)[RT][2], float ks, float vs, bool there, uint32_t gt) {
+  // Scores of the lane's 16 tokens from gt on that a row does not see become -inf; of a page marked
+  // NaN (bad) those it sees become NaN, and the caller's scales one.
+  __device__ __forceinline__ void hide(v4f (&sc)[RT][4], bool there, bool bad, uint32_t gt) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int left = there ? (int)min(limit[rt], 0x7FFFFFFFu) - (int)min(gt, 0x7FFFFFFFu) : 0;  // tokens from gt on that the row sees
+      const int left = there ? (int)min(limit[rt], 0x7FFFFFFFu) - (int)min(gt, 0x7FFFFFFFu) : 0;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          sc[rt][t][r] = 4 * t + r >= left ? -INFINITY : bad ? __uint_as_float(0x7FC00000u) : sc[rt][t][r];
+    }
+  }
+  // scores -> weights, the running maximum and sum
+  __device__ __forceinline__ void weights(v4f (&sc)[RT][4], v8bf (&pf)[RT][2], float ks, float vs) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
       float top = -INFINITY;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (MASK) sc[rt][t][r] = 4 * t + r < left ? sc[rt][t][r] * ks : -INFINITY;
-          top = fmaxf(top, sc[rt][t][r]);
-        }
-      if constexpr (!MASK) top *= ks;
-      top = groups_max(top);
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[rt][t][r]);
+      top = groups_max(top * ks);
       if (__any(top > mx[rt])) {
         const float mn = fmaxf(mx[rt], top);
         const float alpha = __builtin_amdgcn_exp2f(mx[rt] - (mn == -INFINITY ? 0.0f : mn));
@@ -314,14 +327,10 @@ struct Rows {
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float e = __builtin_amdgcn_exp2f(MASK ? sc[rt][t][r] - base : __builtin_fmaf(sc[rt][t][r], ks, -base));
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[rt][t][r], ks, -base));
           sum[rt] += e;
-          // rounded to bf16, with an int8 page's scale on it (a power of two: no further
-          // rounding); a masked token's weight is zero whatever its page's scale holds
-          float w = e;
-          if constexpr (MASK) w = sc[rt][t][r] == -INFINITY ? 0.0f : e * vs;
-          else if constexpr (I8) w = e * vs;
-          pf[rt][t >> 1][(t & 1) * 4 + r] = (__bf16)w;
+          // rounded to bf16, with an int8 page's scale on it (a power of two: no further rounding)
+          pf[rt][t >> 1][(t & 1) * 4 + r] = (__bf16)(I8 ? e * vs : e);
         }
     }
   }
@@ -333,12 +342,13 @@ struct Rows {
     auto begin_rows = [&]() __attribute__((always_inline)) { load_q(a, s, h, r0, j, g); };
     const KvArgs& c = a.c;
     const uint32_t per = (uint32_t)c.P >> 4, recip = c.page_recip, one = per == 1 ? ~0u : 0u, H = (uint32_t)c.H;
-    const float to_log2 = fabsf(a.scale) * 1.44269504088896340736f;
+    const float to_log2 = log2_scale(a);
     const uint32_t page_bytes = (uint32_t)c.P * D;
     const uint8_t* K = static_cast<const uint8_t*>(c.k) + (uint32_t)h * page_bytes;
     const uint8_t* V = static_cast<const uint8_t*>(c.v) + (uint32_t)h * page_bytes;
     const int64_t page_step = (int64_t)H * page_bytes;
     const int kg = j >> 2;  // the token group that this lane reads keys of
+    const uint32_t first = __builtin_amdgcn_readfirstlane((int)limit[0]);  // the least of the wave's limits
     struct Page {
       uint32_t at, slot;
       bool there;
@@ -393,7 +403,7 @@ struct Rows {
             for (int rt = 0; rt < RT; ++rt) sc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[rt][cc][m], sc[rt][t], 0, 0, 0);
           }
       }
-      const float ks = scale_of(kb) * to_log2;
+      const uint32_t kbyte = kb;
       // ---- the next step's keys
       const Page npv = place(nstep, g, nv);
       load_k(place(nstep, kg, nk));
@@ -402,22 +412,22 @@ struct Rows {
       nk = number(nstep, kg);
       nv = number(nstep, g);
       // ---- weights and values
-      const float vs = scale_of(vb);
-      // (always masked: a second copy of this code without the masks is slower to fetch than it saves)
+      const bool tail = tok0 + kTokTile > s.seen || !__all(pv.there), bad = kbyte == 255u || vb == 255u;
+      if (tail || tok0 + kTokTile > first || __any(bad)) hide(sc, pv.there, bad, gt);
+      const float ks = bad || !pv.there ? 1.0f : scale_of(kbyte) * to_log2, vs = bad || !pv.there ? 1.0f : scale_of(vb);
       v8bf pf[RT][2];
-      weights<true>(sc, pf, ks, vs, pv.there, gt);
-      if (tok0 + kTokTile > s.seen || !__all(pv.there)) {
+      weights(sc, pf, ks, vs);
 #pragma unroll
-        for (int i = 0; i < ND; ++i) vv[i] = keep_bytes(vv[i], there_slots(s, pv.there, gt));
-      }
-#pragma unroll
-      for (int i = 0; i < ND; ++i)
+      for (int i = 0; i < ND; ++i) {
+        // E4M3 codes behind the sequence's end may be NaN (an int8 times a zero weight is zero)
+        if (!I8 && tail) vv[i] = keep_bytes(vv[i], there_slots(s, pv.there, gt));
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          const v8bf vf = widen8<I8>(vv[i][2 * m], vv[i][2 * m + 1], 1.0f);
+          const v8bf vf = widen8<I8>(vv[i][2 * m], vv[i][2 * m + 1], vs);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) o[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][m], o[rt][i], 0, 0, 0);
         }
+      }
       // ---- the next step's values
       pv = npv;
       load_v(pv);
@@ -454,7 +464,7 @@ struct SharedRows {
     const KvArgs& c = a.c;
     const int j = lane & 15, g = lane >> 4;
     const uint32_t per = (uint32_t)c.P >> 4, recip = c.page_recip, one = per == 1 ? ~0u : 0u, H = (uint32_t)c.H;
-    const float to_log2 = fabsf(a.scale) * 1.44269504088896340736f;
+    const float to_log2 = log2_scale(a);
     const uint32_t page_bytes = (uint32_t)c.P * D;
     const uint8_t* K = static_cast<const uint8_t*>(c.k) + (uint32_t)h * page_bytes;
     const uint8_t* V = static_cast<const uint8_t*>(c.v) + (uint32_t)h * page_bytes;
@@ -525,8 +535,7 @@ struct SharedRows {
       const uint32_t* sb = reinterpret_cast<const uint32_t*>(sv + kTile);
       stage = stage + 1 == S ? 0 : stage + 1;
       if (step >= most) continue;  // uniform in the wave
-      // operands are read one ahead of their use; the barriers keep the compiler from reading many
-      // ahead, for which there are no registers
+      // operands are read one ahead of their use
       v4f sc[RT][4];
       auto key = [&](int x) __attribute__((always_inline)) {
         const int tok = 16 * (j >> 2) + 4 * (x / NC) + (j & 3), ch = 4 * (x % NC) + g;
@@ -547,37 +556,31 @@ struct SharedRows {
           for (int rt = 0; rt < RT; ++rt) sc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, w.qf[rt][cc][m], sc[rt][t], 0, 0, 0);
         }
         kk = next;
-        __builtin_amdgcn_sched_barrier(0);
       }
-      const uint32_t vbyte = sb[4 + g];
-      const float ks = scale_of(sb[g]) * to_log2, vs = scale_of(vbyte);
+      const uint32_t kbyte = sb[g], vbyte = sb[4 + g];
       const uint32_t tok0 = step * kTokTile, gt = tok0 + 16 * g;
-      const bool there = !(none >> g & 1u);
-      auto finish = [&](auto masked) __attribute__((always_inline)) {
-        constexpr bool MASK = decltype(masked)::value;
-        v8bf pf[RT][2];
-        auto value = [&](int i) __attribute__((always_inline)) {
-          return *reinterpret_cast<const v4u*>(sv + (16 * i + j) * 64 + ((g ^ v_swz(j)) << 4));
-        };
-        v4u vv = value(0);
-        w.template weights<MASK>(sc, pf, ks, vs, there, gt);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < ND; ++i) {
-          const v4u next = i + 1 < ND ? value(i + 1) : vv;
-          if constexpr (MASK) vv = keep_bytes(vv, there_slots(s, there, gt));
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const v8bf vf = widen8<I8>(vv[2 * m], vv[2 * m + 1], MASK ? 1.0f : vs);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) w.o[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][m], w.o[rt][i], 0, 0, 0);
-          }
-          vv = next;
-          __builtin_amdgcn_sched_barrier(0);
-        }
+      const bool there = !(none >> g & 1u), tail = tok0 + kTokTile > s.seen || none != 0, bad = kbyte == 255u || vbyte == 255u;
+      if (tail || tok0 + kTokTile > first || __any(bad)) w.hide(sc, there, bad, gt);
+      const float ks = bad || !there ? 1.0f : scale_of(kbyte) * to_log2, vs = bad || !there ? 1.0f : scale_of(vbyte);
+      auto value = [&](int i) __attribute__((always_inline)) {
+        return *reinterpret_cast<const v4u*>(sv + (16 * i + j) * 64 + ((g ^ v_swz(j)) << 4));
       };
-      if (tok0 + kTokTile <= first && none == 0 && __all(vbyte != 255u)) finish(std::false_type{});
-      else finish(std::true_type{});
+      v4u vv = value(0);
+      v8bf pf[RT][2];
+      w.weights(sc, pf, ks, vs);
+#pragma unroll
+      for (int i = 0; i < ND; ++i) {
+        const v4u next = i + 1 < ND ? value(i + 1) : vv;
+        // E4M3 codes behind the sequence's end may be NaN (an int8 times a zero weight is zero)
+        if (!I8 && tail) vv = keep_bytes(vv, there_slots(s, there, gt));
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const v8bf vf = widen8<I8>(vv[2 * m], vv[2 * m + 1], vs);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) w.o[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[rt][m], w.o[rt][i], 0, 0, 0);
+        }
+        vv = next;
+      }
     }
     wait_vm<0>();   // no page number is still on its way
     lds_barrier();  // the ring may be filled again
