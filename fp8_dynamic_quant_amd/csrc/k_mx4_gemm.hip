@@ -302,6 +302,201 @@ __global__ __launch_bounds__(256, 2) void k_mx4_tile(Mx4Args p, int tiles_m, int
   }
 }
 
+// ---- many tiles: persistent 256 x 256 ---------------------------------------------------------
+// One workgroup of eight waves (2 x 4, 128 x 64 outputs each) on every CU walks over its tiles; the
+// ring of slices runs on across them, so the next tile's first slices land while this one's outputs
+// are stored.  A slice is KD deep: 256 with 4-bit operands (128-byte rows: whole cache lines), 128
+// with E4M3 activations or an odd number of 128-deep blocks.
+template <bool A8, int KD, int S>
+struct BigRing {
+  static constexpr int kARow = A8 ? KD : KD / 2, kWRow = KD / 2, kBlocks = KD / 128;
+  static constexpr int kA = 256 * kARow, kW = 256 * kWRow, kS = kBlocks * 2048;  // kS: words, [block][256 rows, 256 columns]
+  static constexpr int kStage = kA + kW + kS;
+  static constexpr int kNA = kA / 8192, kNW = kW / 8192, kNS = kBlocks;  // DMAs of a wave
+  static constexpr int kDma = kNA + kNW + kNS;
+  static constexpr int kStores = 16;  // a wave's stores of a whole tile
+  static_assert(kStage >= 8 * 4096, "a stage holds the waves' output blocks");
+};
+
+template <bool A8, int KD, int S>
+__global__ __launch_bounds__(512, 2) void k_mx4_big(Mx4Args p, int tiles_m, int tiles_n, int per_xcd, int wgs_xcd) {
+  using R = BigRing<A8, KD, S>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(t >> 6), wm = wv >> 2, wn = wv & 3;
+  const int M = p.M, N = p.N, KB = p.K >> 7, KT = p.K / KD;  // 128-deep blocks, slices
+  const int per_group = tiles_m * tiles_n, xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
+  const int total = per_group * p.batch, lin_end = min(total, (xcd + 1) * per_xcd);
+  const int lin0 = xcd * per_xcd + local;
+  if (lin0 >= lin_end) return;
+  const int slices = (lin_end - lin0 + wgs_xcd - 1) / wgs_xcd * KT;
+  struct Tile {
+    int g, m0, n0;
+  };
+  auto tile_at = [&](int lin) __attribute__((always_inline)) {  // in bands of eight tile rows
+    const int g = lin / per_group, in_g = lin % per_group;
+    const int band = in_g / (8 * tiles_n), rows8 = min(8, tiles_m - 8 * band), in_b = in_g - band * 8 * tiles_n;
+    return Tile{g, (8 * band + in_b % rows8) * 256, in_b / rows8 * 256};
+  };
+  // lane offsets of this wave's DMA instructions wv, wv + 8, ... (rows are clamped per tile below)
+  auto row_of = [&](int i, int per) { return ((wv + 8 * i) * 64 + lane) / per; };
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_u8)smem;
+  // where slices are sent from: the tile of the next one
+  int s_lin = lin0, s_kt = 0;
+  Tile st = tile_at(lin0);
+  uint32_t aoff[R::kNA], woff[R::kNW];
+  auto offsets = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < R::kNA; ++i) {
+      constexpr int per = R::kARow / 16;
+      const int r = row_of(i, per), c = (lane % per) ^ chunk_swz<R::kARow>(r);
+      aoff[i] = (uint32_t)(min(r, M - 1 - st.m0) * (int)p.lda + c * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < R::kNW; ++i) {
+      constexpr int per = R::kWRow / 16;
+      const int r = row_of(i, per), c = (lane % per) ^ chunk_swz<R::kWRow>(r);
+      woff[i] = (uint32_t)(min(r, N - 1 - st.n0) * (p.K / 2) + c * 16);
+    }
+  };
+  offsets();
+  auto send = [&](int stage) __attribute__((always_inline)) {
+    const uint32_t to = lds0 + stage * R::kStage;
+    const uint8_t* a = p.a + st.g * p.a_batch_stride + (int64_t)st.m0 * p.lda + (int64_t)s_kt * R::kARow;
+    const uint8_t* w = p.w + st.g * p.w_batch_stride + (int64_t)st.n0 * (p.K / 2) + (int64_t)s_kt * R::kWRow;
+#pragma unroll
+    for (int i = 0; i < R::kNA; ++i) dma16(a, aoff[i], to + (wv + 8 * i) * 1024);
+#pragma unroll
+    for (int i = 0; i < R::kNW; ++i) dma16(w, woff[i], to + R::kA + (wv + 8 * i) * 1024);
+    // the words of 64 rows (waves 0 .. 3) or columns (4 .. 7) of each 128-deep block
+    const int r = (wv & 3) * 64 + lane;
+    const uint32_t off = (uint32_t)(wv < 4 ? min(r, M - 1 - st.m0) : min(r, N - 1 - st.n0));
+#pragma unroll
+    for (int b = 0; b < R::kBlocks; ++b) {
+      const int64_t kb = (int64_t)st.g * KB + s_kt * R::kBlocks + b;
+      const int32_t* words = wv < 4 ? p.a_scale + kb * p.a_tokens + st.m0 : p.w_scale + kb * N + st.n0;
+      dma4_at(words + off, to + R::kA + R::kW + b * 2048 + wv * 256);
+    }
+    if (++s_kt == KT) {
+      s_kt = 0;
+      s_lin += wgs_xcd;
+      if (s_lin < lin_end) {
+        st = tile_at(s_lin);
+        offsets();
+      }
+    }
+  };
+
+  v16f acc[4][2];
+  const int l32 = lane & 31, h = lane >> 5;
+  const int ar = wm * 128 + l32, wr = wn * 64 + l32;
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  };
+  auto multiply = [&](int stage) __attribute__((always_inline)) {
+    const uint8_t* sa = smem + stage * R::kStage;
+    const uint8_t* sw = sa + R::kA;
+#pragma unroll
+    for (int b = 0; b < R::kBlocks; ++b) {
+      const uint32_t* ss = reinterpret_cast<const uint32_t*>(sw + R::kW + b * 2048);
+      uint32_t xa[4], xw[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xa[i] = ss[ar + 32 * i] >> (8 * h);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) xw[j] = ss[256 + wr + 32 * j] >> (8 * h);
+      auto step = [&](auto which) __attribute__((always_inline)) {
+        constexpr int s = decltype(which)::value;  // 64-deep half; its scale bytes are 2 s + h
+        v4i al[4], ah[4], wf[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) wf[j] = *reinterpret_cast<const v4i*>(sw + lds_at<R::kWRow>(wr + 32 * j, 4 * b + 2 * s + h));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (A8) {
+            al[i] = *reinterpret_cast<const v4i*>(sa + lds_at<128>(ar + 32 * i, 4 * s + h));
+            ah[i] = *reinterpret_cast<const v4i*>(sa + lds_at<128>(ar + 32 * i, 4 * s + 2 + h));
+          } else {
+            al[i] = *reinterpret_cast<const v4i*>(sa + lds_at<R::kARow>(ar + 32 * i, 4 * b + 2 * s + h));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                regs4(wf[j]), A8 ? regs8(al[i], ah[i]) : regs4(al[i]), acc[i][j], 4, A8 ? 0 : 4, 2 * s, xw[j], 2 * s, xa[i]);
+      };
+      step(std::integral_constant<int, 0>{});
+      step(std::integral_constant<int, 1>{});
+    }
+  };
+
+  clear();
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s)
+    if (s < slices) send(s);
+  int stage = 0, kt = 0, lin = lin0;
+  bool stored = false;  // the last thing done was to store a whole tile
+  for (int sl = 0; sl < slices; ++sl) {
+    // This wave's share of slice sl has landed: S - 2 later ones may be on their way, and the stores
+    // behind them (memory operations end in their order).
+    if (sl + S - 2 >= slices) wait_vm<0>();
+    else if (stored) wait_vm<R::kDma*(S - 2) + R::kStores>();
+    else wait_vm<R::kDma*(S - 2)>();
+    stored = false;
+    lds_barrier();  // everyone's has, and slice sl - 1, or the outputs in its place, has been read by all
+    if (sl + S - 1 < slices) send(stage == 0 ? S - 1 : stage - 1);
+    multiply(stage);
+    if (++kt == KT) {
+      // ---- outputs: bf16, 32 rows of 128 bytes at a time through the wave's 4 KiB of the slice's
+      // stage (16-byte chunks XORed with bits 1..3 of the row), then 16 bytes a lane, whole lines.
+      // They are not read again here: streaming stores leave the L2 to the operands.
+      kt = 0;
+      const Tile o = tile_at(lin);
+      lin += wgs_xcd;
+      lds_barrier();
+      uint8_t* so = smem + stage * R::kStage + wv * 4096;
+      auto out_at = [&](int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); };
+      const int mw = o.m0 + wm * 128, n = o.n0 + wn * 64 + (lane & 7) * 8;
+      uint16_t* Y = p.y + o.g * p.y_batch_stride + n;
+      const bool inside = o.m0 + 256 <= M && o.n0 + 256 <= N;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t w0 = f32_to_bf16_nan(acc[i][j][4 * q]) | f32_to_bf16_nan(acc[i][j][4 * q + 1]) << 16;
+            const uint32_t w1 = f32_to_bf16_nan(acc[i][j][4 * q + 2]) | f32_to_bf16_nan(acc[i][j][4 * q + 3]) << 16;
+            *reinterpret_cast<v2u*>(so + out_at(l32, 4 * j + q) + 8 * h) = v2u{w0, w1};
+          }
+        v4u v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const v4u*>(so + out_at(8 * k + (lane >> 3), lane & 7));
+        if (inside) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            __builtin_nontemporal_store(v[k], reinterpret_cast<v4u*>(Y + (int64_t)(mw + 32 * i + 8 * k + (lane >> 3)) * p.ldy));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int m = mw + 32 * i + 8 * k + (lane >> 3);
+            if (m < M && n < N) *reinterpret_cast<v4u*>(Y + (int64_t)m * p.ldy) = v[k];
+          }
+        }
+      }
+      if (inside) stored = true;
+      else wait_vm<0>();  // their number is not known
+      clear();
+    }
+    stage = stage + 1 == S ? 0 : stage + 1;
+  }
+}
+
 template <bool A8, int RT, int CT>
 hipError_t few(const Mx4Args& a, hipStream_t st) {
   const dim3 grid((unsigned)((a.N + 16 * CT - 1) / (16 * CT)), (unsigned)a.batch);
@@ -333,11 +528,30 @@ hipError_t tile(const Mx4Args& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <bool A8, int KD, int S>
+hipError_t big(const Mx4Args& a, int num_cu, hipStream_t st) {
+  using R = BigRing<A8, KD, S>;
+  const int64_t tm = (a.M + 255) / 256, tn = (a.N + 255) / 256, total = tm * tn * a.batch;
+  if (total * (a.K / KD) >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+  const int per_xcd = (int)((total + 7) / 8), wgs = num_cu / 8;
+  const void* kernel = reinterpret_cast<const void*>(k_mx4_big<A8, KD, S>);
+  hipError_t e = set_lds_limit(kernel, S * R::kStage);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_mx4_big<A8, KD, S>), dim3((unsigned)(8 * wgs)), dim3(512), S * R::kStage, st, a, (int)tm, (int)tn,
+                     per_xcd, wgs);
+  return hipGetLastError();
+}
+
 template <bool A8>
 hipError_t launch(const Mx4Args& a, int num_cu, hipStream_t st) {
   if (a.M <= 64) {
     if ((int64_t)a.N / 32 * a.batch >= num_cu) return few_rows<A8, 2>(a, st);
     return few_rows<A8, 1>(a, st);
+  }
+  const int64_t huge = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256) * a.batch;
+  if (huge >= num_cu && num_cu % 8 == 0 && huge * (a.K / 128) < ((int64_t)1 << 31)) {
+    if constexpr (A8) return big<true, 128, 3>(a, num_cu, st);
+    else return a.K % 256 == 0 ? big<false, 256, 2>(a, num_cu, st) : big<false, 128, 4>(a, num_cu, st);
   }
   const int64_t large = (int64_t)((a.M + 127) / 128) * ((a.N + 255) / 256) * a.batch;
   if (large >= num_cu) return tile<A8, 2, 4, A8 ? 2 : 3>(a, st);

@@ -144,6 +144,13 @@ def test_product(M, G, N, K, a8):
 
 
 @pytest.mark.parametrize("a8", [False, True])
+@pytest.mark.parametrize("M, G, N, K", [(4100, 1, 4112, 512), (1000, 8, 2064, 384), (4096, 1, 8192, 256), (4096, 1, 4096, 128)])
+def test_product_of_many_tiles(M, G, N, K, a8):
+    # enough 256 x 256 tiles for every compute unit: partial ones, several to a workgroup, short and odd depths
+    _product(M, G, N, K, a8)
+
+
+@pytest.mark.parametrize("a8", [False, True])
 @pytest.mark.parametrize("M, G, N, K", [(3, 2, 64, 256), (40, 1, 208, 512), (200, 3, 176, 384), (384, 1, 768, 640)])
 def test_product_of_wide_scales_in_wider_buffers(M, G, N, K, a8):
     _product(M, G, N, K, a8, spread=4.0, pad=48, ypad=24, tokens=8)
