@@ -26,88 +26,78 @@ __device__ __forceinline__ v8i regs8(const v4i lo, const v4i hi) {
 }
 
 // ---- few rows: the weights stream past ------------------------------------------------------
-// A workgroup makes up to 16 RT rows x 16 CT columns of one group over all of K: eight waves
+// A workgroup makes up to 16 rows x 16 CT columns of one group over all of K: eight waves
 // take eight runs of 128-deep steps, operands straight from memory into registers (each byte of
 // the weights is read once), and add their f32 sums in LDS in wave order.
-constexpr int kFewWaves = 8;
-constexpr int kFewSteps = 4;  // steps whose operands are in flight together
+constexpr int kFewWaves = 8, kFewSteps = 4;  // and steps whose operands are in flight together
 
-template <bool A8, int RT, int CT>
+template <bool A8, int CT>
 __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(Mx4Args p) {
-  __shared__ float red[kFewWaves][RT * CT * 4][64];
+  __shared__ float red[kFewWaves][CT * 4][64];
   const int t = threadIdx.x, lane = t & 63;
   const int wv = __builtin_amdgcn_readfirstlane(t >> 6);
   const int cl = lane & 15, q = lane >> 4;
-  const int g = blockIdx.y, n0 = blockIdx.x * 16 * CT, M = p.M, N = p.N, KT = p.K >> 7;
+  // workgroups go to the XCDs in turn: each XCD takes a run of consecutive slices of columns, so that
+  // a group's rows come into as few L2s as can be
+  const int S = gridDim.x, all = S * gridDim.y, id = blockIdx.x + S * blockIdx.y;
+  const int item = (all & 7) == 0 ? (id & 7) * (all >> 3) + (id >> 3) : id;
+  const int g = item / S, n0 = item % S * 16 * CT, M = p.M, N = p.N, KT = p.K >> 7;
   const int k_lo = KT * wv / kFewWaves, k_hi = KT * (wv + 1) / kFewWaves;
   const uint8_t* A = p.a + g * p.a_batch_stride + q * 16;
   const uint8_t* W = p.w + g * p.w_batch_stride + q * 16;
   const int32_t* SA = p.a_scale + (int64_t)g * KT * p.a_tokens;
   const int32_t* SW = p.w_scale + (int64_t)g * KT * N;
   // rows behind the last read the last, columns likewise: they feed outputs that are not stored
-  const uint8_t* ar[RT];
+  const int row = min(cl, M - 1);
+  const uint8_t* ar = A + row * p.lda;
   const uint8_t* wr[CT];
-  int row[RT], col[CT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    row[i] = min(16 * i + cl, M - 1);
-    ar[i] = A + row[i] * p.lda;
-  }
+  int col[CT];
 #pragma unroll
   for (int j = 0; j < CT; ++j) {
     col[j] = min(n0 + 16 * j + cl, N - 1);
     wr[j] = W + (int64_t)col[j] * (p.K / 2);
   }
-  v4f acc[RT][CT];
+  v4f acc[CT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+  for (int j = 0; j < CT; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int F = kFewSteps;
+  for (int k0 = k_lo; k0 < k_hi; k0 += F) {
+    v4i w[F][CT], lo[F], hi[F];
+    int sa[F], sw[F][CT];
 #pragma unroll
-    for (int j = 0; j < CT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k0 = k_lo; k0 < k_hi; k0 += kFewSteps) {
-    v4i w[kFewSteps][CT], lo[kFewSteps][RT], hi[kFewSteps][RT];
-    int sa[kFewSteps][RT], sw[kFewSteps][CT];
-#pragma unroll
-    for (int s = 0; s < kFewSteps; ++s) {
+    for (int s = 0; s < F; ++s) {
       const int kb = min(k0 + s, k_hi - 1);  // loads of steps past the run are not used
 #pragma unroll
       for (int j = 0; j < CT; ++j) {
         w[s][j] = *reinterpret_cast<const v4i*>(wr[j] + kb * 64);
         sw[s][j] = SW[(int64_t)kb * N + col[j]];
       }
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        sa[s][i] = SA[kb * p.a_tokens + row[i]];
-        lo[s][i] = *reinterpret_cast<const v4i*>(ar[i] + kb * (A8 ? 128 : 64));
-        if constexpr (A8) hi[s][i] = *reinterpret_cast<const v4i*>(ar[i] + kb * 128 + 64);
-      }
+      sa[s] = SA[kb * p.a_tokens + row];
+      lo[s] = *reinterpret_cast<const v4i*>(ar + kb * (A8 ? 128 : 64));
+      if constexpr (A8) hi[s] = *reinterpret_cast<const v4i*>(ar + kb * 128 + 64);
     }
     __builtin_amdgcn_sched_barrier(0);  // every load above before the first use
 #pragma unroll
-    for (int s = 0; s < kFewSteps; ++s) {
+    for (int s = 0; s < F; ++s) {
       if (k0 + s < k_hi) {  // uniform
+        const v8i a = A8 ? regs8(lo[s], hi[s]) : regs4(lo[s]);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const v8i a = A8 ? regs8(lo[s][i], hi[s][i]) : regs4(lo[s][i]);
-#pragma unroll
-          for (int j = 0; j < CT; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                a, regs4(w[s][j]), acc[i][j], A8 ? 0 : 4, 4, 0, (uint32_t)sa[s][i] >> (8 * q), 0, (uint32_t)sw[s][j] >> (8 * q));
-        }
+        for (int j = 0; j < CT; ++j)
+          acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              a, regs4(w[s][j]), acc[j], A8 ? 0 : 4, 4, 0, (uint32_t)sa[s] >> (8 * q), 0, (uint32_t)sw[s][j] >> (8 * q));
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+  for (int j = 0; j < CT; ++j)
 #pragma unroll
-    for (int j = 0; j < CT; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) red[wv][(i * CT + j) * 4 + r][lane] = acc[i][j][r];
+    for (int r = 0; r < 4; ++r) red[wv][j * 4 + r][lane] = acc[j][r];
   __syncthreads();
   uint16_t* Y = p.y + g * p.y_batch_stride;
-  for (int e = t; e < RT * CT * 4 * 64; e += 64 * kFewWaves) {
-    const int ln = e & 63, r = (e >> 6) & 3, j = (e >> 8) % CT, i = (e >> 8) / CT;
+  for (int e = t; e < CT * 4 * 64; e += 64 * kFewWaves) {
+    const int ln = e & 63, r = (e >> 6) & 3, j = e >> 8;
     // output layout: column lane % 16, row 4 (lane / 16) + r
-    const int m = 16 * i + 4 * (ln >> 4) + r, n = n0 + 16 * j + (ln & 15);
+    const int m = 4 * (ln >> 4) + r, n = n0 + 16 * j + (ln & 15);
     float v = red[0][e >> 6][ln];
 #pragma unroll
     for (int w = 1; w < kFewWaves; ++w) v += red[w][e >> 6][ln];
@@ -130,7 +120,7 @@ __device__ __forceinline__ int chunk_swz(int row) { return B == 64 ? (row >> 2) 
 template <int B>
 __device__ __forceinline__ int lds_at(int row, int c) { return row * B + ((c ^ chunk_swz<B>(row)) << 4); }
 
-template <bool A8, int WM, int WN, int S>
+template <bool A8, int WM, int WN, int S, int KS>
 struct Ring {
   static constexpr int kBM = 64 * WM, kBN = 64 * WN;
   static constexpr int kARow = A8 ? 128 : 64;          // bytes of a row's slice
@@ -139,16 +129,18 @@ struct Ring {
   static constexpr int kNA = kA / 4096, kNW = kW / 4096, kNS = (kBM + kBN + 255) / 256;  // DMAs of a wave
   static constexpr int kDma = kNA + kNW + kNS;
   static constexpr int kOut = kBM * kBN * 2;           // the bf16 tile, staged in the ring's place
-  static constexpr int kBytes = S * kStage > kOut ? S * kStage : kOut;
+  static constexpr int kSum = (KS - 1) * kBM * kBN * 4; // sums of the waves behind the first four
+  static constexpr int kBytes = KS * S * kStage > kOut + kSum ? KS * S * kStage : kOut + kSum;
 };
 
-template <bool A8, int WM, int WN, int S>
-__global__ __launch_bounds__(256, 2) void k_mx4_tile(Mx4Args p, int tiles_m, int tiles_n, int per_xcd) {
-  using R = Ring<A8, WM, WN, S>;
+template <bool A8, int WM, int WN, int S, int KS>
+__global__ __launch_bounds__(256 * KS, 2) void k_mx4_tile(Mx4Args p, int tiles_m, int tiles_n, int per_xcd) {
+  using R = Ring<A8, WM, WN, S, KS>;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int t = threadIdx.x, lane = t & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(t >> 6), wm = wv >> 1, wn = wv & 1;
-  const int M = p.M, N = p.N, KT = p.K >> 7;
+  const int wv = __builtin_amdgcn_readfirstlane(t >> 6) & 3, wm = wv >> 1, wn = wv & 1;
+  const int ks = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(t >> 8);
+  const int M = p.M, N = p.N, KT = p.K >> 7, ST = (KT + KS - 1) / KS;  // slices, steps
   // workgroups go to the XCDs in turn; each XCD takes a run of consecutive tiles, in groups of
   // eight tile rows, so that what its L2 holds is used by its neighbours
   const int per_group = tiles_m * tiles_n;
@@ -183,8 +175,9 @@ __global__ __launch_bounds__(256, 2) void k_mx4_tile(Mx4Args p, int tiles_m, int
     soff[i] = (uint32_t)(d < WM ? min(r, M - 1 - m0) : min(r - R::kBM, N - 1 - n0)) * 4u;
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_u8)smem;
-  auto issue = [&](int kt, int stage) __attribute__((always_inline)) {
-    const uint32_t st = lds0 + stage * R::kStage;
+  auto issue = [&](int step, int stage) __attribute__((always_inline)) {
+    const int kt = KS == 1 ? step : min(KS * step + ks, KT - 1);
+    const uint32_t st = lds0 + (stage * KS + ks) * R::kStage;
     const uint8_t* a = A + (int64_t)kt * R::kARow;
     const uint8_t* w = W + (int64_t)kt * 64;
 #pragma unroll
@@ -209,7 +202,7 @@ __global__ __launch_bounds__(256, 2) void k_mx4_tile(Mx4Args p, int tiles_m, int
   const int l32 = lane & 31, h = lane >> 5;
   const int ar = wm * 32 * WM + l32, wr = wn * 32 * WN + l32;
   auto multiply = [&](int stage) __attribute__((always_inline)) {
-    const uint8_t* sa = smem + stage * R::kStage;
+    const uint8_t* sa = smem + (stage * KS + ks) * R::kStage;
     const uint8_t* sw = sa + R::kA;
     const uint32_t* ss = reinterpret_cast<const uint32_t*>(sw + R::kW);
     uint32_t xa[WM], xw[WN];
@@ -247,11 +240,11 @@ __global__ __launch_bounds__(256, 2) void k_mx4_tile(Mx4Args p, int tiles_m, int
             regs4(wf[1][j]), A8 ? regs8(al[1][i], ah[1][i]) : regs4(al[1][i]), acc[i][j], 4, A8 ? 0 : 4, 2, xw[j], 2, xa[i]);
   };
 
-  // slices 0 .. S - 2 are sent ahead (past the last one, the last again: never read)
+  // steps 0 .. S - 2 are sent ahead (past the last one, the last again: never read)
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) issue(min(s, KT - 1), s);
+  for (int s = 0; s < S - 1; ++s) issue(min(s, ST - 1), s);
   int kt = 0, stage = 0;
-  for (; kt + S - 1 < KT; ++kt) {
+  for (; kt + S - 1 < ST; ++kt) {
     wait_vm<R::kDma*(S - 2)>();  // this wave's share of slice kt has landed
     lds_barrier();               // everyone's has, and slice kt - 1 has been read by all
     const int next = stage == 0 ? S - 1 : stage - 1;
@@ -259,13 +252,13 @@ __global__ __launch_bounds__(256, 2) void k_mx4_tile(Mx4Args p, int tiles_m, int
     multiply(stage);
     stage = stage + 1 == S ? 0 : stage + 1;
   }
-  // the last slices, nothing left to send
+  // the last steps, nothing left to send
   auto last = [&](auto left) __attribute__((always_inline)) {
-    constexpr int L = decltype(left)::value;  // slices behind this one
-    if (kt + L == KT - 1) {
+    constexpr int L = decltype(left)::value;  // steps behind this one
+    if (kt + L == ST - 1) {
       wait_vm<R::kDma * L>();
       lds_barrier();
-      multiply(stage);
+      if (KS == 1 || L > 0 || KS * kt + ks < KT) multiply(stage);
       stage = stage + 1 == S ? 0 : stage + 1;
       ++kt;
     }
@@ -278,9 +271,27 @@ __global__ __launch_bounds__(256, 2) void k_mx4_tile(Mx4Args p, int tiles_m, int
   // XORed with the row, so that both the 8-byte writes (a row a lane) and the reads of whole
   // rows meet all banks; then 16 bytes a lane to memory
   lds_barrier();
+  if constexpr (KS == 2) {  // the second half of the slices' sums come through LDS
+    v4f* sum = reinterpret_cast<v4f*>(smem + R::kOut) + wv * (WM * WN * 4 * 64) + lane;
+    if (ks == 1) {
+#pragma unroll
+      for (int e = 0; e < WM * WN * 4; ++e) {
+        const v16f& c = acc[e / 4 / WN][e / 4 % WN];
+        sum[e * 64] = v4f{c[e % 4 * 4], c[e % 4 * 4 + 1], c[e % 4 * 4 + 2], c[e % 4 * 4 + 3]};
+      }
+    }
+    __syncthreads();
+    if (ks == 1) return;
+#pragma unroll
+    for (int e = 0; e < WM * WN * 4; ++e) {
+      const v4f c = sum[e * 64];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[e / 4 / WN][e / 4 % WN][e % 4 * 4 + r] += c[r];
+    }
+  }
   constexpr int RB = 64 * WN, CH = RB / 16;
   uint8_t* so = smem + wv * (32 * WM * RB);
-  auto out_at = [&](int r, int c) { return r * RB + ((c ^ (CH == 16 ? r & 15 : (r >> 1) & 7)) << 4); };
+  auto out_at = [&](int r, int c) { return r * RB + ((c ^ (CH == 16 ? r & 15 : CH == 8 ? (r >> 1) & 7 : (r >> 2) & 3)) << 4); };
 #pragma unroll
   for (int i = 0; i < WM; ++i)
 #pragma unroll
@@ -298,264 +309,39 @@ __global__ __launch_bounds__(256, 2) void k_mx4_tile(Mx4Args p, int tiles_m, int
   for (int k = 0; k < 32 * WM / RPI; ++k) {
     const int r = k * RPI + lane / CH;
     const v4u v = *reinterpret_cast<const v4u*>(so + out_at(r, lane % CH));
-    if (mw + r < M && n < N) *reinterpret_cast<v4u*>(Y + (int64_t)(mw + r) * p.ldy) = v;
+    if (mw + r < M && n < N) __builtin_nontemporal_store(v, reinterpret_cast<v4u*>(Y + (int64_t)(mw + r) * p.ldy));
   }
-}
-
-// ---- many tiles: persistent 256 x 256 ---------------------------------------------------------
-// One workgroup of eight waves (2 x 4, 128 x 64 outputs each) on every CU walks over its tiles; the
-// ring of slices runs on across them, so the next tile's first slices land while this one's outputs
-// are stored.  A slice is KD deep: 256 with 4-bit operands (128-byte rows: whole cache lines), 128
-// with E4M3 activations or an odd number of 128-deep blocks.
-template <bool A8, int KD, int S>
-struct BigRing {
-  static constexpr int kARow = A8 ? KD : KD / 2, kWRow = KD / 2, kBlocks = KD / 128;
-  static constexpr int kA = 256 * kARow, kW = 256 * kWRow, kS = kBlocks * 2048;  // kS: words, [block][256 rows, 256 columns]
-  static constexpr int kStage = kA + kW + kS;
-  static constexpr int kNA = kA / 8192, kNW = kW / 8192, kNS = kBlocks;  // DMAs of a wave
-  static constexpr int kDma = kNA + kNW + kNS;
-  static constexpr int kStores = 16;  // a wave's stores of a whole tile
-  static_assert(kStage >= 8 * 4096, "a stage holds the waves' output blocks");
-};
-
-template <bool A8, int KD, int S>
-__global__ __launch_bounds__(512, 2) void k_mx4_big(Mx4Args p, int tiles_m, int tiles_n, int per_xcd, int wgs_xcd) {
-  using R = BigRing<A8, KD, S>;
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  const int t = threadIdx.x, lane = t & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(t >> 6), wm = wv >> 2, wn = wv & 3;
-  const int M = p.M, N = p.N, KB = p.K >> 7, KT = p.K / KD;  // 128-deep blocks, slices
-  const int per_group = tiles_m * tiles_n, xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
-  const int total = per_group * p.batch, lin_end = min(total, (xcd + 1) * per_xcd);
-  const int lin0 = xcd * per_xcd + local;
-  if (lin0 >= lin_end) return;
-  const int slices = (lin_end - lin0 + wgs_xcd - 1) / wgs_xcd * KT;
-  struct Tile {
-    int g, m0, n0;
-  };
-  auto tile_at = [&](int lin) __attribute__((always_inline)) {  // in bands of eight tile rows
-    const int g = lin / per_group, in_g = lin % per_group;
-    const int band = in_g / (8 * tiles_n), rows8 = min(8, tiles_m - 8 * band), in_b = in_g - band * 8 * tiles_n;
-    return Tile{g, (8 * band + in_b % rows8) * 256, in_b / rows8 * 256};
-  };
-  // lane offsets of this wave's DMA instructions wv, wv + 8, ... (rows are clamped per tile below)
-  auto row_of = [&](int i, int per) { return ((wv + 8 * i) * 64 + lane) / per; };
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_u8)smem;
-  // where slices are sent from: the tile of the next one
-  int s_lin = lin0, s_kt = 0;
-  Tile st = tile_at(lin0);
-  uint32_t aoff[R::kNA], woff[R::kNW];
-  auto offsets = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < R::kNA; ++i) {
-      constexpr int per = R::kARow / 16;
-      const int r = row_of(i, per), c = (lane % per) ^ chunk_swz<R::kARow>(r);
-      aoff[i] = (uint32_t)(min(r, M - 1 - st.m0) * (int)p.lda + c * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < R::kNW; ++i) {
-      constexpr int per = R::kWRow / 16;
-      const int r = row_of(i, per), c = (lane % per) ^ chunk_swz<R::kWRow>(r);
-      woff[i] = (uint32_t)(min(r, N - 1 - st.n0) * (p.K / 2) + c * 16);
-    }
-  };
-  offsets();
-  auto send = [&](int stage) __attribute__((always_inline)) {
-    const uint32_t to = lds0 + stage * R::kStage;
-    const uint8_t* a = p.a + st.g * p.a_batch_stride + (int64_t)st.m0 * p.lda + (int64_t)s_kt * R::kARow;
-    const uint8_t* w = p.w + st.g * p.w_batch_stride + (int64_t)st.n0 * (p.K / 2) + (int64_t)s_kt * R::kWRow;
-#pragma unroll
-    for (int i = 0; i < R::kNA; ++i) dma16(a, aoff[i], to + (wv + 8 * i) * 1024);
-#pragma unroll
-    for (int i = 0; i < R::kNW; ++i) dma16(w, woff[i], to + R::kA + (wv + 8 * i) * 1024);
-    // the words of 64 rows (waves 0 .. 3) or columns (4 .. 7) of each 128-deep block
-    const int r = (wv & 3) * 64 + lane;
-    const uint32_t off = (uint32_t)(wv < 4 ? min(r, M - 1 - st.m0) : min(r, N - 1 - st.n0));
-#pragma unroll
-    for (int b = 0; b < R::kBlocks; ++b) {
-      const int64_t kb = (int64_t)st.g * KB + s_kt * R::kBlocks + b;
-      const int32_t* words = wv < 4 ? p.a_scale + kb * p.a_tokens + st.m0 : p.w_scale + kb * N + st.n0;
-      dma4_at(words + off, to + R::kA + R::kW + b * 2048 + wv * 256);
-    }
-    if (++s_kt == KT) {
-      s_kt = 0;
-      s_lin += wgs_xcd;
-      if (s_lin < lin_end) {
-        st = tile_at(s_lin);
-        offsets();
-      }
-    }
-  };
-
-  v16f acc[4][2];
-  const int l32 = lane & 31, h = lane >> 5;
-  const int ar = wm * 128 + l32, wr = wn * 64 + l32;
-  auto clear = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  };
-  auto multiply = [&](int stage) __attribute__((always_inline)) {
-    const uint8_t* sa = smem + stage * R::kStage;
-    const uint8_t* sw = sa + R::kA;
-#pragma unroll
-    for (int b = 0; b < R::kBlocks; ++b) {
-      const uint32_t* ss = reinterpret_cast<const uint32_t*>(sw + R::kW + b * 2048);
-      uint32_t xa[4], xw[2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) xa[i] = ss[ar + 32 * i] >> (8 * h);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) xw[j] = ss[256 + wr + 32 * j] >> (8 * h);
-      auto step = [&](auto which) __attribute__((always_inline)) {
-        constexpr int s = decltype(which)::value;  // 64-deep half; its scale bytes are 2 s + h
-        v4i al[4], ah[4], wf[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) wf[j] = *reinterpret_cast<const v4i*>(sw + lds_at<R::kWRow>(wr + 32 * j, 4 * b + 2 * s + h));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (A8) {
-            al[i] = *reinterpret_cast<const v4i*>(sa + lds_at<128>(ar + 32 * i, 4 * s + h));
-            ah[i] = *reinterpret_cast<const v4i*>(sa + lds_at<128>(ar + 32 * i, 4 * s + 2 + h));
-          } else {
-            al[i] = *reinterpret_cast<const v4i*>(sa + lds_at<R::kARow>(ar + 32 * i, 4 * b + 2 * s + h));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                regs4(wf[j]), A8 ? regs8(al[i], ah[i]) : regs4(al[i]), acc[i][j], 4, A8 ? 0 : 4, 2 * s, xw[j], 2 * s, xa[i]);
-      };
-      step(std::integral_constant<int, 0>{});
-      step(std::integral_constant<int, 1>{});
-    }
-  };
-
-  clear();
-#pragma unroll
-  for (int s = 0; s < S - 1; ++s)
-    if (s < slices) send(s);
-  int stage = 0, kt = 0, lin = lin0;
-  bool stored = false;  // the last thing done was to store a whole tile
-  for (int sl = 0; sl < slices; ++sl) {
-    // This wave's share of slice sl has landed: S - 2 later ones may be on their way, and the stores
-    // behind them (memory operations end in their order).
-    if (sl + S - 2 >= slices) wait_vm<0>();
-    else if (stored) wait_vm<R::kDma*(S - 2) + R::kStores>();
-    else wait_vm<R::kDma*(S - 2)>();
-    stored = false;
-    lds_barrier();  // everyone's has, and slice sl - 1, or the outputs in its place, has been read by all
-    if (sl + S - 1 < slices) send(stage == 0 ? S - 1 : stage - 1);
-    multiply(stage);
-    if (++kt == KT) {
-      // ---- outputs: bf16, 32 rows of 128 bytes at a time through the wave's 4 KiB of the slice's
-      // stage (16-byte chunks XORed with bits 1..3 of the row), then 16 bytes a lane, whole lines.
-      // They are not read again here: streaming stores leave the L2 to the operands.
-      kt = 0;
-      const Tile o = tile_at(lin);
-      lin += wgs_xcd;
-      lds_barrier();
-      uint8_t* so = smem + stage * R::kStage + wv * 4096;
-      auto out_at = [&](int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); };
-      const int mw = o.m0 + wm * 128, n = o.n0 + wn * 64 + (lane & 7) * 8;
-      uint16_t* Y = p.y + o.g * p.y_batch_stride + n;
-      const bool inside = o.m0 + 256 <= M && o.n0 + 256 <= N;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t w0 = f32_to_bf16_nan(acc[i][j][4 * q]) | f32_to_bf16_nan(acc[i][j][4 * q + 1]) << 16;
-            const uint32_t w1 = f32_to_bf16_nan(acc[i][j][4 * q + 2]) | f32_to_bf16_nan(acc[i][j][4 * q + 3]) << 16;
-            *reinterpret_cast<v2u*>(so + out_at(l32, 4 * j + q) + 8 * h) = v2u{w0, w1};
-          }
-        v4u v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const v4u*>(so + out_at(8 * k + (lane >> 3), lane & 7));
-        if (inside) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            __builtin_nontemporal_store(v[k], reinterpret_cast<v4u*>(Y + (int64_t)(mw + 32 * i + 8 * k + (lane >> 3)) * p.ldy));
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int m = mw + 32 * i + 8 * k + (lane >> 3);
-            if (m < M && n < N) *reinterpret_cast<v4u*>(Y + (int64_t)m * p.ldy) = v[k];
-          }
-        }
-      }
-      if (inside) stored = true;
-      else wait_vm<0>();  // their number is not known
-      clear();
-    }
-    stage = stage + 1 == S ? 0 : stage + 1;
-  }
-}
-
-template <bool A8, int RT, int CT>
-hipError_t few(const Mx4Args& a, hipStream_t st) {
-  const dim3 grid((unsigned)((a.N + 16 * CT - 1) / (16 * CT)), (unsigned)a.batch);
-  hipLaunchKernelGGL((k_mx4_few<A8, RT, CT>), grid, dim3(64 * kFewWaves), 0, st, a);
-  return hipGetLastError();
 }
 
 template <bool A8, int CT>
-hipError_t few_rows(const Mx4Args& a, hipStream_t st) {
-  switch ((a.M + 15) / 16) {
-    case 1: return few<A8, 1, CT>(a, st);
-    case 2: return few<A8, 2, CT>(a, st);
-    case 3: return few<A8, 3, CT>(a, st);
-    default: return few<A8, 4, CT>(a, st);
-  }
-}
-
-template <bool A8, int WM, int WN, int S>
-hipError_t tile(const Mx4Args& a, hipStream_t st) {
-  using R = Ring<A8, WM, WN, S>;
-  const int64_t tm = (a.M + R::kBM - 1) / R::kBM, tn = (a.N + R::kBN - 1) / R::kBN;
-  const int64_t total = tm * tn * a.batch, per_xcd = (total + 7) / 8;
-  if (per_xcd * 8 >= ((int64_t)1 << 31) || tm * tn >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-  const void* kernel = reinterpret_cast<const void*>(k_mx4_tile<A8, WM, WN, S>);
-  hipError_t e = set_lds_limit(kernel, R::kBytes);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_mx4_tile<A8, WM, WN, S>), dim3((unsigned)(per_xcd * 8)), dim3(256), R::kBytes, st, a, (int)tm,
-                     (int)tn, (int)per_xcd);
+hipError_t few(const Mx4Args& a, hipStream_t st) {
+  const dim3 grid((unsigned)((a.N + 16 * CT - 1) / (16 * CT)), (unsigned)a.batch);
+  hipLaunchKernelGGL((k_mx4_few<A8, CT>), grid, dim3(64 * kFewWaves), 0, st, a);
   return hipGetLastError();
 }
 
-template <bool A8, int KD, int S>
-hipError_t big(const Mx4Args& a, int num_cu, hipStream_t st) {
-  using R = BigRing<A8, KD, S>;
-  const int64_t tm = (a.M + 255) / 256, tn = (a.N + 255) / 256, total = tm * tn * a.batch;
-  if (total * (a.K / KD) >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-  const int per_xcd = (int)((total + 7) / 8), wgs = num_cu / 8;
-  const void* kernel = reinterpret_cast<const void*>(k_mx4_big<A8, KD, S>);
-  hipError_t e = set_lds_limit(kernel, S * R::kStage);
+template <bool A8, int WM, int WN, int S, int KS>
+hipError_t tile(const Mx4Args& a, hipStream_t st) {
+  using R = Ring<A8, WM, WN, S, KS>;
+  const int64_t tm = (a.M + R::kBM - 1) / R::kBM, tn = (a.N + R::kBN - 1) / R::kBN;
+  const int64_t total = tm * tn * a.batch, per_xcd = (total + 7) / 8;
+  if (per_xcd * 8 >= ((int64_t)1 << 31) || tm * tn >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+  const void* kernel = reinterpret_cast<const void*>(k_mx4_tile<A8, WM, WN, S, KS>);
+  hipError_t e = set_lds_limit(kernel, R::kBytes);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_mx4_big<A8, KD, S>), dim3((unsigned)(8 * wgs)), dim3(512), S * R::kStage, st, a, (int)tm, (int)tn,
-                     per_xcd, wgs);
+  hipLaunchKernelGGL((k_mx4_tile<A8, WM, WN, S, KS>), dim3((unsigned)(per_xcd * 8)), dim3(256 * KS), R::kBytes, st, a, (int)tm,
+                     (int)tn, (int)per_xcd);
   return hipGetLastError();
 }
 
 template <bool A8>
 hipError_t launch(const Mx4Args& a, int num_cu, hipStream_t st) {
-  if (a.M <= 64) {
-    if ((int64_t)a.N / 32 * a.batch >= num_cu) return few_rows<A8, 2>(a, st);
-    return few_rows<A8, 1>(a, st);
-  }
-  const int64_t huge = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256) * a.batch;
-  if (huge >= num_cu && num_cu % 8 == 0 && huge * (a.K / 128) < ((int64_t)1 << 31)) {
-    if constexpr (A8) return big<true, 128, 3>(a, num_cu, st);
-    else return a.K % 256 == 0 ? big<false, 256, 2>(a, num_cu, st) : big<false, 128, 4>(a, num_cu, st);
-  }
+  if (a.M <= 16) return (int64_t)a.N / 16 * a.batch >= 2 * num_cu ? few<A8, 2>(a, st) : few<A8, 1>(a, st);
   const int64_t large = (int64_t)((a.M + 127) / 128) * ((a.N + 255) / 256) * a.batch;
-  if (large >= num_cu) return tile<A8, 2, 4, A8 ? 2 : 3>(a, st);
-  return tile<A8, 1, 2, 4>(a, st);
+  if (large >= num_cu) return tile<A8, 2, 4, A8 ? 2 : 3, 1>(a, st);
+  const int64_t small = (int64_t)((a.M + 63) / 64) * ((a.N + 127) / 128) * a.batch;
+  if (small >= num_cu) return tile<A8, 1, 2, 4, 1>(a, st);
+  return tile<A8, 1, 1, 4, 2>(a, st);
 }
 
 }  // namespace

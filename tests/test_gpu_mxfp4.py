@@ -146,7 +146,7 @@ def test_product(M, G, N, K, a8):
 @pytest.mark.parametrize("a8", [False, True])
 @pytest.mark.parametrize("M, G, N, K", [(4100, 1, 4112, 512), (1000, 8, 2064, 384), (4096, 1, 8192, 256), (4096, 1, 4096, 128)])
 def test_product_of_many_tiles(M, G, N, K, a8):
-    # enough 256 x 256 tiles for every compute unit: partial ones, several to a workgroup, short and odd depths
+    # tiles for every compute unit and more: partial ones, several bands of rows, short and odd depths
     _product(M, G, N, K, a8)
 
 
