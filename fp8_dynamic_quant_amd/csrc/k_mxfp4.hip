@@ -22,99 +22,124 @@ __device__ __forceinline__ int e2m1_exp(uint32_t a) {
   return e < -127 ? -127 : e;
 }
 
-// One wave for 512 consecutive elements of a row: lane l takes 8 of them (16 bytes read, 4
-// written), four lanes a block, 16 lanes a scale word.
+// Both kernels: a wave takes 512 consecutive elements of one group in four consecutive tokens, a
+// workgroup 16 tokens of them.  Lane l holds 8 elements (16 bytes of bf16, 4 of codes) of each token,
+// four lanes a block, 16 lanes a scale word; the four tokens' words are 16 consecutive bytes.
+struct Share {
+  int g, p, h;   // group; this 16-lane row's scale word, this quad's block
+  int64_t t0;    // the first of the wave's four tokens
+  bool word, block;
+};
+__device__ __forceinline__ Share share_of(int G, int D) {
+  const int lane = threadIdx.x & 63, HG = D / 32, PH = (HG + 3) / 4;
+  const uint32_t PW = (uint32_t)(PH + 3) / 4, across = (uint32_t)G * PW;
+  const uint32_t rows = blockIdx.x / across, in = blockIdx.x % across;
+  Share s;
+  s.g = (int)(in / PW);
+  s.t0 = (int64_t)rows * 16 + (threadIdx.x >> 6) * 4;
+  s.p = 4 * (int)(in % PW) + (lane >> 4);
+  s.h = 4 * s.p + ((lane >> 2) & 3);
+  s.word = s.p < PH;
+  s.block = s.h < HG;
+  return s;
+}
+hipError_t share_grid(int64_t T, int G, int D, dim3* grid) {
+  const int64_t blocks = (T + 15) / 16 * G * (((int64_t)D / 32 + 15) / 16);
+  if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+  *grid = dim3((unsigned)blocks);
+  return hipSuccess;
+}
+
 __global__ __launch_bounds__(256) void k_group_quant_mxfp4(const uint16_t* __restrict__ x, int64_t T, int G, int D,
                                                            uint8_t* __restrict__ xq, int32_t* __restrict__ xs) {
-  const int lane = threadIdx.x & 63;
-  const int HG = D / 32, PH = (HG + 3) / 4, PW = (PH + 3) / 4;
-  const int64_t TA = (T + 3) / 4 * 4;
-  const int64_t wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (wid >= TA * G * PW) return;
-  const int pw = (int)(wid % PW);
-  const int64_t tg = wid / PW;
-  const int g = (int)(tg % G);
-  const int64_t t = tg / G;
-  const int p = 4 * pw + (lane >> 4);         // this 16-lane row's scale word
-  const int h = 4 * p + ((lane >> 2) & 3);    // this quad's block
-  int byte = 0;
-  if (t < T && p < PH && h < HG) {
-    const int64_t off = (t * G + g) * (int64_t)D + (int64_t)h * 32 + (lane & 3) * 8;
-    const v4u u = *reinterpret_cast<const v4u*>(x + off);
+  const Share s = share_of(G, D);
+  if (s.t0 >= T) return;  // whole waves
+  const int64_t TA = (T + 3) / 4 * 4, step = (int64_t)G * D;
+  const int64_t off = (s.t0 * G + s.g) * D + (int64_t)s.h * 32 + (threadIdx.x & 3) * 8;
+  v4u u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    u[i] = v4u{0, 0, 0, 0};
+    if (s.block && s.t0 + i < T) u[i] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(x + off + i * step));
+  }
+  v4u words;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
     uint32_t a = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a = max(a, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
-    // max over the quad: swap neighbours, then pairs (exec covers whole quads here)
+    for (int j = 0; j < 4; ++j) a = max(a, max(u[i][j] & 0x7FFFu, (u[i][j] >> 16) & 0x7FFFu));
+    // max over the quad: swap neighbours, then pairs
     a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0xB1, 0xF, 0xF, false));
     a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x4E, 0xF, 0xF, false));
+    const bool there = s.block && s.t0 + i < T;
     uint32_t q = 0;
-    if (a < 0x7F80u) {
+    int byte = 0;
+    if (there && a < 0x7F80u) {
       const int e = e2m1_exp(a);
       byte = e + 127;
-      const float s = ldexpf(1.0f, e);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, (uint32_t)u[0]), s, 0);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, (uint32_t)u[1]), s, 1);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, (uint32_t)u[2]), s, 2);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, (uint32_t)u[3]), s, 3);
-    } else {
+      const float f = ldexpf(1.0f, e);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, (uint32_t)u[i][0]), f, 0);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, (uint32_t)u[i][1]), f, 1);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, (uint32_t)u[i][2]), f, 2);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, (uint32_t)u[i][3]), f, 3);
+    } else if (there) {
       byte = 255;  // a NaN or an infinity among the 32: the scale's NaN, codes zero
     }
-    *reinterpret_cast<uint32_t*>(xq + off / 2) = q;
+    if (there) *reinterpret_cast<uint32_t*>(xq + (off + i * step) / 2) = q;
+    // the row's four quad bytes (0 for blocks past the last and tokens past T) form the word
+    const int base = threadIdx.x & 48;
+    words[i] = (uint32_t)byte | (uint32_t)__shfl(byte, base + 4, 64) << 8 | (uint32_t)__shfl(byte, base + 8, 64) << 16 |
+               (uint32_t)__shfl(byte, base + 12, 64) << 24;
   }
-  // the row's four quad bytes (0 for blocks past HG) form the word; lane 16 r writes it
-  const int base = lane & ~15;
-  const int b1 = __shfl(byte, base + 4, 64), b2 = __shfl(byte, base + 8, 64), b3 = __shfl(byte, base + 12, 64);
-  if ((lane & 15) == 0 && p < PH) {
-    const uint32_t word = (uint32_t)byte | ((uint32_t)b1 << 8) | ((uint32_t)b2 << 16) | ((uint32_t)b3 << 24);
-    xs[((int64_t)g * PH + p) * TA + t] = (int32_t)word;
-  }
+  if ((threadIdx.x & 15) == 0 && s.word)
+    *reinterpret_cast<v4u*>(xs + ((int64_t)s.g * ((D / 32 + 3) / 4) + s.p) * TA + s.t0) = words;
 }
 
 hipError_t launch_group_quant_mxfp4(const uint16_t* x, int64_t T, int G, int D, uint8_t* xq, int32_t* xs,
                                     hipStream_t st) {
-  const int HG = D / 32, PH = (HG + 3) / 4, PW = (PH + 3) / 4;
-  const int64_t TA = (T + 3) / 4 * 4;
-  const int64_t waves = TA * G * PW;
-  if (waves == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_group_quant_mxfp4, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, x, T, G, D, xq, xs);
+  if (T == 0 || G == 0 || D == 0) return hipSuccess;
+  dim3 grid;
+  const hipError_t e = share_grid(T, G, D, &grid);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_group_quant_mxfp4, grid, dim3(256), 0, st, x, T, G, D, xq, xs);
   return hipGetLastError();
 }
 
 // y = code * 2^(byte - 127), exact in bf16: two significant bits, and the least magnitude
-// 0.5 * 2^-127 is a bf16 subnormal.  Byte 255 gives NaN.  Eight elements a lane.
+// 0.5 * 2^-127 is a bf16 subnormal.  Byte 255 gives NaN.
 __global__ __launch_bounds__(256) void k_group_dequant_mxfp4(const uint8_t* __restrict__ xq,
                                                              const int32_t* __restrict__ xs, int64_t T, int G, int D,
                                                              uint16_t* __restrict__ y) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // 8 elements
-  const int per = D / 8;
-  const int64_t tg = i / per;
-  const int d8 = (int)(i % per);
-  const int g = (int)(tg % G);
-  const int64_t t = tg / G;
-  if (t >= T) return;
-  const int PH = (D / 32 + 3) / 4;
-  const int64_t TA = (T + 3) / 4 * 4;
-  const int h = d8 / 4;
-  const uint32_t byte = ((uint32_t)xs[((int64_t)g * PH + h / 4) * TA + t] >> (8 * (h & 3))) & 0xFFu;
-  const uint32_t q = *reinterpret_cast<const uint32_t*>(xq + i * 4);
-  v4u o;
-  if (byte == 255) {
-    o = v4u{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
-  } else {
-    const float s = ldexpf(1.0f, (int)byte - 127);
-    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0));
-    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1));
-    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2));
-    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 3));
+  const Share s = share_of(G, D);
+  if (s.t0 >= T || !s.block) return;
+  const int64_t TA = (T + 3) / 4 * 4, step = (int64_t)G * D;
+  const int64_t off = (s.t0 * G + s.g) * D + (int64_t)s.h * 32 + (threadIdx.x & 3) * 8;
+  const v4u words = *reinterpret_cast<const v4u*>(xs + ((int64_t)s.g * ((D / 32 + 3) / 4) + s.p) * TA + s.t0);
+  uint32_t q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    q[i] = s.t0 + i < T ? __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(xq + (off + i * step) / 2)) : 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t byte = (words[i] >> (8 * (s.h & 3))) & 0xFFu;
+    const float f = ldexpf(1.0f, (int)byte - 127);
+    v4u o;
+    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[i], f, 0));
+    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[i], f, 1));
+    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[i], f, 2));
+    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[i], f, 3));
+    if (byte == 255) o = v4u{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+    if (s.t0 + i < T) __builtin_nontemporal_store(o, reinterpret_cast<v4u*>(y + off + i * step));
   }
-  *reinterpret_cast<v4u*>(y + i * 8) = o;
 }
 
 hipError_t launch_group_dequant_mxfp4(const uint8_t* xq, const int32_t* xs, int64_t T, int G, int D, uint16_t* y,
                                       hipStream_t st) {
-  const int64_t n = T * G * (D / 8);
-  if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_group_dequant_mxfp4, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, xq, xs, T, G, D, y);
+  if (T == 0 || G == 0 || D == 0) return hipSuccess;
+  dim3 grid;
+  const hipError_t e = share_grid(T, G, D, &grid);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_group_dequant_mxfp4, grid, dim3(256), 0, st, xq, xs, T, G, D, y);
   return hipGetLastError();
 }
 
