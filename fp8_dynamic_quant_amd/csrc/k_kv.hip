@@ -72,6 +72,18 @@ __device__ __forceinline__ uint32_t encode(float y) {
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, y, 0, false) & 0xFFu;
   }
 }
+// the codes of four numbers, the first in the lowest byte
+template <bool I8>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  if constexpr (I8) {
+    return encode<true>(a) | encode<true>(b) << 8 | encode<true>(c) << 16 | encode<true>(d) << 24;
+  } else {
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false), true);
+  }
+}
+__device__ __forceinline__ float half_of(const v4u& u, int j) {  // element j of eight bf16
+  return __uint_as_float((j & 1) ? u[j / 2] & 0xFFFF0000u : u[j / 2] << 16);
+}
 
 // a held code at a larger scale: its value times 2^d, d < 0, rounded once more.  int8 codes stay
 // within a unit of the exact quotient however often a page's scale grows: each growth at least
@@ -86,60 +98,159 @@ __device__ __forceinline__ uint32_t rescale(uint32_t code, int d) {
   }
 }
 
+// find_slot by a workgroup of 256, and the sequence's length: each round asks for 256 sequences at
+// once, and the thread that has the one sought tells the others
+struct Found {
+  int b;
+  int64_t row0, rows, j, len;
+};
+__device__ __forceinline__ Found find_slot_256(const KvArgs& c, int64_t item, int div, int per, Found* told, int* count) {
+  const int t = threadIdx.x;
+  int lo = 0, span = c.B;
+  for (;;) {
+    const int step = (span + 255) / 256, i = t * step;
+    const bool mine = i < span;
+    const int64_t row0 = mine ? seq_offset(c, lo + i) : 0, base = row0 / div + (int64_t)per * (lo + i);
+    int64_t end = 0, len = 0;
+    if (step == 1 && mine) {
+      end = seq_offset(c, lo + i + 1);
+      len = c.lens[lo + i];
+    }
+    const uint64_t votes = __ballot(mine && base <= item);
+    if ((t & 63) == 0) count[t >> 6] = __popcll(votes);
+    __syncthreads();
+    const int at = max(count[0] + count[1] + count[2] + count[3] - 1, 0);
+    if (step == 1) {
+      // j < 0: offsets that do not begin at 0, rows before the first sequence
+      if (t == at) *told = Found{lo + i, row0, item < base ? 0 : end - row0, max(item - base, (int64_t)0), len};
+      __syncthreads();
+      return *told;
+    }
+    __syncthreads();  // the counts have been read
+    lo += at * step;
+    span = min(step, span - at * step);
+  }
+}
+
 // One workgroup for the new rows of one sequence in one page of one head, keys (side 0) or
-// values (side 1).
+// values (side 1).  A thread's share is four pieces of eight elements: of keys 256 pieces apart in
+// the order of memory, of values the four slots of an aligned group, whose codes are then whole
+// words of the value rows.  The first share stays in registers between the two passes (the
+// largest magnitude, the codes); larger pages read the others again.
 template <bool I8>
-__global__ __launch_bounds__(256) void k_kv_append(KvArgs c, const uint16_t* k_new, int64_t ldk, const uint16_t* v_new,
+__global__ __launch_bounds__(256) void k_kv_append(KvArgs c, int div, int per_seq, const uint16_t* k_new, int64_t ldk, const uint16_t* v_new,
                                                    int64_t ldv) {
+  __shared__ int count[4];
+  __shared__ Found told;
   __shared__ uint32_t red[4];
   const int t = threadIdx.x, h = blockIdx.y, side = blockIdx.z;
-  const SeqSlot s = find_slot(c, blockIdx.x, 1, c.P, 2);
+  const Found s = find_slot_256(c, blockIdx.x, div, per_seq, &told, count);
   if (s.rows <= 0) return;
-  const int64_t len = c.lens[s.b], start = len - s.rows;
+  const int64_t len = s.len, start = len - s.rows;
   const int64_t pg = max(start, (int64_t)0) / c.P + s.j;
   const int64_t lo = max(start, pg * c.P), hi = min(len, (pg + 1) * c.P);
   if (lo >= hi || pg >= c.max_pages) return;
   const int page = c.table[s.b * c.table_stride + pg];
-  if (page < 0 || page >= c.pages) return;
-  const int D = c.D, P = c.P, s0 = (int)(lo - pg * P), n = (int)(hi - lo);
+  const int D = c.D, P = c.P, s0 = (int)(lo - pg * P), n = (int)(hi - lo), per = D / 8;
   const int64_t ld = side ? ldv : ldk;
   const uint16_t* x = (side ? v_new : k_new) + (s.row0 + (lo - start)) * ld + (int64_t)h * D;
-  // largest magnitude of the new rows
-  const int per = D / 8;
-  uint32_t a = 0;
-  for (int i = t; i < n * per; i += 256) {
-    const v4u u = *reinterpret_cast<const v4u*>(x + (i / per) * ld + (i % per) * 8);
+  const int q0 = s0 / 4, nq = (s0 + n - 1) / 4 + 1 - q0;  // groups of four slots
+  const int units = side ? nq * per : (n * per + 3) / 4;
+  // piece e of unit i: its row (of the new ones here) and eighth of D; false if there is none
+  auto piece = [&](int i, int e, int& r, int& d8) __attribute__((always_inline)) {
+    if (side) {
+      r = 4 * (q0 + i % nq) + e - s0;
+      d8 = i / nq;
+      return i < units && r >= 0 && r < n;
+    }
+    const int at = (i & ~255) * 4 + e * 256 + (i & 255);
+    r = at / per;
+    d8 = at % per;
+    return r < n;
+  };
+  auto load = [&](int i, v4u (&u)[4]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) a = max(a, max(u[j] & 0x7FFFu, (u[j] >> 16) & 0x7FFFu));
+    for (int e = 0; e < 4; ++e) {
+      int r, d8;
+      u[e] = v4u{0, 0, 0, 0};
+      if (piece(i, e, r, d8)) u[e] = *reinterpret_cast<const v4u*>(x + r * ld + d8 * 8);
+    }
+  };
+  const int rounds = side ? (units + 255) / 256 : (n * per + 1023) / 1024;
+  v4u first[4];
+  load(t, first);
+  if (page < 0 || page >= c.pages) return;
+  uint8_t* scale = (side ? c.v_scale : c.k_scale) + (int64_t)page * c.H + h;
+  const int old = s0 > 0 ? *scale : 0;
+  // largest magnitude of the new rows
+  uint32_t a = 0;
+  auto largest = [&](const v4u (&u)[4]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a = max(a, max(u[e][j] & 0x7FFFu, (u[e][j] >> 16) & 0x7FFFu));
+  };
+  largest(first);
+  for (int k = 1; k < rounds; ++k) {
+    v4u u[4];
+    load(256 * k + t, u);
+    largest(u);
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) a = max(a, (uint32_t)__shfl_xor((int)a, o, 64));
   if ((t & 63) == 0) red[t >> 6] = a;
-  __syncthreads();
+  __syncthreads();  // and every thread has read the old byte
   a = max(max(red[0], red[1]), max(red[2], red[3]));
-  uint8_t* scale = (side ? c.v_scale : c.k_scale) + (int64_t)page * c.H + h;
-  const int old = s0 > 0 ? *scale : 0;
   const int byte = max(old, a < 0x7F80u ? block_exp<I8>(a) + 127 : 255);
-  __syncthreads();  // every thread has read the old byte
   if (t == 0) *scale = (uint8_t)byte;
   uint8_t* codes = static_cast<uint8_t*>(side ? c.v : c.k) + ((int64_t)page * c.H + h) * P * D;
   // keys: slot-major rows of D; values: D rows of P slots
-  const int slot_step = side ? 1 : D, d_step = side ? P : 1;
   if (s0 > 0 && old < byte && byte != 255) {
     for (int i = t; i < s0 * D; i += 256) {
       uint8_t* at = side ? codes + (int64_t)(i / s0) * P + i % s0 : codes + i;
       *at = (uint8_t)rescale<I8>(*at, old - byte);
     }
   }
-  for (int i = t; i < n * per; i += 256) {
-    const int r = i / per, d = (i % per) * 8;
-    const v4u u = *reinterpret_cast<const v4u*>(x + r * ld + d);
-    uint8_t* at = codes + (s0 + r) * slot_step + d * d_step;
+  const float f = byte == 255 ? 0.0f : ldexpf(1.0f, 127 - byte);  // a power of two: products are exact
+  auto store = [&](int i, v4u (&u)[4]) __attribute__((always_inline)) {
+    if (byte == 255) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = v4u{0, 0, 0, 0};  // NaN and infinities too: codes of zero
+    }
+    if (!side) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        int r, d8;
+        if (!piece(i, e, r, d8)) continue;
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = half_of(u[e], j) * f;
+        *reinterpret_cast<v2u*>(codes + (s0 + r) * D + d8 * 8) =
+            v2u{encode4<I8>(y[0], y[1], y[2], y[3]), encode4<I8>(y[4], y[5], y[6], y[7])};
+      }
+      return;
+    }
+    if (i >= units) return;
+    const int q = 4 * (q0 + i % nq);  // the group's first slot
+    uint8_t* at = codes + (int64_t)(i / nq) * 8 * P + q;
+    const bool whole = q >= s0 && q + 4 <= s0 + n;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float v = __uint_as_float((j & 1) ? u[j / 2] & 0xFFFF0000u : u[j / 2] << 16);
-      at[j * d_step] = byte == 255 ? 0 : (uint8_t)encode<I8>(ldexpf(v, 127 - byte));
+      const uint32_t w = encode4<I8>(half_of(u[0], j) * f, half_of(u[1], j) * f, half_of(u[2], j) * f, half_of(u[3], j) * f);
+      if (whole) {
+        *reinterpret_cast<uint32_t*>(at + j * P) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (q + e >= s0 && q + e < s0 + n) at[j * P + e] = (uint8_t)(w >> (8 * e));
+      }
     }
+  };
+  store(t, first);
+  for (int k = 1; k < rounds; ++k) {
+    v4u u[4];
+    load(256 * k + t, u);
+    store(256 * k + t, u);
   }
 }
 
@@ -973,11 +1084,15 @@ __global__ __launch_bounds__(64 * W) void k_kv_join(KvAttnArgs a) {
 
 hipError_t launch_kv_append(const KvArgs& c, bool i8, const uint16_t* k_new, int64_t ldk, const uint16_t* v_new,
                             int64_t ldv, hipStream_t st) {
-  const dim3 grid((unsigned)(c.T / c.P + 2 * (int64_t)c.B), (unsigned)c.H, 2);
+  // rows / P + 2 pages hold a sequence's rows, and no more than its rows: the host knows the sums only
+  const int64_t by_pages = c.T / c.P + 2 * (int64_t)c.B;
+  const bool by_rows = c.T <= by_pages;
+  const int div = by_rows ? 1 : c.P, per = by_rows ? 0 : 2;
+  const dim3 grid((unsigned)(by_rows ? c.T : by_pages), (unsigned)c.H, 2);
   if (i8)
-    hipLaunchKernelGGL(k_kv_append<true>, grid, dim3(256), 0, st, c, k_new, ldk, v_new, ldv);
+    hipLaunchKernelGGL(k_kv_append<true>, grid, dim3(256), 0, st, c, div, per, k_new, ldk, v_new, ldv);
   else
-    hipLaunchKernelGGL(k_kv_append<false>, grid, dim3(256), 0, st, c, k_new, ldk, v_new, ldv);
+    hipLaunchKernelGGL(k_kv_append<false>, grid, dim3(256), 0, st, c, div, per, k_new, ldk, v_new, ldv);
   return hipGetLastError();
 }
 

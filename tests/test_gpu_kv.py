@@ -118,6 +118,14 @@ def test_append_of_zeros_and_extremes(i8):
     _append_check(6, i8, 16, 64, 1, [2, 2, 1, 1], [2, 5, 3, 17], 2, spoil=spoil)
 
 
+@pytest.mark.parametrize("B, n", [(256, 1), (257, 2), (700, 40), (1, 3)])
+def test_append_to_many_sequences(B, n):
+    # more sequences than a workgroup asks for at once; fewer rows than pages they could need, and more
+    g = np.random.default_rng(B)
+    ns = (g.integers(1, n + 1, B) * (g.random(B) < 0.8)).tolist()
+    _append_check(B, True, 16, 64, 1, ns, [int(x) for x in np.array(ns) + g.integers(0, 40, B)], 5, extra=2)
+
+
 # ---- attention --------------------------------------------------------------------------------------
 
 

@@ -209,6 +209,66 @@ def test_every_new_row_has_one_slot(seed):
     assert sorted(got, key=str) == sorted(want, key=str)
 
 
+def find_slot_256(offsets, T, item, div, per):
+    """The same by rounds of 256 sequences, as append's workgroups search it."""
+    off = lambda b: min(max(int(offsets[b]), 0), T)  # noqa: E731
+    lo, span = 0, len(offsets) - 1
+    while True:
+        step = (span + 255) // 256
+        votes = sum(off(lo + i) // div + per * (lo + i) <= item for i in range(0, 256 * step, step) if i < span)
+        at = max(votes - 1, 0)
+        if step == 1:
+            base = off(lo + at) // div + per * (lo + at)
+            return lo + at, off(lo + at), 0 if item < base else off(lo + at + 1) - off(lo + at), max(item - base, 0)
+        lo, span = lo + at * step, min(step, span - at * step)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_slots_of_append_by_rows_or_by_pages(seed):
+    from oracle import kv_cache as kvo
+
+    g = np.random.default_rng(300 + seed)
+    B, page = int(g.choice([1, 5, 255, 256, 257, 600])), int(g.choice([16, 48]))
+    n = g.integers(0, int(g.choice([2, 3, 90])), B) * (g.random(B) < 0.7)
+    offsets = np.concatenate(([0], np.cumsum(n)))
+    T = int(offsets[-1] + g.integers(0, 5))
+    lens, max_pages = n + g.integers(-3, 90, B), int(g.integers(1, 9))
+    by_rows = T <= append_slots(T, B, page)
+    div, per = (1, 0) if by_rows else (page, 2)
+    got = []
+    for item in range(T if by_rows else append_slots(T, B, page)):
+        b, row0, rows, j = find_slot_256(offsets, T, item, div, per)
+        if rows <= 0:
+            continue
+        start = int(lens[b]) - rows
+        pg = max(start, 0) // page + j
+        lo, hi = max(start, pg * page), min(int(lens[b]), (pg + 1) * page)
+        if lo >= hi or pg >= max_pages:
+            continue
+        assert 0 <= row0 + lo - start and row0 + hi - start <= T
+        got.append((b, pg, lo - pg * page, range(lo - start, hi - start)))
+    want = [(b, *s) for b in range(B) for s in kvo.spans(int(n[b]), int(lens[b]), page, max_pages)]
+    assert sorted(got, key=str) == sorted(want, key=str)
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_append_of_offsets_that_hold_anything_stays_in_bounds(seed):
+    g = np.random.default_rng(400 + seed)
+    B, T, page = int(g.choice([1, 7, 300])), int(g.integers(1, 100)), 16
+    offsets, lens = g.integers(-50, 150, B + 1), g.integers(-20, 200, B)
+    for div, per in ((1, 0), (page, 2)):
+        for item in range(T if per == 0 else append_slots(T, B, page)):
+            b, row0, rows, j = find_slot_256(offsets, T, item, div, per)
+            assert 0 <= b < B
+            if rows <= 0:
+                continue
+            start = int(lens[b]) - rows
+            pg = max(start, 0) // page + j
+            lo, hi = max(start, pg * page), min(int(lens[b]), (pg + 1) * page)
+            if lo < hi:
+                assert 0 <= row0 + lo - start and row0 + hi - start <= T
+
+
 @pytest.mark.parametrize("seed", range(60))
 def test_every_query_row_has_one_tile(seed):
     g = np.random.default_rng(100 + seed)
