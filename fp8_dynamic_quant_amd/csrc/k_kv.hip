@@ -1007,77 +1007,140 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs16(KvAt
   }
 }
 
-// The items that runs cut: one workgroup for each (run that stands for one, row of the tile).  W
-// waves take every W-th part, with the weights of all parts in LDS first, and are added in order.
-template <int D, int W>
-__global__ __launch_bounds__(64 * W) void k_kv_join(KvAttnArgs a) {
+// The items that runs cut: the parts of one row, weighted by their maxima, over the weighted sum.
+struct JoinRow {
+  const KvAttnArgs& a;
+  KvJoin d;
+  int run, row;  // the run that stands for the item; row of the tile
+  __device__ __forceinline__ int64_t tile_row() const { return (int64_t)d.tile * a.tile_rows + row; }
+  __device__ __forceinline__ bool there() const { return d.parts > 0 && tile_row() < (int64_t)d.rows * a.R; }
+  __device__ __forceinline__ int64_t slot(int p) const {
+    return (int64_t)(p == 0 ? d.first_slot : 2 * (run - 1 + p)) * a.tile_rows + row;
+  }
+  // the parts' weights into LDS, their maximum and the sum, by W waves
+  template <int W>
+  __device__ __forceinline__ float2 weigh(float* wgt, float* red) const {
+    const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+    float M = -INFINITY;
+    for (int p = t; p < d.parts; p += 64 * W) {
+      const float m = a.stat[slot(p)].x;
+      wgt[p] = m;
+      M = fmaxf(M, m);
+    }
+    M = wave_max(M);
+    if constexpr (W > 1) {
+      if (lane == 0) red[wv] = M;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < W; ++w) M = fmaxf(M, red[w]);
+      __syncthreads();
+    }
+    const float Mb = M == -INFINITY ? 0.0f : M;
+    float L = 0.0f;
+    for (int p = t; p < d.parts; p += 64 * W) {
+      const float x = __builtin_amdgcn_exp2f(wgt[p] - Mb);
+      wgt[p] = x;
+      L += x * a.stat[slot(p)].y;
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) L += __shfl_xor(L, o, 64);
+    if (lane == 0) red[wv] = L;
+    __syncthreads();
+    L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) L += red[w];
+    return float2{M, L};
+  }
+  __device__ __forceinline__ float inverse(float2 ml) const { return ml.x == -INFINITY ? 0.0f : 1.0f / ml.y; }
+  __device__ __forceinline__ int64_t token() const { return (int64_t)d.row0 + (int)tile_row() / a.R; }
+  __device__ __forceinline__ int head() const { return d.h * a.R + (int)tile_row() % a.R; }
+  __device__ __forceinline__ void store_lse(float2 ml) const {
+    if (threadIdx.x == 0 && a.lse) a.lse[token() * (int64_t)(a.c.H * a.R) + head()] = log_sum(ml.x, ml.y);
+  }
+};
+
+// Few parts to an item: one wave for each (run, row), which goes over the parts in order.
+template <int D>
+__global__ __launch_bounds__(64) void k_kv_join(KvAttnArgs a) {
   constexpr int kAhead = 8, E = D / 64;  // parts in flight; elements of a lane
-  __shared__ float wgt[kMaxRuns + 1], o_lds[W][D], red[W];
-  const KvJoin d = a.joins[blockIdx.x + 1];
-  const int row = blockIdx.y, run = blockIdx.x + 1;
-  const int64_t rr = (int64_t)d.tile * a.tile_rows + row;
-  if (d.parts == 0 || rr >= (int64_t)d.rows * a.R) return;
-  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
-  auto slot_of = [&](int p) -> int64_t { return (int64_t)(p == 0 ? d.first_slot : 2 * (run - 1 + p)) * a.tile_rows + row; };
-  float M = -INFINITY;
-  for (int p = t; p < d.parts; p += 64 * W) {
-    const float m = a.stat[slot_of(p)].x;
-    wgt[p] = m;
-    M = fmaxf(M, m);
-  }
-  M = wave_max(M);
-  if constexpr (W > 1) {
-    if (lane == 0) red[wv] = M;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < W; ++w) M = fmaxf(M, red[w]);
-    __syncthreads();
-  }
-  const float Mb = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f;
-  for (int p = t; p < d.parts; p += 64 * W) {
-    const float x = __builtin_amdgcn_exp2f(wgt[p] - Mb);
-    wgt[p] = x;
-    L += x * a.stat[slot_of(p)].y;
-  }
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) L += __shfl_xor(L, o, 64);
-  if (lane == 0) red[wv] = L;
-  __syncthreads();
-  L = 0.0f;
-#pragma unroll
-  for (int w = 0; w < W; ++w) L += red[w];
+  __shared__ float wgt[kMaxRuns + 1], red[1];
+  const JoinRow r{a, a.joins[blockIdx.x + 1], (int)blockIdx.x + 1, (int)blockIdx.y};
+  if (!r.there()) return;
+  const int lane = threadIdx.x;
+  const float2 ml = r.template weigh<1>(wgt, red);
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-  for (int p0 = wv; p0 < d.parts; p0 += W * kAhead) {
+  for (int p0 = 0; p0 < r.d.parts; p0 += kAhead) {
     float v[kAhead][E];
 #pragma unroll
     for (int x = 0; x < kAhead; ++x) {
-      const float* from = a.part + slot_of(min(p0 + x * W, d.parts - 1)) * D + lane * E;
+      const float* from = a.part + r.slot(min(p0 + x, r.d.parts - 1)) * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; ++e) v[x][e] = from[e];
     }
 #pragma unroll
     for (int x = 0; x < kAhead; ++x)
-      if (p0 + x * W < d.parts) {
+      if (p0 + x < r.d.parts) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += wgt[p0 + x * W] * v[x][e];
+        for (int e = 0; e < E; ++e) acc[e] += wgt[p0 + x] * v[x][e];
       }
   }
-  const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
-  const int i = (int)rr / a.R, head = d.h * a.R + (int)rr % a.R;
-  uint16_t* out = a.out + ((int64_t)d.row0 + i) * a.ldo + (int64_t)head * D;
+  const float inv = r.inverse(ml);
+  uint16_t* out = a.out + r.token() * a.ldo + (int64_t)r.head() * D;
 #pragma unroll
-  for (int e = 0; e < E; ++e) o_lds[wv][lane * E + e] = acc[e];
-  __syncthreads();
-  for (int x = t; x < D; x += 64 * W) {
-    float v = o_lds[0][x];
-#pragma unroll
-    for (int w = 1; w < W; ++w) v += o_lds[w][x];
-    out[x] = (uint16_t)f32_to_bf16_nan(v * inv);
+  for (int e = 0; e < E; ++e) out[lane * E + e] = (uint16_t)f32_to_bf16_nan(acc[e] * inv);
+  r.store_lse(ml);
+}
+
+// Many parts to an item: blockIdx.x counts the items that were cut, blockIdx.y rows, blockIdx.z
+// slices of 64 columns.  16 lanes of four columns take a part, 16 parts go at a time, and the 16
+// sums are added in order.
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_join_wide(KvAttnArgs a) {
+  constexpr int kAhead = 8;
+  __shared__ float wgt[kMaxRuns + 1], red[4];
+  __shared__ v4f sums[16][16];
+  __shared__ int count[4], found;
+  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+  if (t == 0) found = 0;
+  int before = 0;
+  for (int w0 = 1; w0 < a.runs; w0 += 256) {  // the blockIdx.x-th run that stands for an item
+    const bool one = w0 + t < a.runs && a.joins[w0 + t].parts > 0;
+    const uint64_t votes = __ballot(one);
+    if (lane == 0) count[wv] = __popcll(votes);
+    __syncthreads();
+    int rank = before + __popcll(votes & (((uint64_t)1 << lane) - 1));
+    for (int w = 0; w < wv; ++w) rank += count[w];
+    if (one && rank == (int)blockIdx.x) found = w0 + t;
+    before += count[0] + count[1] + count[2] + count[3];
+    __syncthreads();
   }
-  if (a.lse && t == 0) a.lse[((int64_t)d.row0 + i) * (a.c.H * a.R) + head] = log_sum(M, L);
+  if (before <= (int)blockIdx.x) return;
+  const JoinRow r{a, a.joins[found], found, (int)blockIdx.y};
+  if (!r.there()) return;
+  const float2 ml = r.template weigh<4>(wgt, red);
+  const int col = blockIdx.z * 64 + (t & 15) * 4, mine = t >> 4;
+  v4f acc{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int p0 = mine; p0 < r.d.parts; p0 += 16 * kAhead) {
+    v4f v[kAhead];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x)
+      v[x] = *reinterpret_cast<const v4f*>(a.part + r.slot(min(p0 + 16 * x, r.d.parts - 1)) * D + col);
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x)
+      if (p0 + 16 * x < r.d.parts) acc += wgt[p0 + 16 * x] * v[x];
+  }
+  sums[mine][t & 15] = acc;
+  __syncthreads();
+  if (t < 16) {
+    for (int w = 1; w < 16; ++w) acc += sums[w][t];
+    const float inv = r.inverse(ml);
+    uint16_t* out = a.out + r.token() * a.ldo + (int64_t)r.head() * D + col;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = (uint16_t)f32_to_bf16_nan(acc[e] * inv);
+  }
+  if (blockIdx.z == 0) r.store_lse(ml);
 }
 
 }  // namespace
@@ -1105,7 +1168,7 @@ constexpr size_t kJoinBytes = 64u << 20;
 // How a call runs: row tiles of `rows` rows, whole (many rows), or in equal runs of the work.
 struct Shape {
   bool whole;
-  int rows, runs, least, cut, fixed;
+  int rows, runs, least, cut, fixed, items;
   bool wide_join;
 };
 
@@ -1129,12 +1192,13 @@ Shape shape_of(const KvArgs& c, int R, int num_cu) {
   s.cut = cap > (s.rows == 16 ? 4 * kAttnWaves : 8);
   s.least = !s.cut ? 1 : s.rows == 16 ? 2 * kAttnWaves : 4;
   s.fixed = s.rows == 16 ? 2 * kAttnWaves : 4;
-  const int most = (int)min((int64_t)min(kMaxRuns, 2 * num_cu), (int64_t)(kJoinBytes / ((size_t)2 * s.rows * (c.D * 4 + 8) + sizeof(KvJoin))));
+  const int most = (int)min((int64_t)min(kMaxRuns, (c.D == 256 ? 1 : 2) * num_cu), (int64_t)(kJoinBytes / ((size_t)2 * s.rows * (c.D * 4 + 8) + sizeof(KvJoin))));
   if (!s.cut) {
     s.runs = (int)min(items, (int64_t)1 << 30);
   } else {
     s.runs = (int)min((int64_t)most, (items * (cap + s.fixed) + s.least - 1) / s.least);
     s.wide_join = items * 8 < s.runs;  // many parts to an item
+    s.items = (int)min(items, (int64_t)s.runs);
   }
   return s;
 }
@@ -1171,9 +1235,9 @@ hipError_t attention_of(KvAttnArgs a, const Shape& s, hipStream_t st) {
     if (s.cut && s.runs > 1) {
       const dim3 grid((unsigned)(s.runs - 1), (unsigned)s.rows);
       if (s.wide_join)
-        hipLaunchKernelGGL((k_kv_join<D, 4>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL(k_kv_join_wide<D>, dim3((unsigned)s.items, (unsigned)s.rows, D / 64), dim3(256), 0, st, a);
       else
-        hipLaunchKernelGGL((k_kv_join<D, 1>), grid, dim3(64), 0, st, a);
+        hipLaunchKernelGGL(k_kv_join<D>, grid, dim3(64), 0, st, a);
     }
   }
   return hipGetLastError();
