@@ -136,7 +136,12 @@ __device__ __forceinline__ Found find_slot_256(const KvArgs& c, int64_t item, in
 // values (side 1).  A thread's share is four pieces of eight elements: of keys 256 pieces apart in
 // the order of memory, of values the four slots of an aligned group, whose codes are then whole
 // words of the value rows.  The first share stays in registers between the two passes (the
-// largest magnitude, the codes); larger pages read the others again.
+// largest magnitude, the codes); larger pages read the others again.  The codes are products with a
+// power of two, exact but for the one rounding to 8 bits.
+// Latency bounds it where rows are few: the sequence, its page, the page's scale, the codes in turn;
+// one token to each of 64 sequences of 8 x 128 heads takes 7.8 us (10.7 with a search by halves and a
+// workgroup for every two pages a sequence can touch).  2000 rows to each of three sequences: 12.2 us,
+// 24 MB, 2.0 TB/s (15.6 when values were stored a byte at a time and rows read twice).
 template <bool I8>
 __global__ __launch_bounds__(256) void k_kv_append(KvArgs c, int div, int per_seq, const uint16_t* k_new, int64_t ldk, const uint16_t* v_new,
                                                    int64_t ldv) {
@@ -725,7 +730,10 @@ __device__ __forceinline__ void store_rows(const KvAttnArgs& a, const Seq& s, Ro
 }
 
 // Many rows: a workgroup takes 64 RT rows of one sequence and cache head over all their keys.  A
-// sequence's last rows, which see most, come first.
+// sequence's last rows, which see most, come first.  The arithmetic around the matrix instructions
+// bounds it: for each 16 x 16 of scores a lane widens codes, scales, takes maximum, power of two and
+// rounding of four, beside 2 x D / 32 instructions of 16 clocks.  Two prompts of 2000 behind 2099, 32
+// query heads on 8 of 128: 255 us, 637 TFLOP/s of the 1376 that a bf16 product of 8192^3 reaches.
 template <int D, bool I8, int RT, int S>
 __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_rows(KvAttnArgs a) {
   using W = SharedRows<D, I8, RT, S>;
@@ -896,7 +904,9 @@ __device__ __forceinline__ void tell_join(const KvAttnArgs& a, const Plan& p, co
   a.joins[w] = d;
 }
 
-// 64-row tiles, each wave 16 rows of its own, keys shared through LDS
+// 64-row tiles, each wave 16 rows of its own, keys shared through LDS.  64 rows over 131072 tokens of
+// one head of 256: 34 us and 8 for the join, a fifth of the rate at which the codes could be read: a
+// CU has one run of eight steps, whose loads, widening and matrix instructions wait for each other.
 template <int D, bool I8, int S>
 __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs64(KvAttnArgs a) {
   using W = SharedRows<D, I8, 1, S>;
@@ -936,7 +946,9 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs64(KvAt
   }
 }
 
-// 16-row tiles: the waves share the rows and take steps in turn, and are joined in LDS
+// 16-row tiles: the waves share the rows and take steps in turn, and are joined in LDS.  Reading the
+// cache bounds it: 64 sequences of 8192 tokens, int8, 8 heads of 128, 584 MB in 123 us, 4.75 TB/s
+// with the joins; one sequence of 1000 takes 12.5 us, latencies of plan, page numbers and codes.
 template <int D, bool I8>
 __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs16(KvAttnArgs a) {
   constexpr int kRows = 16;
@@ -1177,18 +1189,24 @@ int rows_of_whole(int D) { return D == 256 ? 64 : 128; }
 Shape shape_of(const KvArgs& c, int R, int num_cu) {
   Shape s{};
   const int big = rows_of_whole(c.D);
-  // whole row tiles once they fill the chip twice over
-  if (c.T * R / big * c.H >= 2 * num_cu) {
+  // whole row tiles once they fill the chip (runs against whole tiles, us, 8 heads of 128, R = 4: at a
+  // tile a CU 1024 rows over 2048 tokens 84 / 70, over 16384 501 / 456; at half of that, 512 rows,
+  // over 2048 61 / 67, over 16384 283 / 449)
+  if (c.T * R / big * c.H >= num_cu) {
     s.whole = true;
     s.rows = big;
     return s;
   }
+  // 16-row tiles for sequences that have no more on average (16 against 64: one token of a sequence of
+  // 1000, 12.5 / 16.1 us; of each of 64 of 8192, 123 / 158), where the registers hold a head
   const int64_t avg = (c.T * R + c.B - 1) / c.B;
   s.rows = avg <= 16 && c.D < 256 ? 16 : 64;
   const int64_t B = min((int64_t)c.B, (int64_t)kPlanSeqs);
   const int64_t cap = ((int64_t)c.max_pages * c.P + kTokTile - 1) / kTokTile;  // steps of the longest sequence
   const int64_t items = (c.T * R / s.rows + B) * c.H;
-  // a sequence of few steps is not worth cutting: a run is an item then
+  // a sequence of few steps is not worth cutting: a run is an item then.  Heads of 256 get one run a
+  // CU: their parts are large (131072 tokens, 64 rows: 56 us with two, 43 with one; 8 sequences of
+  // 9000: 73 / 56)
   s.cut = cap > (s.rows == 16 ? 4 * kAttnWaves : 8);
   s.least = !s.cut ? 1 : s.rows == 16 ? 2 * kAttnWaves : 4;
   s.fixed = s.rows == 16 ? 2 * kAttnWaves : 4;

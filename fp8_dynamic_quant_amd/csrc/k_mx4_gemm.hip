@@ -28,7 +28,10 @@ __device__ __forceinline__ v8i regs8(const v4i lo, const v4i hi) {
 // ---- few rows: the weights stream past ------------------------------------------------------
 // A workgroup makes up to 16 rows x 16 CT columns of one group over all of K: eight waves
 // take eight runs of 128-deep steps, operands straight from memory into registers (each byte of
-// the weights is read once), and add their f32 sums in LDS in wave order.
+// the weights is read once), and add their f32 sums in LDS in wave order.  What bounds it is the
+// latency of one round of loads, at large sizes the weights' stream: M=1 N=1024 K=4096 takes 3.1 us
+// (1.7 of them any kernel's), M=1 G=8 N=1024 K=4096 5.5 us (17.8 MB, 3.25 TB/s), M=1 N=8192 K=8192
+// 8.4 us (4.2 TB/s).
 constexpr int kFewWaves = 8, kFewSteps = 4;  // and steps whose operands are in flight together
 
 template <bool A8, int CT>
@@ -109,7 +112,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(Mx4Args p) {
 // 64 WM x 64 WN outputs for a workgroup of four waves (2 x 2, 32 WM x 32 WN each, of 32 x 32
 // instructions).  128-deep slices of both operands and of their scale words go global -> LDS
 // by DMA into a ring of S stages, S - 1 ahead; two workgroups share a CU, so that one's
-// epilogue runs beside the other's matrix instructions.
+// epilogue runs beside the other's matrix instructions.  With KS = 2 a second four waves take the
+// odd slices (a slice of a 64 x 64 tile is a chain of wait, barrier, LDS read and two dependent
+// instructions, which two halves go through side by side: M=64 G=8 N=1024 K=4096 11.8 -> 10.6 us),
+// and their sums are added through LDS.
+// What bounds it: with large tiles LDS, whose reads and DMA writes take about as many clocks as the
+// 4-bit matrix instructions (M=8192 N=32768 K=1024: 236 - 250 us, 2.2 - 2.3 PFLOP/s; 256 x 256 tiles,
+// which read less from L2, were no faster: 269); with small ones the chain of a slice and the reads
+// of both operands from L2 (M=64 G=8 N=1024 K=4096: 10.6 us, 2.0 TB/s).  Outputs are stored past
+// the caches: they would drive out operands (269 -> 250 us at M=8192).
 //
 // A 4-bit row's slice is 64 bytes, four chunks of 16; four rows make a 256-byte line of LDS
 // (all its banks), and a chunk is XORed with bits 2..3 of its row, so that sixteen rows read at
@@ -336,7 +347,18 @@ hipError_t tile(const Mx4Args& a, hipStream_t st) {
 
 template <bool A8>
 hipError_t launch(const Mx4Args& a, int num_cu, hipStream_t st) {
-  if (a.M <= 16) return (int64_t)a.N / 16 * a.batch >= 2 * num_cu ? few<A8, 2>(a, st) : few<A8, 1>(a, st);
+  // Tiles of 64 x 64, 64 x 128 or 128 x 256: the largest that still give every CU one, since what a
+  // CU reads for an output shrinks with the tile (64 x 64 against 64 x 128, us: M=64 G=8 N=1024
+  // K=4096 10.6 / 14.1, M=1000 N=2064 K=1152 13.8 / 9.2; 64 x 128 against 128 x 256: M=2048 N=4096
+  // K=4096 36.7 / 28.0, M=8192 N=32768 K=1024 308 / 246).
+  const int64_t narrow = (int64_t)((a.M + 63) / 64) * ((a.N + 63) / 64) * a.batch;
+  // Up to 16 rows the streaming kernel, unless 64-column tiles fill the chip by themselves (streaming
+  // against tiles, us: M=16 G=8 N=1024 K=4096 6.7 / 8.9, M=1 N=8192 K=8192 8.5 / 12.0; at 256 tiles
+  // M=1 N=16384 K=4096 7.9 / 8.1, M=16 8.9 / 8.3; at 512 M=1 N=32768 K=1024 11.2 / 5.9, M=16
+  // K=8192 40.6 / 34.5).  32 columns to a workgroup where two a CU remain, else 16 (16 against 32:
+  // M=16 G=8 N=1024 K=4096 8.3 / 6.7, M=1 N=1024 K=4096 3.1 / 4.1).
+  if (a.M <= 16 && narrow < num_cu)
+    return (int64_t)a.N / 16 * a.batch >= 2 * num_cu ? few<A8, 2>(a, st) : few<A8, 1>(a, st);
   const int64_t large = (int64_t)((a.M + 127) / 128) * ((a.N + 255) / 256) * a.batch;
   if (large >= num_cu) return tile<A8, 2, 4, A8 ? 2 : 3, 1>(a, st);
   const int64_t small = (int64_t)((a.M + 63) / 64) * ((a.N + 127) / 128) * a.batch;

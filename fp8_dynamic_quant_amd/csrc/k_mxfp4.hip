@@ -24,7 +24,12 @@ __device__ __forceinline__ int e2m1_exp(uint32_t a) {
 
 // Both kernels: a wave takes 512 consecutive elements of one group in four consecutive tokens, a
 // workgroup 16 tokens of them.  Lane l holds 8 elements (16 bytes of bf16, 4 of codes) of each token,
-// four lanes a block, 16 lanes a scale word; the four tokens' words are 16 consecutive bytes.
+// four lanes a block, 16 lanes a scale word; the four tokens' words are 16 consecutive bytes (a word a
+// token, written by itself, and one token a wave took 38.6 us instead of 31 for both kernels on 8192
+// tokens of 4096).  Memory bounds both: quantising and back at that size moves 152 MB, 4.9 TB/s, the
+// rate of a large copy; one token of 8 x 4096 takes 4.2 us for both, which is launch and one latency.
+// x and codes are read, y is written once: streaming accesses.  Codes and scales stay cached for the
+// product that reads them.
 struct Share {
   int g, p, h;   // group; this 16-lane row's scale word, this quad's block
   int64_t t0;    // the first of the wave's four tokens

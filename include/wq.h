@@ -365,8 +365,8 @@ typedef struct {
  *   the new codes are RN(x * 2^(127 - byte)) (nearest-even).  Slots behind them keep their codes.
  * A NaN or an infinity among the rows makes the byte 255 (UE8M0's NaN) and their codes zero:
  * the page's tokens of that head read as NaN until the page is begun anew.
- * The same call again writes the same bytes.  A page written by the call is in the table of
- * one sequence only (a shared one is copied first). */
+ * The same call again writes the same bytes.  A page written by the call stands in one place
+ * of the tables (a shared one is copied first). */
 int wq_kv_append(wq_ctx* ctx, const wq_kv_cache* cache, const void* k_new, int64_t ldk, const void* v_new, int64_t ldv,
                  int64_t T, int64_t B, const int64_t* offsets, const int32_t* lens, void* stream);
 

@@ -235,6 +235,14 @@ def test_attention_long_sequences(i8, ns):
     _attend_check(11, i8, 64, 64, 1, 4, ns, [3000, 1985], 47)
 
 
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_sequences_in_many_and_in_few_parts(i8, D):
+    # few items in parts of a step or two each; more items than an eighth of the runs
+    _attend_check(13, i8, 64, D, 2, 3, [1, 40], [3000, 1985], 47, extra=2)
+    _attend_check(14, i8, 64, D, 2, 3, [1] * 20, [60 * b + 5 for b in range(20)], 20)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attention_scales_and_scores_far_apart(D):
     # values' scales over forty powers of two between pages, a negative and a zero score scale
