@@ -905,7 +905,7 @@ __device__ __forceinline__ void tell_join(const KvAttnArgs& a, const Plan& p, co
 }
 
 // 64-row tiles, each wave 16 rows of its own, keys shared through LDS.  64 rows over 131072 tokens of
-// one head of 256: 34 us and 8 for the join, a fifth of the rate at which the codes could be read: a
+// one head of 256: 33 us and 8 for the join, a third of the rate at which the codes could be read: a
 // CU has one run of eight steps, whose loads, widening and matrix instructions wait for each other.
 template <int D, bool I8, int S>
 __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs64(KvAttnArgs a) {

@@ -907,12 +907,12 @@ int wq_kv_append(wq_ctx* c, const wq_kv_cache* k, const void* k_new, int64_t ldk
   return status_of(e);
 }
 
-// q_heads a multiple of the cache's heads; row tiles are counted in 32 bits, their steps of 64
-// tokens in 52
+// q_heads a multiple of the cache's heads; a cache head's rows and the row tiles are counted in 32
+// bits, the tiles' steps of 64 tokens in 52
 static bool kv_heads_ok(const wq_kv_cache* k, int64_t q_heads, int64_t T, int64_t B) {
   if (q_heads < k->heads || q_heads % k->heads != 0 || q_heads > (1 << 20)) return false;
-  const int64_t tiles = (T * (q_heads / k->heads) / 16 + B) * k->heads;
-  return tiles < ((int64_t)1 << 31) && (double)tiles * ((double)k->max_pages * k->page_tokens / 64 + 16) < 4503599627370496.0;
+  const int64_t rows = T * (q_heads / k->heads), tiles = (rows / 16 + B) * k->heads;
+  return rows < ((int64_t)1 << 31) && tiles < ((int64_t)1 << 31) && (double)tiles * ((double)k->max_pages * k->page_tokens / 64 + 16) < 4503599627370496.0;
 }
 
 int64_t wq_kv_attention_workspace_bytes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B) {

@@ -243,6 +243,16 @@ def test_attention_sequences_in_many_and_in_few_parts(i8, D):
     _attend_check(14, i8, 64, D, 2, 3, [1] * 20, [60 * b + 5 for b in range(20)], 20)
 
 
+@pytest.mark.parametrize("max_pages", [1, 18])
+def test_attention_of_more_sequences_than_a_launch_plans(max_pages):
+    # items, and runs that are cut, each in two launches
+    g = np.random.default_rng(15)
+    lens = [int(x) for x in g.integers(0, 65, 1100)]
+    for b in (3, 1023, 1024, 1099):
+        lens[b] = 64 * max_pages - b % 5
+    _attend_check(15, True, 64, 64, 1, 1, [int(x) for x in g.integers(0, 2, 1100)], lens, max_pages)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attention_scales_and_scores_far_apart(D):
     # values' scales over forty powers of two between pages, a negative and a zero score scale

@@ -151,6 +151,20 @@ def test_product_of_many_tiles(M, G, N, K, a8):
 
 
 @pytest.mark.parametrize("a8", [False, True])
+@pytest.mark.parametrize("M, G, N, K", [(1, 1, 16400, 128), (5, 1, 16400, 384), (16, 8, 2064, 256), (1, 2, 8208, 640), (3, 40, 16, 128)])
+def test_product_of_few_rows_and_many_columns(M, G, N, K, a8):
+    _product(M, G, N, K, a8)
+
+
+@pytest.mark.parametrize("a8", [False, True])
+@pytest.mark.parametrize("K", [128, 256, 384, 1152])
+@pytest.mark.parametrize("M, N", [(17, 16), (33, 80), (70, 208)])
+def test_product_of_narrow_tiles_at_every_depth(M, N, K, a8):
+    # one slice (none for the second half of a workgroup), two, three, nine
+    _product(M, 2, N, K, a8)
+
+
+@pytest.mark.parametrize("a8", [False, True])
 @pytest.mark.parametrize("M, G, N, K", [(3, 2, 64, 256), (40, 1, 208, 512), (200, 3, 176, 384), (384, 1, 768, 640)])
 def test_product_of_wide_scales_in_wider_buffers(M, G, N, K, a8):
     _product(M, G, N, K, a8, spread=4.0, pad=48, ypad=24, tokens=8)
