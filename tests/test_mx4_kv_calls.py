@@ -129,6 +129,13 @@ def test_attention_workspace(ctx):
     assert L.wq_kv_attention_workspace_bytes(None, ctypes.byref(one), 1, 8, 1) == -NULL
 
 
+def test_attention_refuses_rows_beyond_31_bits(ctx):
+    one = _cache(heads=1)
+    need = lambda T, heads: wq.lib().wq_kv_attention_workspace_bytes(ctx, ctypes.byref(one), T, heads, 1)  # noqa: E731
+    assert need(1 << 27, 16) == -SHAPE and need((1 << 27) - 1, 16) >= 0
+    assert _attend(ctx, one, T=1 << 30, heads=2, ldq=1 << 20, ldo=1 << 20) == SHAPE
+
+
 def test_binding_refusals():
     x = torch.zeros((3, 1, 64), dtype=torch.bfloat16)
     for bad in (x.float(), x[0], x.transpose(0, 2), torch.zeros((3, 1, 48), dtype=torch.bfloat16)):
