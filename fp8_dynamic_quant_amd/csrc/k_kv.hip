@@ -7,8 +7,9 @@
 // come from memory in operand order and nothing is transposed when they are read.
 #include <type_traits>
 
-#include "wq_device.h"
+#include "wq_dma.h"
 #include "wq_kernels.h"
+#include "wq_mx4_kv.h"
 
 namespace wq {
 

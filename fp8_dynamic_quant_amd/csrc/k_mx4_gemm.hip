@@ -10,8 +10,9 @@
 // scale operand of lane group s applies to K 32s .. 32s+31 of either.
 #include <type_traits>
 
-#include "wq_device.h"
+#include "wq_dma.h"
 #include "wq_kernels.h"
+#include "wq_mx4_kv.h"
 
 namespace wq {
 

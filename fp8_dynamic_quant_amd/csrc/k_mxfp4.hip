@@ -6,7 +6,7 @@
 // scales have the layout of the 8-bit blocks: four bytes to an int32 word, one word for the
 // 128 elements that a matrix instruction takes, [G, ceil(D / 128), align4(T)].
 #include "wq_device.h"
-#include "wq_kernels.h"
+#include "wq_mx4_kv.h"
 
 namespace wq {
 

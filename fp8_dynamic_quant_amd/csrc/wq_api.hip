@@ -23,6 +23,7 @@
 
 #include "../../include/wq.h"
 #include "wq_kernels.h"
+#include "wq_mx4_kv.h"
 
 struct wq_ctx {
   int device;
