@@ -101,6 +101,8 @@ EXPORTS = {
                                        _c_void_p, _c_void_p, ctypes.c_float, ctypes.c_int, _c_void_p, _i64,
                                        _c_void_p, _c_void_p, ctypes.c_size_t, _c_void_p]),
     "wq_kv_attention_workspace_bytes": (_i64, [_c_void_p, ctypes.POINTER(KvCacheDesc), _i64, _i64, _i64]),
+    "wq_kv_attention_path": (ctypes.c_int, [_c_void_p, ctypes.POINTER(KvCacheDesc), _i64, _i64, _i64]),
+    "wq_mx4_path": (ctypes.c_int, [_c_void_p, _i64, _i64, _i64, _i64]),
     "wq_pack_weight_i8": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p]),
     "wq_fused_quant_matmul_packed": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p,
                                                     _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p,
@@ -505,6 +507,24 @@ def wq_kv_attention(cache: KvCache, q: torch.Tensor, offsets, lens, table, *, sc
     if st:
         _check("wq_kv_attention", st)
     return (out, lse) if lse is not None else out
+
+
+def wq_kv_attention_path(cache: KvCache, T: int, q_heads: int, table) -> int:
+    """Which kernels wq_kv_attention takes for T rows of q_heads heads (the numbers stand in wq.h)."""
+    pages, heads, page_tokens, D = cache.k.shape
+    d = KvCacheDesc(WQ_KV_E4M3, pages, heads, page_tokens, D, None, None, None, None, None, table.shape[1], table.shape[1])
+    r = lib().wq_kv_attention_path(context(cache.k.device).handle, ctypes.byref(d), T, q_heads, table.shape[0])
+    if r < 0:
+        _check("wq_kv_attention_path", -r)
+    return r
+
+
+def wq_mx4_path(M: int, N: int, K: int, groups: int = 1, device=None) -> int:
+    """Which kernel a product on 4-bit weights takes (the numbers stand in wq.h)."""
+    r = lib().wq_mx4_path(context(device if device is not None else "cuda").handle, M, N, K, groups)
+    if r < 0:
+        _check("wq_mx4_path", -r)
+    return r
 
 
 def wq_fused_quant_matmul(x, w, w_scale, *, y=None, x_q_out=None, x_scale_out=None, acc_out=None):

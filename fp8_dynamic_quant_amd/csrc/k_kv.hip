@@ -1269,9 +1269,9 @@ size_t kv_attention_workspace(const KvArgs& c, int R, int num_cu) {
   return s.cut ? (size_t)s.runs * ((size_t)2 * s.rows * (c.D * 4 + 8) + sizeof(KvJoin)) : 0;
 }
 
-const char* kv_attention_kind(const KvArgs& c, int R, int num_cu) {
+int kv_attention_path(const KvArgs& c, int R, int num_cu) {
   const Shape s = shape_of(c, R, num_cu);
-  return s.whole ? "row tiles" : s.cut ? "equal runs" : "items";
+  return s.whole ? 1 : (s.cut ? 4 : 2) + (s.rows == 64) + (s.wide_join ? 8 : 0);
 }
 
 hipError_t launch_kv_attention(KvAttnArgs a, bool i8, int num_cu, void* ws, hipStream_t st) {

@@ -347,30 +347,39 @@ hipError_t tile(const Mx4Args& a, hipStream_t st) {
 }
 
 template <bool A8>
-hipError_t launch(const Mx4Args& a, int num_cu, hipStream_t st) {
+hipError_t launch(const Mx4Args& a, int path, hipStream_t st) {
+  switch (path) {
+    case 1: return few<A8, 1>(a, st);
+    case 2: return few<A8, 2>(a, st);
+    case 3: return tile<A8, 1, 1, 4, 2>(a, st);
+    case 4: return tile<A8, 1, 2, 4, 1>(a, st);
+    default: return tile<A8, 2, 4, A8 ? 2 : 3, 1>(a, st);
+  }
+}
+
+}  // namespace
+
+int mx4_path(int M, int N, int batch, int num_cu) {
   // Tiles of 64 x 64, 64 x 128 or 128 x 256: the largest that still give every CU one, since what a
   // CU reads for an output shrinks with the tile (64 x 64 against 64 x 128, us: M=64 G=8 N=1024
   // K=4096 10.6 / 14.1, M=1000 N=2064 K=1152 13.8 / 9.2; 64 x 128 against 128 x 256: M=2048 N=4096
   // K=4096 36.7 / 28.0, M=8192 N=32768 K=1024 308 / 246).
-  const int64_t narrow = (int64_t)((a.M + 63) / 64) * ((a.N + 63) / 64) * a.batch;
+  const int64_t narrow = (int64_t)((M + 63) / 64) * ((N + 63) / 64) * batch;
   // Up to 16 rows the streaming kernel, unless 64-column tiles fill the chip by themselves (streaming
   // against tiles, us: M=16 G=8 N=1024 K=4096 6.7 / 8.9, M=1 N=8192 K=8192 8.5 / 12.0; at 256 tiles
   // M=1 N=16384 K=4096 7.9 / 8.1, M=16 8.9 / 8.3; at 512 M=1 N=32768 K=1024 11.2 / 5.9, M=16
   // K=8192 40.6 / 34.5).  32 columns to a workgroup where two a CU remain, else 16 (16 against 32:
   // M=16 G=8 N=1024 K=4096 8.3 / 6.7, M=1 N=1024 K=4096 3.1 / 4.1).
-  if (a.M <= 16 && narrow < num_cu)
-    return (int64_t)a.N / 16 * a.batch >= 2 * num_cu ? few<A8, 2>(a, st) : few<A8, 1>(a, st);
-  const int64_t large = (int64_t)((a.M + 127) / 128) * ((a.N + 255) / 256) * a.batch;
-  if (large >= num_cu) return tile<A8, 2, 4, A8 ? 2 : 3, 1>(a, st);
-  const int64_t small = (int64_t)((a.M + 63) / 64) * ((a.N + 127) / 128) * a.batch;
-  if (small >= num_cu) return tile<A8, 1, 2, 4, 1>(a, st);
-  return tile<A8, 1, 1, 4, 2>(a, st);
+  if (M <= 16 && narrow < num_cu) return (int64_t)N / 16 * batch >= 2 * num_cu ? 2 : 1;
+  const int64_t large = (int64_t)((M + 127) / 128) * ((N + 255) / 256) * batch;
+  if (large >= num_cu) return 5;
+  const int64_t small = (int64_t)((M + 63) / 64) * ((N + 127) / 128) * batch;
+  return small >= num_cu ? 4 : 3;
 }
 
-}  // namespace
-
 hipError_t launch_mx4(const Mx4Args& a, bool a8, int num_cu, hipStream_t st) {
-  return a8 ? launch<true>(a, num_cu, st) : launch<false>(a, num_cu, st);
+  const int path = mx4_path(a.M, a.N, a.batch, num_cu);
+  return a8 ? launch<true>(a, path, st) : launch<false>(a, path, st);
 }
 
 }  // namespace wq

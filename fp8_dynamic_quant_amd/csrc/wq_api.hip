@@ -613,12 +613,21 @@ static int fp8_matmul(wq_ctx* c, const wq_matmul_desc* d, hipStream_t st) {
   return status_of(e);
 }
 
+static bool mx4_shape_ok(int64_t N, int64_t K, int64_t G) { return N % 16 == 0 && K % 128 == 0 && K <= 131072 && G <= 65535; }
+
+int wq_mx4_path(const wq_ctx* c, int64_t M, int64_t N, int64_t K, int64_t G) {
+  if (!c) return -WQ_ERR_NULL;
+  if (M < 0 || N <= 0 || K <= 0 || G < 1 || M > (int64_t)1 << 30 || N > (int64_t)1 << 30 || !mx4_shape_ok(N, K, G))
+    return -WQ_ERR_SHAPE;
+  return M == 0 ? 0 : wq::mx4_path((int)M, (int)N, (int)G, c->num_cu);
+}
+
 static int mx4_matmul(wq_ctx* c, const wq_matmul_desc* d, hipStream_t st) {
   const int64_t M = d->M, N = d->N, K = d->K, G = d->batch;
   if (d->seg_offsets || d->acc_out || d->epilogue != WQ_EPI_BF16) return WQ_ERR_UNSUPPORTED;
   const bool a8 = d->payload == WQ_PAYLOAD_MXFP8_W4;
   const int64_t row = a8 ? K : K / 2;  // bytes of an activation row
-  if (N % 16 != 0 || K % 128 != 0 || K > 131072 || G > 65535) return WQ_ERR_SHAPE;
+  if (!mx4_shape_ok(N, K, G)) return WQ_ERR_SHAPE;
   // 128 rows of a tile are addressed by 32-bit offsets
   if (d->lda < row || d->lda >= (1 << 23) || d->ldy < N || d->a_batch_stride < 0 || d->y_batch_stride < 0 || d->b_batch_stride < 0)
     return WQ_ERR_SHAPE;
@@ -644,8 +653,8 @@ static int mx4_matmul(wq_ctx* c, const wq_matmul_desc* d, hipStream_t st) {
   t.M = (int)M; t.N = (int)N; t.K = (int)K; t.batch = (int)G;
   hipError_t e = wq::launch_mx4(t, a8, c->num_cu, st);
   if (c->log)
-    std::fprintf(stderr, "[wq] quant_matmul %s M=%lld N=%lld K=%lld groups=%lld\n", a8 ? "mxfp8 x mxfp4" : "mxfp4",
-                 (long long)M, (long long)N, (long long)K, (long long)G);
+    std::fprintf(stderr, "[wq] quant_matmul %s M=%lld N=%lld K=%lld groups=%lld: path %d\n", a8 ? "mxfp8 x mxfp4" : "mxfp4",
+                 (long long)M, (long long)N, (long long)K, (long long)G, wq::mx4_path(t.M, t.N, t.batch, c->num_cu));
   return e == hipErrorInvalidValue ? WQ_ERR_SHAPE : status_of(e);
 }
 
@@ -916,21 +925,33 @@ static bool kv_heads_ok(const wq_kv_cache* k, int64_t q_heads, int64_t T, int64_
   return rows < ((int64_t)1 << 31) && tiles < ((int64_t)1 << 31) && (double)tiles * ((double)k->max_pages * k->page_tokens / 64 + 16) < 4503599627370496.0;
 }
 
-int64_t wq_kv_attention_workspace_bytes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B) {
+// the sizes that choose attention's kernels: 0, 1 for an empty problem, or -status
+static int kv_sizes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B, wq::KvArgs* a) {
   if (!c || !k) return -WQ_ERR_NULL;
   if (k->heads < 1 || k->page_tokens < 16 || k->page_tokens > 256 || k->max_pages < 1 || k->max_pages > INT32_MAX ||
       !wq::kv_head_dim_ok(k->head_dim) || T < 0 || B < 0 || T > ((int64_t)1 << 30) || B > ((int64_t)1 << 24) ||
       !kv_heads_ok(k, q_heads, T, B))
     return -WQ_ERR_SHAPE;
-  if (T == 0 || B == 0) return 0;
+  if (T == 0 || B == 0) return 1;
+  a->H = (int)k->heads;
+  a->P = (int)k->page_tokens;
+  a->D = (int)k->head_dim;
+  a->max_pages = (int)k->max_pages;
+  a->B = (int)B;
+  a->T = T;
+  return 0;
+}
+
+int64_t wq_kv_attention_workspace_bytes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B) {
   wq::KvArgs a{};
-  a.H = (int)k->heads;
-  a.P = (int)k->page_tokens;
-  a.D = (int)k->head_dim;
-  a.max_pages = (int)k->max_pages;
-  a.B = (int)B;
-  a.T = T;
+  if (int r = kv_sizes(c, k, T, q_heads, B, &a)) return r < 0 ? r : 0;
   return (int64_t)wq::kv_attention_workspace(a, (int)(q_heads / k->heads), c->num_cu);
+}
+
+int wq_kv_attention_path(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B) {
+  wq::KvArgs a{};
+  if (int r = kv_sizes(c, k, T, q_heads, B, &a)) return r < 0 ? r : 0;
+  return wq::kv_attention_path(a, (int)(q_heads / k->heads), c->num_cu);
 }
 
 int wq_kv_attention(wq_ctx* c, const wq_kv_cache* k, const void* q, int64_t ldq, int64_t T, int64_t q_heads, int64_t B,
@@ -963,9 +984,9 @@ int wq_kv_attention(wq_ctx* c, const wq_kv_cache* k, const void* q, int64_t ldq,
   hipError_t e = wq::launch_kv_attention(a, k->code == WQ_KV_INT8, c->num_cu, workspace,
                                          static_cast<hipStream_t>(stream));
   if (c->log)
-    std::fprintf(stderr, "[wq] kv_attention %s T=%lld B=%lld heads=%lld/%lld D=%lld page=%lld: %s\n",
+    std::fprintf(stderr, "[wq] kv_attention %s T=%lld B=%lld heads=%lld/%lld D=%lld page=%lld: path %d\n",
                  k->code == WQ_KV_INT8 ? "int8" : "e4m3", (long long)T, (long long)B, (long long)q_heads,
-                 (long long)k->heads, (long long)k->head_dim, (long long)k->page_tokens, wq::kv_attention_kind(a.c, a.R, c->num_cu));
+                 (long long)k->heads, (long long)k->head_dim, (long long)k->page_tokens, wq::kv_attention_path(a.c, a.R, c->num_cu));
   return status_of(e);
 }
 

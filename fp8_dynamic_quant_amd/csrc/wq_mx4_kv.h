@@ -31,6 +31,8 @@ struct Mx4Args {
 };
 // a8: E4M3 activation codes instead of E2M1 pairs
 hipError_t launch_mx4(const Mx4Args& a, bool a8, int num_cu, hipStream_t st);
+// its kernel, as wq_mx4_path numbers them
+int mx4_path(int M, int N, int batch, int num_cu);
 
 // The paged 8-bit cache (k_kv.hip).  A page holds P tokens of every head: k [page][H][P][D],
 // v [page][H][D][P], one UE8M0 byte for each (page, head) of either.
@@ -73,8 +75,9 @@ struct KvAttnArgs {
   KvJoin* joins;
 };
 bool kv_head_dim_ok(int64_t D);
-// how a call of these sizes runs, and the bytes that joining cut items takes
-const char* kv_attention_kind(const KvArgs& c, int R, int num_cu);
+// how a call of these sizes runs, as wq_kv_attention_path numbers it, and the bytes that joining
+// cut items takes
+int kv_attention_path(const KvArgs& c, int R, int num_cu);
 size_t kv_attention_workspace(const KvArgs& c, int R, int num_cu);
 hipError_t launch_kv_attention(KvAttnArgs a, bool i8, int num_cu, void* ws, hipStream_t st);
 

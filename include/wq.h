@@ -267,6 +267,12 @@ typedef struct {
 
 int wq_quant_matmul(wq_ctx* ctx, const wq_matmul_desc* desc, void* stream);
 
+/* Which kernel a product on 4-bit weights (WQ_PAYLOAD_MXFP4, WQ_PAYLOAD_MXFP8_W4) of these sizes
+ * takes: the weights' stream in 1 = 16 or 2 = 32 columns a workgroup, or tiles of 3 = 64 x 64,
+ * 4 = 64 x 128 or 5 = 128 x 256 outputs.  0 for an empty problem; a negative value is -status.
+ * Host only: no device work. */
+int wq_mx4_path(const wq_ctx* ctx, int64_t M, int64_t N, int64_t K, int64_t batch);
+
 /* ---- fused quant + INT8 GEMM -------------------------------------------------------
  * The whole chain of section 一 of the W8A8 article: per-token quant of the bf16 x [M, K]
  * (row stride ldx), the INT8 GEMM against w [N, K] and the bf16 epilogue.  Outputs are
@@ -393,6 +399,14 @@ int wq_kv_attention(wq_ctx* ctx, const wq_kv_cache* cache, const void* q, int64_
  * negative value is -status.  Host only: no device work. */
 int64_t wq_kv_attention_workspace_bytes(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T, int64_t q_heads,
                                         int64_t B);
+
+/* Which kernels wq_kv_attention takes for these sizes (read as for the workspace):
+ *   1  whole row tiles of 128 rows (64 for heads of 256) of one sequence and head
+ *   2, 3  16-row, 64-row tiles, a workgroup for each (sequence, head, tile)
+ *   4, 5  16-row, 64-row tiles, their work cut into equal runs, with a join of the parts;
+ *   8 more where the items are few and their parts many, so that a join is split over columns.
+ * 0 for an empty problem; a negative value is -status.  Host only: no device work. */
+int wq_kv_attention_path(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T, int64_t q_heads, int64_t B);
 
 /* ---- expert sort (MoE) ---------------------------------------------------------------
  * "DeepSeek V4 950" section 3.2: sort the (token, slot) pairs by expert id before the
