@@ -704,9 +704,13 @@ struct SharedRows {
   }
 };
 
+// The log-sum-exp of maximum m (log2) and sum l, and what the weighted values are multiplied by.  A
+// row that saw no token has l = 0 and gets -inf and zeros.  The maximum does not tell: it passes
+// over NaN, so that it stays -inf too where all that a row saw was NaN.  The sum keeps NaN.
 __device__ __forceinline__ float log_sum(float m, float l) {
-  return m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
+  return (m + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f;
 }
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
 // A wave's own rows, whole: lane (j, g) holds of row j the elements 16 i + 4 g .. + 3
 template <int D, bool I8, int RT>
@@ -718,7 +722,7 @@ __device__ __forceinline__ void store_rows(const KvAttnArgs& a, const Seq& s, Ro
     const int64_t rr = r0 + 16 * rt + j;
     if (rr >= s.nrows) continue;
     const int i = (int)rr / a.R, head = h * a.R + (int)rr % a.R;
-    const float inv = w.mx[rt] == -INFINITY ? 0.0f : 1.0f / l;
+    const float inv = inverse_sum(l);
     uint16_t* out = a.out + (s.row0 + i) * a.ldo + (int64_t)head * D + 4 * g;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
@@ -997,7 +1001,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_runs16(KvAt
         wgt[x] = __builtin_amdgcn_exp2f(m_lds[x][row] - Mb);
         L += wgt[x] * l_lds[x][row];
       }
-      const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
+      const float inv = inverse_sum(L);
       const int i = (int)rr / a.R, head = r.it.h * a.R + (int)rr % a.R;
       vE v = 0.0f;
 #pragma unroll
@@ -1064,7 +1068,6 @@ struct JoinRow {
     for (int w = 0; w < W; ++w) L += red[w];
     return float2{M, L};
   }
-  __device__ __forceinline__ float inverse(float2 ml) const { return ml.x == -INFINITY ? 0.0f : 1.0f / ml.y; }
   __device__ __forceinline__ int64_t token() const { return (int64_t)d.row0 + (int)tile_row() / a.R; }
   __device__ __forceinline__ int head() const { return d.h * a.R + (int)tile_row() % a.R; }
   __device__ __forceinline__ void store_lse(float2 ml) const {
@@ -1099,7 +1102,7 @@ __global__ __launch_bounds__(64) void k_kv_join(KvAttnArgs a) {
         for (int e = 0; e < E; ++e) acc[e] += wgt[p0 + x] * v[x][e];
       }
   }
-  const float inv = r.inverse(ml);
+  const float inv = inverse_sum(ml.y);
   uint16_t* out = a.out + r.token() * a.ldo + (int64_t)r.head() * D;
 #pragma unroll
   for (int e = 0; e < E; ++e) out[lane * E + e] = (uint16_t)f32_to_bf16_nan(acc[e] * inv);
@@ -1148,7 +1151,7 @@ __global__ __launch_bounds__(256) void k_kv_join_wide(KvAttnArgs a) {
   __syncthreads();
   if (t < 16) {
     for (int w = 1; w < 16; ++w) acc += sums[w][t];
-    const float inv = r.inverse(ml);
+    const float inv = inverse_sum(ml.y);
     uint16_t* out = a.out + r.token() * a.ldo + (int64_t)r.head() * D + col;
 #pragma unroll
     for (int e = 0; e < 4; ++e) out[e] = (uint16_t)f32_to_bf16_nan(acc[e] * inv);

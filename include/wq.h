@@ -382,7 +382,8 @@ int wq_kv_append(wq_ctx* ctx, const wq_kv_cache* cache, const void* k_new, int64
  *   s_j = scale * sum_d q_d k_jd,  lse = log sum_j exp(s_j),  out_d = sum_j exp(s_j - lse) v_jd
  * out: bf16 [T, q_heads * head_dim], row stride ldo (it may not overlap q); lse: f32
  * [T, q_heads] or NULL.  A row that sees no token gets zeros and lse = -inf; one that sees a
- * token of a page and head whose keys' or values' byte is 255 gets NaN for both.  Codes behind
+ * token of a page and head whose keys' or values' byte is 255, or that sees a token and holds
+ * a NaN itself, gets NaN for both.  Codes behind
  * lens[b] may hold anything; E4M3's NaN patterns in front of it, which wq_kv_append never
  * writes, may reach rows that do not see them.  The products take the codes exactly (bf16),
  * sums and softmax statistics are f32, and a weight exp(s - max) is rounded to bf16.
