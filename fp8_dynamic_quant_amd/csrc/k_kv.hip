@@ -366,9 +366,14 @@ __device__ __forceinline__ v4u keep_bytes(v4u v, int n) {  // the first n bytes,
   return v;
 }
 
-// |scale| log2(e), with which scores become powers of two (1 for a zero scale, at which q is zero)
-__device__ __forceinline__ float log2_scale(const KvAttnArgs& a) {
-  return a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.44269504088896340736f;
+// |scale| (1 for a zero scale, at which q is zero)
+__device__ __forceinline__ float score_scale(const KvAttnArgs& a) { return a.scale == 0.0f ? 1.0f : fabsf(a.scale); }
+// |scale| 2^(byte - 127) log2(e), with which a page's scores become powers of two, kept within the
+// positive finite numbers: scores of -inf (hidden) and 0 stay what they are.  Products of f32 with
+// what lies below the least of them are below 2^-21, with nothing to tell between them.
+__device__ __forceinline__ float log2_scale(float scale, uint32_t byte) {
+  const float f = ldexpf(scale, (int)byte - 127) * 1.44269504088896340736f;
+  return fminf(fmaxf(f, __uint_as_float(1u)), __uint_as_float(0x7F7FFFFFu));
 }
 
 // RT row tiles of a wave over steps [lo, hi) with stride TW, keys and values straight from memory
@@ -459,7 +464,7 @@ struct Rows {
     auto begin_rows = [&]() __attribute__((always_inline)) { load_q(a, s, h, r0, j, g); };
     const KvArgs& c = a.c;
     const uint32_t per = (uint32_t)c.P >> 4, recip = c.page_recip, one = per == 1 ? ~0u : 0u, H = (uint32_t)c.H;
-    const float to_log2 = log2_scale(a);
+    const float abs_scale = score_scale(a);
     const uint32_t page_bytes = (uint32_t)c.P * D;
     const uint8_t* K = static_cast<const uint8_t*>(c.k) + (uint32_t)h * page_bytes;
     const uint8_t* V = static_cast<const uint8_t*>(c.v) + (uint32_t)h * page_bytes;
@@ -531,7 +536,7 @@ struct Rows {
       // ---- weights and values
       const bool tail = tok0 + kTokTile > s.seen || !__all(pv.there), bad = kbyte == 255u || vb == 255u;
       if (tail || tok0 + kTokTile > first || __any(bad)) hide(sc, pv.there, bad, gt);
-      const float ks = bad || !pv.there ? 1.0f : scale_of(kbyte) * to_log2, vs = bad || !pv.there ? 1.0f : scale_of(vb);
+      const float ks = bad || !pv.there ? 1.0f : log2_scale(abs_scale, kbyte), vs = bad || !pv.there ? 1.0f : scale_of(vb);
       v8bf pf[RT][2];
       weights(sc, pf, ks, vs);
 #pragma unroll
@@ -581,7 +586,7 @@ struct SharedRows {
     const KvArgs& c = a.c;
     const int j = lane & 15, g = lane >> 4;
     const uint32_t per = (uint32_t)c.P >> 4, recip = c.page_recip, one = per == 1 ? ~0u : 0u, H = (uint32_t)c.H;
-    const float to_log2 = log2_scale(a);
+    const float abs_scale = score_scale(a);
     const uint32_t page_bytes = (uint32_t)c.P * D;
     const uint8_t* K = static_cast<const uint8_t*>(c.k) + (uint32_t)h * page_bytes;
     const uint8_t* V = static_cast<const uint8_t*>(c.v) + (uint32_t)h * page_bytes;
@@ -678,7 +683,7 @@ struct SharedRows {
       const uint32_t tok0 = step * kTokTile, gt = tok0 + 16 * g;
       const bool there = !(none >> g & 1u), tail = tok0 + kTokTile > s.seen || none != 0, bad = kbyte == 255u || vbyte == 255u;
       if (tail || tok0 + kTokTile > first || __any(bad)) w.hide(sc, there, bad, gt);
-      const float ks = bad || !there ? 1.0f : scale_of(kbyte) * to_log2, vs = bad || !there ? 1.0f : scale_of(vbyte);
+      const float ks = bad || !there ? 1.0f : log2_scale(abs_scale, kbyte), vs = bad || !there ? 1.0f : scale_of(vbyte);
       auto value = [&](int i) __attribute__((always_inline)) {
         return *reinterpret_cast<const v4u*>(sv + (16 * i + j) * 64 + ((g ^ v_swz(j)) << 4));
       };

@@ -387,6 +387,8 @@ int wq_kv_append(wq_ctx* ctx, const wq_kv_cache* cache, const void* k_new, int64
  * lens[b] may hold anything; E4M3's NaN patterns in front of it, which wq_kv_append never
  * writes, may reach rows that do not see them.  The products take the codes exactly (bf16),
  * sums and softmax statistics are f32, and a weight exp(s - max) is rounded to bf16.
+ * Any finite scale is taken, beside any byte; sum_d |q_d code_jd| and the values' sums weighted by
+ * exp(s - max) have to stay below 2^128.
  * workspace: device memory, 16-byte aligned, of at least wq_kv_attention_workspace_bytes()
  * for these sizes, that no other call uses until this one is done (the parts of a sequence
  * that is split over workgroups are joined there); its contents need no initialisation.  NULL:
