@@ -42,9 +42,10 @@ def cache(g, pages, H, P, D, i8):
     return k, v, *(g.integers(*span, (pages, H)).astype(np.uint8) for _ in range(2))
 
 
-def inputs(name, D, i8, seed, extra=2):
-    """(sizes, [k, v, k_scale, v_scale], table, q bits): the first page of no sequence is page 0."""
-    f = form(name, D)
+def inputs(name, D, i8, seed, extra=2, **kw):
+    """(sizes, [k, v, k_scale, v_scale], table, q bits), sizes replaced by kw's."""
+    f = dict(form(name, D), **kw)
+    f["offsets"] = np.concatenate(([0], np.cumsum(f["ns"]))).astype(np.int64)
     g = syn.rng(80, seed, D, int(i8))
     B = len(f["ns"])
     pages = B * f["width"] + 3
