@@ -1198,20 +1198,25 @@ int rows_of_whole(int D) { return D == 256 ? 64 : 128; }
 Shape shape_of(const KvArgs& c, int R, int num_cu) {
   Shape s{};
   const int big = rows_of_whole(c.D);
-  // whole row tiles once they fill the chip (runs against whole tiles, us, 8 heads of 128, R = 4: at a
-  // tile a CU 1024 rows over 2048 tokens 84 / 70, over 16384 501 / 456; at half of that, 512 rows,
-  // over 2048 61 / 67, over 16384 283 / 449)
-  if (c.T * R / big * c.H >= num_cu) {
-    s.whole = true;
-    s.rows = big;
-    return s;
-  }
+  const int64_t cap = ((int64_t)c.max_pages * c.P + kTokTile - 1) / kTokTile;  // steps of the longest sequence
   // 16-row tiles for sequences that have no more on average (16 against 64: one token of a sequence of
   // 1000, 12.5 / 16.1 us; of each of 64 of 8192, 123 / 158), where the registers hold a head
   const int64_t avg = (c.T * R + c.B - 1) / c.B;
   s.rows = avg <= 16 && c.D < 256 ? 16 : 64;
+  // Whole row tiles once they fill the chip (runs against whole tiles, us, 8 heads of 128, R = 4: at a
+  // tile a CU 1024 rows over 2048 tokens 84 / 70, over 16384 501 / 456; at half of that, 512 rows,
+  // over 2048 61 / 67, over 16384 283 / 449).  Sequences of few rows leave most of such a tile empty
+  // and stay with 16-row tiles, unless their tables are short or they need many launches (16-row
+  // against whole tiles, a token a sequence: 256 sequences of 2000, R = 16, 134 / 200, of 300 53 / 60;
+  // 1024 of 4000, R = 4, 826 / 1129, of 600 267 / 271, of 400 241 / 221; 3000 of 4000 2358 / 3179; 4096
+  // of 1000 1495 / 1448.  64-row against whole tiles where sequences have 20 to 40 rows: 0.8 to 1.2
+  // of the time, by length and head).
+  if (c.T * R / big * c.H >= num_cu && !(s.rows == 16 && cap > 8 && c.B <= 4 * kPlanSeqs)) {
+    s.whole = true;
+    s.rows = big;
+    return s;
+  }
   const int64_t B = min((int64_t)c.B, (int64_t)kPlanSeqs);
-  const int64_t cap = ((int64_t)c.max_pages * c.P + kTokTile - 1) / kTokTile;  // steps of the longest sequence
   const int64_t items = (c.T * R / s.rows + B) * c.H;
   // a sequence of few steps is not worth cutting: a run is an item then.  Heads of 256 get one run a
   // CU: their parts are large (131072 tokens, 64 rows: 56 us with two, 43 with one; 8 sequences of
