@@ -144,13 +144,15 @@ __device__ __forceinline__ Found find_slot_256(const KvArgs& c, int64_t item, in
 // workgroup for every two pages a sequence can touch).  2000 rows to each of three sequences: 12.2 us,
 // 24 MB, 2.0 TB/s (15.6 when values were stored a byte at a time and rows read twice).
 template <bool I8>
-__global__ __launch_bounds__(256) void k_kv_append(KvArgs c, int div, int per_seq, const uint16_t* k_new, int64_t ldk, const uint16_t* v_new,
+__global__ __launch_bounds__(256) void k_kv_append(KvArgs c, int64_t slots, int div, int per_seq, const uint16_t* k_new, int64_t ldk, const uint16_t* v_new,
                                                    int64_t ldv) {
   __shared__ int count[4];
   __shared__ Found told;
   __shared__ uint32_t red[4];
-  const int t = threadIdx.x, h = blockIdx.y, side = blockIdx.z;
-  const Found s = find_slot_256(c, blockIdx.x, div, per_seq, &told, count);
+  const int t = threadIdx.x, h = blockIdx.y, side = blockIdx.z & 1;
+  const int64_t slot = blockIdx.x + ((int64_t)(blockIdx.z >> 1) << kGridXLog);
+  if (slot >= slots) return;
+  const Found s = find_slot_256(c, slot, div, per_seq, &told, count);
   if (s.rows <= 0) return;
   const int64_t len = s.len, start = len - s.rows;
   const int64_t pg = max(start, (int64_t)0) / c.P + s.j;
@@ -751,8 +753,9 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_rows(KvAttn
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   constexpr int kRows = 16 * RT * kAttnWaves;
-  const int h = blockIdx.x % a.c.H;
-  const SeqSlot sl = find_slot(a.c, blockIdx.x / a.c.H, a.R, kRows, 1);
+  const uint32_t block = blockIdx.x + (blockIdx.y << kGridXLog);  // < 2^31 + 2^22
+  const int h = block % (uint32_t)a.c.H;
+  const SeqSlot sl = find_slot(a.c, block / (uint32_t)a.c.H, a.R, kRows, 1);
   const Seq s = seq_of(a, sl.b, sl.row0, max(sl.rows, (int64_t)0));
   const int64_t tiles = (s.nrows + kRows - 1) / kRows;
   if (sl.j >= tiles) return;
@@ -1172,11 +1175,12 @@ hipError_t launch_kv_append(const KvArgs& c, bool i8, const uint16_t* k_new, int
   const int64_t by_pages = c.T / c.P + 2 * (int64_t)c.B;
   const bool by_rows = c.T <= by_pages;
   const int div = by_rows ? 1 : c.P, per = by_rows ? 0 : 2;
-  const dim3 grid((unsigned)(by_rows ? c.T : by_pages), (unsigned)c.H, 2);
+  const int64_t slots = by_rows ? c.T : by_pages;
+  const dim3 folds = folded_grid(slots), grid(folds.x, (unsigned)c.H, 2 * folds.y);
   if (i8)
-    hipLaunchKernelGGL(k_kv_append<true>, grid, dim3(256), 0, st, c, div, per, k_new, ldk, v_new, ldv);
+    hipLaunchKernelGGL(k_kv_append<true>, grid, dim3(256), 0, st, c, slots, div, per, k_new, ldk, v_new, ldv);
   else
-    hipLaunchKernelGGL(k_kv_append<false>, grid, dim3(256), 0, st, c, div, per, k_new, ldk, v_new, ldv);
+    hipLaunchKernelGGL(k_kv_append<false>, grid, dim3(256), 0, st, c, slots, div, per, k_new, ldk, v_new, ldv);
   return hipGetLastError();
 }
 
@@ -1226,7 +1230,7 @@ Shape shape_of(const KvArgs& c, int R, int num_cu) {
   s.fixed = s.rows == 16 ? 2 * kAttnWaves : 4;
   const int most = (int)min((int64_t)min(kMaxRuns, (c.D == 256 ? 1 : 2) * num_cu), (int64_t)(kJoinBytes / ((size_t)2 * s.rows * (c.D * 4 + 8) + sizeof(KvJoin))));
   if (!s.cut) {
-    s.runs = (int)min(items, (int64_t)1 << 30);
+    s.runs = (int)min(items, (int64_t)kGridX);  // of more, a run takes several
   } else {
     s.runs = (int)min((int64_t)most, (items * (cap + s.fixed) + s.least - 1) / s.least);
     s.wide_join = items * 8 < s.runs;  // many parts to an item
@@ -1245,7 +1249,7 @@ hipError_t attention_of(KvAttnArgs a, const Shape& s, hipStream_t st) {
     constexpr int lds = SharedRows<D, I8, RT, S>::kBytes;
     hipError_t e = set_lds_limit(reinterpret_cast<const void*>(k_kv_attention_rows<D, I8, RT, S>), lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_kv_attention_rows<D, I8, RT, S>), dim3((unsigned)(tiles * a.c.H)), block, lds, st, a);
+    hipLaunchKernelGGL((k_kv_attention_rows<D, I8, RT, S>), folded_grid(tiles * a.c.H), block, lds, st, a);
     return hipGetLastError();
   }
   const KvAttnArgs all = a;

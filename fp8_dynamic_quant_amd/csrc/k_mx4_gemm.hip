@@ -337,7 +337,8 @@ hipError_t tile(const Mx4Args& a, hipStream_t st) {
   using R = Ring<A8, WM, WN, S, KS>;
   const int64_t tm = (a.M + R::kBM - 1) / R::kBM, tn = (a.N + R::kBN - 1) / R::kBN;
   const int64_t total = tm * tn * a.batch, per_xcd = (total + 7) / 8;
-  if (per_xcd * 8 >= ((int64_t)1 << 31) || tm * tn >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+  // threads of a launch are counted in 32 bits (beyond that the operands alone are 200 GB)
+  if (per_xcd * 8 * 256 * KS >= ((int64_t)1 << 32)) return hipErrorInvalidValue;
   const void* kernel = reinterpret_cast<const void*>(k_mx4_tile<A8, WM, WN, S, KS>);
   hipError_t e = set_lds_limit(kernel, R::kBytes);
   if (e != hipSuccess) return e;

@@ -38,7 +38,7 @@ struct Share {
 __device__ __forceinline__ Share share_of(int G, int D) {
   const int lane = threadIdx.x & 63, HG = D / 32, PH = (HG + 3) / 4;
   const uint32_t PW = (uint32_t)(PH + 3) / 4, across = (uint32_t)G * PW;
-  const uint32_t rows = blockIdx.x / across, in = blockIdx.x % across;
+  const uint32_t block = blockIdx.x + (blockIdx.y << kGridXLog), rows = block / across, in = block % across;
   Share s;
   s.g = (int)(in / PW);
   s.t0 = (int64_t)rows * 16 + (threadIdx.x >> 6) * 4;
@@ -51,7 +51,7 @@ __device__ __forceinline__ Share share_of(int G, int D) {
 hipError_t share_grid(int64_t T, int G, int D, dim3* grid) {
   const int64_t blocks = (T + 15) / 16 * G * (((int64_t)D / 32 + 15) / 16);
   if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-  *grid = dim3((unsigned)blocks);
+  *grid = folded_grid(blocks);
   return hipSuccess;
 }
 

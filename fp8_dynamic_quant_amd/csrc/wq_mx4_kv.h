@@ -9,6 +9,13 @@
 
 namespace wq {
 
+// A launch counts its threads along each axis in 32 bits: of more workgroups than this, x counts
+// kGridX at a time and y (the upper bits of z in append) the rest.
+constexpr uint32_t kGridXLog = 22, kGridX = 1u << kGridXLog;
+inline dim3 folded_grid(int64_t blocks) {
+  return dim3(blocks < kGridX ? (unsigned)blocks : kGridX, (unsigned)((blocks + kGridX - 1) >> kGridXLog));
+}
+
 // Microscaled 4-bit blocks (k_mxfp4.hip): bf16 [T, G, D] -> E2M1 pairs [T, G, D/2] and UE8M0
 // words [G, ceil(D/128), align4(T)], and back (D % 32 == 0)
 hipError_t launch_group_quant_mxfp4(const uint16_t* x, int64_t T, int G, int D, uint8_t* xq, int32_t* xs,

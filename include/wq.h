@@ -228,7 +228,8 @@ int wq_group_dequant_mxfp4(wq_ctx* ctx, const uint8_t* x_q, const int32_t* x_s, 
  *   wq_group_quant_mxfp8, K bytes a row); lda (< 2^23) and a_batch_stride in bytes; a_scale = that
  *   call's storage [G, K/128, TA]; b = E2M1 pairs [G][N][K/2], b_batch_stride in bytes;
  *   b_scale = int32 words [G][K/128][N], the storage of wq_group_quant_mxfp4 on each group's
- *   weights (not floats); any M, N % 16 == 0, K % 128 == 0, K <= 131072, G <= 65535;
+ *   weights (not floats); any M, N % 16 == 0, K % 128 == 0, K <= 131072, G <= 65535, fewer than
+ *   2^24 tiles of 128 x 256 (WQ_ERR_SHAPE otherwise);
  *   y[m, g, n] = bf16_RN( sum over 32-deep blocks of 2^(e_a + e_b) sum_{k in kb} a b ).
  *   seg_offsets, acc_out, WQ_EPI_SWIGLU_F32 and WQ_LAYOUT_FRAGMENT: WQ_ERR_UNSUPPORTED.
  * acc_out (INT8 dense only, may be NULL): the raw int32 accumulators [M, N], row stride N. */

@@ -50,3 +50,12 @@ def _path(ctx, T, q_heads, B, **kw):
 def test_attention(ctx, T, q_heads, B, kw, want):
     assert _path(ctx, T, q_heads, B, **kw) == want
     assert _path(None, T, q_heads, B, **kw) == -NULL
+
+
+def test_products_of_more_tiles_than_a_launch_counts(ctx):
+    d = wq.MatmulDesc()
+    for k, v in dict(payload=4, epilogue=1, M=32769, N=16, K=128, batch=65535, a=1 << 16, lda=64, a_batch_stride=1 << 21,
+                     a_scale=1 << 16, a_scale_tokens=32772, b=1 << 16, b_batch_stride=1024, b_scale=1 << 16, y=1 << 16, ldy=16,
+                     y_batch_stride=1 << 20).items():
+        setattr(d, k, v)
+    assert wq.lib().wq_quant_matmul(ctx, ctypes.byref(d), None) == SHAPE
