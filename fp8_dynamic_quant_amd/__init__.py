@@ -363,6 +363,8 @@ def wq_quant_matmul(a, a_scale, b, b_scale, *, y=None, acc_out=None, seg_offsets
     if mx4:
         if fp8_groups is None or acc_out is not None or seg_offsets is not None or epilogue != WQ_EPI_BF16 or b_fragment:
             raise ValueError("mx4 takes fp8_groups, and no acc_out, segments, SwiGLU epilogue or fragment order")
+        if mx or (a_scale_tokens and a_scale_tokens != a_scale.shape[-1]) or (n is not None and n != b.shape[-2]):
+            raise ValueError("mx4 is not mx, and takes a_scale_tokens and n from the operands' shapes")
         return _mx4_matmul(a, a_scale, b, b_scale, fp8_groups, y)
     d = MatmulDesc()
     d.b_layout = WQ_LAYOUT_FRAGMENT if b_fragment else WQ_LAYOUT_PLAIN

@@ -5,6 +5,7 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 import fp8_dynamic_quant_amd as wq
 
@@ -59,3 +60,14 @@ def test_products_of_more_tiles_than_a_launch_counts(ctx):
                      y_batch_stride=1 << 20).items():
         setattr(d, k, v)
     assert wq.lib().wq_quant_matmul(ctx, ctypes.byref(d), None) == SHAPE
+
+
+@pytest.mark.parametrize("kw", [dict(mx=True), dict(a_scale_tokens=8), dict(n=32)])
+def test_arguments_that_contradict_the_operands(kw):
+    a, sa = torch.zeros((3, 1, 64), dtype=torch.uint8), torch.zeros((1, 1, 4), dtype=torch.int32)
+    w, sw = torch.zeros((1, 16, 64), dtype=torch.uint8), torch.zeros((1, 1, 16), dtype=torch.int32)
+    with pytest.raises(ValueError):
+        wq.wq_quant_matmul(a, sa, w, sw, fp8_groups=1, mx4=True, **kw)
+    for good in ({}, dict(a_scale_tokens=4), dict(n=16)):  # accepted, up to the device
+        with pytest.raises(RuntimeError, match="GPU only"):
+            wq.wq_quant_matmul(a, sa, w, sw, fp8_groups=1, mx4=True, **good)
