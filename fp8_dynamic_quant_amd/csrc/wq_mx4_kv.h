@@ -10,7 +10,7 @@
 namespace wq {
 
 // A launch counts its threads along each axis in 32 bits: of more workgroups than this, x counts
-// kGridX at a time and y (the upper bits of z in append) the rest.
+// kGridX at a time and y the rest (append, which has no axis left, takes several launches).
 constexpr uint32_t kGridXLog = 22, kGridX = 1u << kGridXLog;
 inline dim3 folded_grid(int64_t blocks) {
   return dim3(blocks < kGridX ? (unsigned)blocks : kGridX, (unsigned)((blocks + kGridX - 1) >> kGridXLog));
