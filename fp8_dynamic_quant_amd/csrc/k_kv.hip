@@ -451,7 +451,10 @@ struct Rows {
         for (int r = 0; r < 4; ++r) {
           const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[rt][t][r], ks, -base));
           sum[rt] += e;
-          // rounded to bf16, with an int8 page's scale on it (a power of two: no further rounding)
+          // rounded to bf16, with an int8 page's scale on it (a power of two: no further rounding).  By
+          // at most 2^-8 of each weight, as the output itself is: against 64 bits outputs are off by 0.0019
+          // to 0.0020 (relative, over all) where f32 weights give 0.0017.  The instruction takes bf16;
+          // keeping the weights' other bits would take a second one for each.
           pf[rt][t >> 1][(t & 1) * 4 + r] = (__bf16)(I8 ? e * vs : e);
         }
     }
@@ -743,7 +746,10 @@ __device__ __forceinline__ void store_rows(const KvAttnArgs& a, const Seq& s, Ro
 // sequence's last rows, which see most, come first.  The arithmetic around the matrix instructions
 // bounds it: for each 16 x 16 of scores a lane widens codes, scales, takes maximum, power of two and
 // rounding of four, beside 2 x D / 32 instructions of 16 clocks.  Two prompts of 2000 behind 2099, 32
-// query heads on 8 of 128: 255 us, 637 TFLOP/s of the 1376 that a bf16 product of 8192^3 reaches.
+// query heads on 8 of 128: E4M3 255 to 260 us, 630 TFLOP/s of the 1376 that a bf16 product of 8192^3
+// reaches (vector instructions 46 % of the SIMDs' cycles, matrix instructions 26 %); int8, whose
+// codes take twelve instructions for eight where E4M3's take four, 334 us (57 and 20 %); heads of 64
+// 172 / 216 us, of 256 497 / 729.
 template <int D, bool I8, int RT, int S>
 __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attention_rows(KvAttnArgs a) {
   using W = SharedRows<D, I8, RT, S>;
@@ -1223,8 +1229,9 @@ Shape shape_of(const KvArgs& c, int R, int num_cu) {
   const int64_t B = min((int64_t)c.B, (int64_t)kPlanSeqs);
   const int64_t items = (c.T * R / s.rows + B) * c.H;
   // a sequence of few steps is not worth cutting: a run is an item then.  Heads of 256 get one run a
-  // CU: their parts are large (131072 tokens, 64 rows: 56 us with two, 43 with one; 8 sequences of
-  // 9000: 73 / 56)
+  // CU: two workgroups' rings and plans (84,528 bytes each) do not fit a CU's LDS together, and a
+  // second run would wait for the first (131072 tokens, 64 rows: 56 us with two runs a CU, 43 with
+  // one; 8 sequences of 9000: 73 / 56)
   s.cut = cap > (s.rows == 16 ? 4 * kAttnWaves : 8);
   s.least = !s.cut ? 1 : s.rows == 16 ? 2 * kAttnWaves : 4;
   s.fixed = s.rows == 16 ? 2 * kAttnWaves : 4;

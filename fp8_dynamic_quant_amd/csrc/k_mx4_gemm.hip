@@ -117,11 +117,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx4_few(Mx4Args p) {
 // odd slices (a slice of a 64 x 64 tile is a chain of wait, barrier, LDS read and two dependent
 // instructions, which two halves go through side by side: M=64 G=8 N=1024 K=4096 11.8 -> 10.6 us),
 // and their sums are added through LDS.
-// What bounds it: with large tiles LDS, whose reads and DMA writes take about as many clocks as the
-// 4-bit matrix instructions (M=8192 N=32768 K=1024: 236 - 250 us, 2.2 - 2.3 PFLOP/s; 256 x 256 tiles,
-// which read less from L2, were no faster: 269); with small ones the chain of a slice and the reads
-// of both operands from L2 (M=64 G=8 N=1024 K=4096: 10.6 us, 2.0 TB/s).  Outputs are stored past
-// the caches: they would drive out operands (269 -> 250 us at M=8192).
+// What bounds it: with large tiles no single unit (M=8192 N=32768 K=1024: 202 us alone at 2.0 GHz, 233 -
+// 260 in a row; matrix instructions take 32 % of the cycles, others 30, LDS reads 25 and DMA writes about 13 %), but
+// the chain of wait, barrier, LDS reads and instructions that two waves a SIMD go through (a quarter
+// of their time they wait for loads, 38 % to issue), beside 537 MB of output; with 8-bit activations
+// matrix instructions take 53 % (297 us in a row).  256 x 256 tiles, which read less
+// from L2, were no faster: 269.  With small tiles the chain of a slice, and CUs without a tile:
+// M=64 G=8 N=1024 K=4096 has 128 tiles, 10.6 us, 2.0 TB/s.  Outputs are stored past the caches: they
+// would drive out operands (269 -> 250 us at M=8192).
 //
 // A 4-bit row's slice is 64 bytes, four chunks of 16; four rows make a 256-byte line of LDS
 // (all its banks), and a chunk is XORed with bits 2..3 of its row, so that sixteen rows read at

@@ -188,7 +188,8 @@ int wq_group_quant_mxfp4(wq_ctx* ctx, const void* x, int64_t T, int64_t G, int64
                          void* stream);
 
 /* The inverse: y[t, g, d] = code * 2^(byte - 127), bf16 [T, G, D] contiguous (exact: every
- * value of a finite block is a bf16 number; byte 255 gives NaN). */
+ * value of a finite block below 2^128 is a bf16 number; a magnitude from 1.75 * 2^127 on was rounded
+ * up to 2^128, which reads as infinity; byte 255 gives NaN). */
 int wq_group_dequant_mxfp4(wq_ctx* ctx, const uint8_t* x_q, const int32_t* x_s, int64_t T, int64_t G, int64_t D,
                            void* y, void* stream);
 
@@ -372,6 +373,8 @@ typedef struct {
  *   the new codes are RN(x * 2^(127 - byte)) (nearest-even).  Slots behind them keep their codes.
  * A NaN or an infinity among the rows makes the byte 255 (UE8M0's NaN) and their codes zero:
  * the page's tokens of that head read as NaN until the page is begun anew.
+ * Magnitudes from 1.9375 * 2^127 (E4M3) or 1.9921875 * 2^127 (int8) on round up to 2^128, which reads
+ * as infinity, and from a page of E4M3 codes may reach as NaN rows of its sequence that do not see it.
  * The same call again writes the same bytes.  A page written by the call stands in one place
  * of the tables (a shared one is copied first). */
 int wq_kv_append(wq_ctx* ctx, const wq_kv_cache* cache, const void* k_new, int64_t ldk, const void* v_new, int64_t ldv,

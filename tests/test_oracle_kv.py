@@ -32,3 +32,21 @@ def test_rows_that_see_a_nan():
     want[21 + np.arange(33)[250 - 33 + np.arange(33) >= 240], :4] = True
     assert np.array_equal(np.isnan(lse), want) and np.array_equal(np.isnan(out).all(-1), want)
     assert np.array_equal(np.isnan(out).any(-1), want)
+
+
+def test_the_largest_magnitudes():
+    """From which magnitude on each format rounds up to 2^128, which bf16 reads as infinity."""
+    from oracle import mxfp4 as m4
+
+    def back(bits, kind):
+        x = np.full((1, 1, 32), bits, np.uint16)
+        if kind == "e2m1":
+            pairs, _, byte = m4.group_quant_mxfp4(x)
+            return m4.values(pairs, byte)[0, 0, 0]
+        dtype = np.int8 if kind == "int8" else np.uint8
+        c = [np.zeros((1, 1, 16, 64), dtype), np.zeros((1, 1, 64, 16), dtype), np.zeros((1, 1), np.uint8), np.zeros((1, 1), np.uint8)]
+        kvo.append(*c, np.full((1, 1, 64), bits, np.uint16), np.full((1, 1, 64), bits, np.uint16), [0, 1], [1], np.zeros((1, 1), int))
+        return (kvo.decode(c[0][0, 0, 0]) * m4.scales(c[2][0, 0]))[0]
+
+    for kind, first in (("e2m1", 0x7F60), ("e4m3", 0x7F78), ("int8", 0x7F7F)):
+        assert back(first - 1, kind) < 2.0**128 and back(first, kind) == 2.0**128 and back(0x7F7F, kind) == 2.0**128
