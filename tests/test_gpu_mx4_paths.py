@@ -30,3 +30,31 @@ def test_weights_that_stream_past_in_32_columns(M, G, N, K, a8):
 def test_every_other_kernel(M, G, N, K, path, a8):
     assert wq.wq_mx4_path(M, N, K, G) == path
     _product(M, G, N, K, a8, pad=16, ypad=8, tokens=4)
+
+
+@pytest.mark.parametrize("a8", [False, True])
+@pytest.mark.parametrize("M, G, N, K, path", [(1, 1, 1024, 512, 1), (16, 8, 1040, 256, 2), (64, 2, 208, 384, 3), (1000, 1, 2064, 256, 4),
+                                              (2100, 1, 4112, 256, 5)])
+def test_graphs_with_eager_calls_between(M, G, N, K, path, a8):
+    assert wq.wq_mx4_path(M, N, K, G) == path
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    rows = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    cast = [wq.wq_group_quant_mxfp4(rows(N, 1, K)) for _ in range(G)]
+    w, ws = torch.stack([c[0].view(N, K // 2) for c in cast]), torch.cat([c[2] for c in cast])
+    x = rows(M, G, K)
+
+    def call():
+        a, _, s = wq.wq_group_quant_fp8_ue8m0(x, group=32) if a8 else wq.wq_group_quant_mxfp4(x)
+        return wq.wq_quant_matmul(a, s, w, ws, fp8_groups=G, mx4=True)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = call()
+    for _ in range(4):
+        x.copy_(rows(M, G, K))
+        graph.replay()
+        eager = call()
+        torch.cuda.synchronize()
+        assert torch.equal(y.view(torch.int16), eager.view(torch.int16)) and torch.isfinite(y).all() and y.any()
