@@ -1215,13 +1215,14 @@ Shape shape_of(const KvArgs& c, int R, int num_cu) {
   s.rows = avg <= 16 && c.D < 256 ? 16 : 64;
   // Whole row tiles once they fill the chip (runs against whole tiles, us, 8 heads of 128, R = 4: at a
   // tile a CU 1024 rows over 2048 tokens 84 / 70, over 16384 501 / 456; at half of that, 512 rows,
-  // over 2048 61 / 67, over 16384 283 / 449).  Sequences of few rows leave most of such a tile empty
-  // and stay with 16-row tiles, unless their tables are short or they need many launches (16-row
-  // against whole tiles, a token a sequence: 256 sequences of 2000, R = 16, 134 / 200, of 300 53 / 60;
-  // 1024 of 4000, R = 4, 826 / 1129, of 600 267 / 271, of 400 241 / 221; 3000 of 4000 2358 / 3179; 4096
-  // of 1000 1495 / 1448.  64-row against whole tiles where sequences have 20 to 40 rows: 0.8 to 1.2
-  // of the time, by length and head).
-  if (c.T * R / big * c.H >= num_cu && !(s.rows == 16 && cap > 8 && c.B <= 4 * kPlanSeqs)) {
+  // over 2048 61 / 67, over 16384 283 / 449).  Single tokens leave most of such a tile empty and stay
+  // with 16-row tiles, unless their tables are short or they need many launches (16-row against
+  // whole tiles: 256 sequences of 2000, R = 16, 134 / 200, of 300 53 / 60; 1024 of 4000, R = 4, 826 / 1129,
+  // of 600 267 / 271, of 400 241 / 221; 3000 of 4000 2358 / 3179; 4096 of 1000 1495 / 1448).  Of more
+  // rows than sequences the host does not know whose they are: four tokens to each of 512 sequences
+  // of 2000 take 258 / 354, but a prompt of 4000 among 3000 single tokens over 1000 1915 / 1762.
+  const bool singles = s.rows == 16 && c.T <= c.B && cap > 8 && c.B <= 4 * kPlanSeqs;
+  if (c.T * R / big * c.H >= num_cu && !singles) {
     s.whole = true;
     s.rows = big;
     return s;

@@ -101,12 +101,12 @@ def test_whole_row_tiles_of_prompts_behind_a_cache(D, i8):
 
 
 @pytest.mark.parametrize("i8", [False, True])
-@pytest.mark.parametrize("name, D, B, R, width", [("items16", 64, 1030, 12, 9), ("runs16", 128, 400, 12, 20), ("rows", 64, 1030, 4, 4),
-                                                  ("rows", 256, 300, 8, 12)])
+@pytest.mark.parametrize("name, D, B, R, width", [("items16", 64, 1030, 12, 9), ("runs16", 128, 600, 16, 20), ("rows", 64, 1030, 12, 4),
+                                                  ("rows", 256, 300, 16, 12)])
 def test_many_sequences_of_a_row(name, D, B, R, width, i8):
     # as many rows as fill whole tiles, a row a sequence: 16-row tiles unless tables are short
     g = np.random.default_rng(B + width)
-    ns = [int(x) for x in g.integers(0, 3, B)]
+    ns = [int(x) for x in g.integers(0, 2, B)]
     lens = [int(x) for x in g.integers(0, 64 * width + 20, B) // (1 + 5 * (g.random(B) < 0.7))]
     path = {"items16": 2, "runs16": 4, "rows": 1}[name]
     f, c, table, q = kf.inputs(name, D, i8, 10, ns=ns, lens=lens, H=8, R=R, P=64, width=width, path=path)

@@ -46,7 +46,7 @@ def _path(ctx, T, q_heads, B, **kw):
     (4, 16, 1, dict(heads=1, head_dim=256, max_pages=8192), 5 + 8),
     (1023, 32, 3, {}, 5), (1024, 32, 3, {}, 1), (511, 32, 3, dict(head_dim=256), 5), (512, 32, 3, dict(head_dim=256), 1),
     (1024, 32, 1024, {}, 2), (1024, 32, 1024, dict(max_pages=256), 4), (1024, 32, 1024, dict(max_pages=32), 1),
-    (1024, 32, 1024, dict(head_dim=256), 1), (256, 128, 256, {}, 2), (4096, 32, 4097, {}, 1), (4096, 32, 240, {}, 1),
+    (1024, 32, 1024, dict(head_dim=256), 1), (256, 128, 256, {}, 2), (4096, 32, 4097, {}, 1), (1025, 32, 1024, dict(max_pages=256), 1), (4096, 32, 240, {}, 1),
     (4000, 32, 2, {}, 1), (1, 12, 1, {}, -SHAPE), (-1, 32, 1, {}, -SHAPE), (1, 32, 1, dict(head_dim=96), -SHAPE)])
 def test_attention(ctx, T, q_heads, B, kw, want):
     assert _path(ctx, T, q_heads, B, **kw) == want
