@@ -15,6 +15,9 @@ The functions carry the C names:
   wq_group_dequant_mxfp4(x_q, storage)    -> bf16 [T,G,D]
   wq_kv_append(cache, k, v, ...)             quantises rows into a paged 8-bit cache (KvCache)
   wq_kv_attention(cache, q, ...)          -> bf16 [T, heads, D] (and lse)
+  wq_add_rms_quant(x, residual, gamma)    -> (x_q, scales, sum): the residual's addition, RMSNorm and 8-bit rows
+  wq_kv_append_rotated(cache, k, v, ...)     appends with keys (and queries) turned by their positions
+  wq_kv_attention_shared(cache, q, ...)   -> as wq_kv_attention, of sequences that begin with the same pages
 """
 
 from __future__ import annotations
@@ -103,6 +106,16 @@ EXPORTS = {
     "wq_kv_attention_workspace_bytes": (_i64, [_c_void_p, ctypes.POINTER(KvCacheDesc), _i64, _i64, _i64]),
     "wq_kv_attention_path": (ctypes.c_int, [_c_void_p, ctypes.POINTER(KvCacheDesc), _i64, _i64, _i64]),
     "wq_mx4_path": (ctypes.c_int, [_c_void_p, _i64, _i64, _i64, _i64]),
+    "wq_add_rms_quant": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, ctypes.c_float, _i64, _i64,
+                                        ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p]),
+    "wq_kv_append_rotated": (ctypes.c_int, [_c_void_p, ctypes.POINTER(KvCacheDesc), _c_void_p, _i64, _c_void_p, _i64,
+                                            _c_void_p, _i64, _i64, _c_void_p, _i64, _c_void_p, _i64, _i64, ctypes.c_int,
+                                            _i64, _i64, _c_void_p, _c_void_p, _c_void_p]),
+    "wq_kv_attention_shared": (ctypes.c_int, [_c_void_p, ctypes.POINTER(KvCacheDesc), _c_void_p, _i64, _i64, _i64, _i64,
+                                              _c_void_p, _c_void_p, _c_void_p, _c_void_p, ctypes.c_float, ctypes.c_int,
+                                              _c_void_p, _i64, _c_void_p, _c_void_p, ctypes.c_size_t, _c_void_p]),
+    "wq_kv_attention_shared_workspace_bytes": (_i64, [_c_void_p, ctypes.POINTER(KvCacheDesc), _i64, _i64, _i64]),
+    "wq_kv_attention_shared_path": (ctypes.c_int, [_c_void_p, ctypes.POINTER(KvCacheDesc), _i64, _i64, _i64]),
     "wq_pack_weight_i8": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p]),
     "wq_fused_quant_matmul_packed": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p,
                                                     _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p,
@@ -259,6 +272,64 @@ def wq_group_quant_fp8_ue8m0(x: torch.Tensor, x_q: torch.Tensor | None = None, s
         _check(fn, st)
     x_s = storage.transpose(-1, -2)[:, :T, :].transpose(0, 1)
     return x_q, x_s, storage
+
+
+def _rows_2d(name, x, M, K):
+    """Row stride of bf16 rows [M, K] with unit stride along K."""
+    if x.shape != (M, K) or x.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bf16 [{M}, {K}]")
+    s = x.stride()
+    if M and s[1] != 1 and K > 1:
+        raise ValueError(f"{name} must have unit stride along K")
+    return s[0] if M > 1 else K
+
+
+def wq_add_rms_quant(x: torch.Tensor, residual: torch.Tensor | None, rms_gamma: torch.Tensor, rms_eps: float = 1e-6, *,
+                     payload: int = WQ_PAYLOAD_INT8, x_q=None, x_s=None, sum_out=None, y=None, return_y: bool = False):
+    """h = x + residual in bf16, its RMSNorm, and the norm's rows in 8 bits: x, residual bf16
+    [M, K] (residual None: h = x), rms_gamma bf16 [K].  Returns (x_q, x_s, h) and with return_y or
+    y= the normalised rows bf16 [M, K] too; h is None without a residual and sum_out.
+    payload WQ_PAYLOAD_INT8: x_q int8 [M, K], x_s f32 [M]; WQ_PAYLOAD_FP8_E4M3 and WQ_PAYLOAD_MXFP8:
+    x_q uint8 [M, 1, K] and x_s the int32 storage [1, PH, TA], operands of wq_quant_matmul with
+    fp8_groups=1.  sum_out may be residual or x itself."""
+    if x.dim() != 2:
+        raise ValueError("x must be bf16 [M, K]")
+    M, K = x.shape
+    ldx = _rows_2d("x", x, M, K)
+    ldr = _rows_2d("residual", residual, M, K) if residual is not None else 0
+    if rms_gamma.shape != (K,) or rms_gamma.dtype != torch.bfloat16 or not rms_gamma.is_contiguous():
+        raise ValueError("rms_gamma must be contiguous bf16 [K]")
+    if payload == WQ_PAYLOAD_INT8:
+        qshape, qtype, sshape, stype = (M, K), torch.int8, (M,), torch.float32
+    else:
+        packs = (K + 511) // 512 if payload == WQ_PAYLOAD_FP8_E4M3 else (K + 127) // 128
+        qshape, qtype, sshape, stype = (M, 1, K), torch.uint8, (1, packs, (M + 3) // 4 * 4), torch.int32
+    if x_q is None:
+        x_q = x.new_empty(qshape, dtype=qtype)
+    elif x_q.shape != qshape or x_q.dtype != qtype or not x_q.is_contiguous():
+        raise ValueError(f"x_q must be contiguous {qtype} {list(qshape)}")
+    if x_s is None:
+        x_s = x.new_empty(sshape, dtype=stype)
+    elif x_s.shape != sshape or x_s.dtype != stype or not x_s.is_contiguous():
+        raise ValueError(f"x_s must be contiguous {stype} {list(sshape)}")
+    if sum_out is not None:
+        lds = _rows_2d("sum_out", sum_out, M, K)
+    elif residual is not None:
+        sum_out, lds = x.new_empty((M, K)), K
+    else:
+        lds = 0
+    if y is not None:
+        ldy = _rows_2d("y", y, M, K)
+    elif return_y:
+        y, ldy = x.new_empty((M, K)), K
+    else:
+        ldy = 0
+    h, stream = _on("wq_add_rms_quant", x, rms_gamma, x_q, x_s, *(t for t in (residual, sum_out, y) if t is not None))
+    st = lib().wq_add_rms_quant(h, x.data_ptr(), ldx, _ptr(residual), ldr, rms_gamma.data_ptr(), rms_eps, M, K, payload,
+                                x_q.data_ptr(), x_s.data_ptr(), _ptr(sum_out), lds, _ptr(y), ldy, stream)
+    if st:
+        _check("wq_add_rms_quant", st)
+    return (x_q, x_s, sum_out) if y is None else (x_q, x_s, sum_out, y)
 
 
 def wq_group_quant_mxfp4(x: torch.Tensor, x_q: torch.Tensor | None = None, storage: torch.Tensor | None = None):
@@ -475,12 +546,53 @@ def wq_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, offsets, lens
         _check("wq_kv_append", st)
 
 
-def wq_kv_attention(cache: KvCache, q: torch.Tensor, offsets, lens, table, *, scale=None, causal=True, out=None,
-                    lse=None, return_lse=False):
-    """Attention of the rows q bf16 [T, q_heads, D] over the cache (offsets, lens and table as
-    in wq_kv_append, the newest rows last) -> bf16 [T, q_heads, D], and the f32 log-sum-exp
-    [T, q_heads] with return_lse or lse=.  scale: 1 / sqrt(D) by default."""
+def rotary_angles(positions: int, rot_dim: int, base: float = 10000.0, *, device="cuda") -> torch.Tensor:
+    """f32 [positions, 2, rot_dim / 2]: cosines and sines of position * base^(-2 i / rot_dim), taken
+    in 64 bits, for wq_kv_append_rotated.  Made once, when a model is loaded."""
+    i = torch.arange(rot_dim // 2, dtype=torch.float64, device=device)
+    turn = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * torch.pow(base, -2.0 * i / rot_dim)
+    return torch.stack((turn.cos(), turn.sin()), 1).float()
+
+
+def wq_kv_append_rotated(cache: KvCache, k: torch.Tensor, v: torch.Tensor, offsets, lens, table, angles: torch.Tensor, *,
+                         q: torch.Tensor | None = None, q_out: torch.Tensor | None = None, interleaved: bool = False):
+    """wq_kv_append with the keys turned by their positions, angles f32 [positions, 2, rot_dim / 2]
+    (rotary_angles).  q bf16 [T, q_heads, D]: the rows' queries, turned as well and returned (in
+    q_out, which may be q itself).  interleaved: pairs are neighbouring elements, not halves."""
     d, B = _kv_desc(cache, offsets, lens, table)
+    H, D = d.heads, d.head_dim
+    ldk, ldv = _kv_rows("k", k, H, D), _kv_rows("v", v, H, D)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same number of rows")
+    if angles.dim() != 3 or angles.shape[1] != 2 or angles.dtype != torch.float32 or not angles.is_contiguous():
+        raise ValueError("angles must be contiguous f32 [positions, 2, rot_dim / 2]")
+    heads, qp, ldq, qo, ldo = 0, None, 0, None, 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T:
+            raise ValueError("q must be bf16 [T, q_heads, D]")
+        heads = q.shape[1]
+        ldq = _kv_rows("q", q, heads, D)
+        if q_out is None:
+            q_out, ldo = q.new_empty((T, heads, D)), heads * D
+        else:
+            if q_out.dim() != 3 or q_out.shape[0] != T:
+                raise ValueError("q_out must have q's shape")
+            ldo = _kv_rows("q_out", q_out, heads, D)
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    h, stream = _on("wq_kv_append_rotated", k, v, *cache, offsets, lens, table, angles, *(() if q is None else (q, q_out)))
+    st = lib().wq_kv_append_rotated(h, ctypes.byref(d), k.data_ptr(), ldk, v.data_ptr(), ldv, qp, ldq, heads, qo, ldo,
+                                    angles.data_ptr(), angles.shape[0], 2 * angles.shape[2], interleaved, T, B,
+                                    offsets.data_ptr(), lens.data_ptr(), stream)
+    if st:
+        _check("wq_kv_append_rotated", st)
+    return q_out
+
+
+def _attention_outputs(d, q, out, lse, return_lse):
+    """Sizes, strides and outputs that the attention calls have in common."""
     if q.dim() != 3:
         raise ValueError("q must be bf16 [T, q_heads, D]")
     T, heads, D = q.shape
@@ -496,6 +608,16 @@ def wq_kv_attention(cache: KvCache, q: torch.Tensor, offsets, lens, table, *, sc
             raise ValueError("lse must be contiguous f32 [T, q_heads]")
     elif return_lse:
         lse = q.new_empty((T, heads), dtype=torch.float32)
+    return T, heads, D, ldq, out, ldo, lse
+
+
+def wq_kv_attention(cache: KvCache, q: torch.Tensor, offsets, lens, table, *, scale=None, causal=True, out=None,
+                    lse=None, return_lse=False):
+    """Attention of the rows q bf16 [T, q_heads, D] over the cache (offsets, lens and table as
+    in wq_kv_append, the newest rows last) -> bf16 [T, q_heads, D], and the f32 log-sum-exp
+    [T, q_heads] with return_lse or lse=.  scale: 1 / sqrt(D) by default."""
+    d, B = _kv_desc(cache, offsets, lens, table)
+    T, heads, D, ldq, out, ldo, lse = _attention_outputs(d, q, out, lse, return_lse)
     h, stream = _on("wq_kv_attention", q, *cache, offsets, lens, table, out, *(() if lse is None else (lse,)))
     by = ctypes.byref(d)
     need = lib().wq_kv_attention_workspace_bytes(h, by, T, heads, B)
@@ -511,14 +633,48 @@ def wq_kv_attention(cache: KvCache, q: torch.Tensor, offsets, lens, table, *, sc
     return (out, lse) if lse is not None else out
 
 
-def wq_kv_attention_path(cache: KvCache, T: int, q_heads: int, table) -> int:
-    """Which kernels wq_kv_attention takes for T rows of q_heads heads (the numbers stand in wq.h)."""
+def wq_kv_attention_shared(cache: KvCache, q: torch.Tensor, offsets, lens, table, group, shared, *, scale=None, causal=True,
+                           out=None, lse=None, return_lse=False):
+    """wq_kv_attention of sequences that begin with the same pages: neighbours with the same id in
+    group (int32 [B], not negative) have their first shared[b] tokens (int32 [B]) in common, which
+    are read and multiplied once for all of them."""
+    d, B = _kv_desc(cache, offsets, lens, table)
+    for name, x in (("group", group), ("shared", shared)):
+        if x.shape != (B,) or x.dtype != torch.int32 or not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous int32 [B]")
+    T, heads, D, ldq, out, ldo, lse = _attention_outputs(d, q, out, lse, return_lse)
+    h, stream = _on("wq_kv_attention_shared", q, *cache, offsets, lens, table, group, shared, out, *(() if lse is None else (lse,)))
+    by = ctypes.byref(d)
+    need = lib().wq_kv_attention_shared_workspace_bytes(h, by, T, heads, B)
+    if need < 0:
+        _check("wq_kv_attention_shared", -need)
+    # from torch's allocator, call by call: calls on several streams and captured graphs share nothing
+    ws = q.new_empty(need, dtype=torch.uint8) if need else None
+    st = lib().wq_kv_attention_shared(h, by, q.data_ptr(), ldq, T, heads, B, offsets.data_ptr(), lens.data_ptr(), group.data_ptr(),
+                                      shared.data_ptr(), D ** -0.5 if scale is None else scale, causal, out.data_ptr(), ldo,
+                                      _ptr(lse), _ptr(ws), need, stream)
+    if st:
+        _check("wq_kv_attention_shared", st)
+    return (out, lse) if lse is not None else out
+
+
+def _attention_path(fn, cache, T, q_heads, table):
     pages, heads, page_tokens, D = cache.k.shape
     d = KvCacheDesc(WQ_KV_E4M3, pages, heads, page_tokens, D, None, None, None, None, None, table.shape[1], table.shape[1])
-    r = lib().wq_kv_attention_path(context(cache.k.device).handle, ctypes.byref(d), T, q_heads, table.shape[0])
+    r = getattr(lib(), fn)(context(cache.k.device).handle, ctypes.byref(d), T, q_heads, table.shape[0])
     if r < 0:
-        _check("wq_kv_attention_path", -r)
+        _check(fn, -r)
     return r
+
+
+def wq_kv_attention_path(cache: KvCache, T: int, q_heads: int, table) -> int:
+    """Which kernels wq_kv_attention takes for T rows of q_heads heads (the numbers stand in wq.h)."""
+    return _attention_path("wq_kv_attention_path", cache, T, q_heads, table)
+
+
+def wq_kv_attention_shared_path(cache: KvCache, T: int, q_heads: int, table) -> int:
+    """As wq_kv_attention_path, of wq_kv_attention_shared."""
+    return _attention_path("wq_kv_attention_shared_path", cache, T, q_heads, table)
 
 
 def wq_mx4_path(M: int, N: int, K: int, groups: int = 1, device=None) -> int:

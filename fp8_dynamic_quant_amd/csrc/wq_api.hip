@@ -23,6 +23,7 @@
 
 #include "../../include/wq.h"
 #include "wq_kernels.h"
+#include "wq_layer.h"
 #include "wq_mx4_kv.h"
 
 struct wq_ctx {
@@ -919,18 +920,18 @@ int wq_kv_append(wq_ctx* c, const wq_kv_cache* k, const void* k_new, int64_t ldk
 
 // q_heads a multiple of the cache's heads; a cache head's rows and the row tiles are counted in 32
 // bits, the tiles' steps of 64 tokens in 52
-static bool kv_heads_ok(const wq_kv_cache* k, int64_t q_heads, int64_t T, int64_t B) {
+static bool kv_heads_ok(const wq_kv_cache* k, int64_t q_heads, int64_t T, int64_t B, double unit = 1.0) {
   if (q_heads < k->heads || q_heads % k->heads != 0 || q_heads > (1 << 20)) return false;
   const int64_t rows = T * (q_heads / k->heads), tiles = (rows / 16 + B) * k->heads;
-  return rows < ((int64_t)1 << 31) && tiles < ((int64_t)1 << 31) && (double)tiles * ((double)k->max_pages * k->page_tokens / 64 + 16) < 4503599627370496.0;
+  return rows < ((int64_t)1 << 31) && tiles < ((int64_t)1 << 31) && unit * (double)tiles * ((double)k->max_pages * k->page_tokens / 64 + 16) < 4503599627370496.0;
 }
 
 // the sizes that choose attention's kernels: 0, 1 for an empty problem, or -status
-static int kv_sizes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B, wq::KvArgs* a) {
+static int kv_sizes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B, wq::KvArgs* a, double unit = 1.0) {
   if (!c || !k) return -WQ_ERR_NULL;
   if (k->heads < 1 || k->page_tokens < 16 || k->page_tokens > 256 || k->max_pages < 1 || k->max_pages > INT32_MAX ||
       !wq::kv_head_dim_ok(k->head_dim) || T < 0 || B < 0 || T > ((int64_t)1 << 30) || B > ((int64_t)1 << 24) ||
-      !kv_heads_ok(k, q_heads, T, B))
+      !kv_heads_ok(k, q_heads, T, B, unit))
     return -WQ_ERR_SHAPE;
   if (T == 0 || B == 0) return 1;
   a->H = (int)k->heads;
@@ -940,6 +941,34 @@ static int kv_sizes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_
   a->B = (int)B;
   a->T = T;
   return 0;
+}
+
+// what the attention calls check, and their arguments; a NULL workspace becomes the context's
+static int attention_args(const wq_ctx* c, const wq_kv_cache* k, const void* q, int64_t ldq, int64_t T, int64_t q_heads, int64_t B,
+                          const int64_t* offsets, const int32_t* lens, float scale, int causal, void* out, int64_t ldo, float* lse,
+                          void** workspace, size_t* workspace_bytes, wq::KvAttnArgs* to) {
+  wq::KvAttnArgs& a = *to;
+  if (int r = kv_args(k, T, B, offsets, lens, &a.c)) return r;
+  if (!kv_heads_ok(k, q_heads, T, B)) return WQ_ERR_SHAPE;
+  if (ldq < q_heads * k->head_dim || ldo < q_heads * k->head_dim || !std::isfinite(scale)) return WQ_ERR_SHAPE;
+  if (T == 0 || B == 0) return WQ_OK;
+  if (!q || !out) return WQ_ERR_NULL;
+  if (!al16(q) || !al16(out) || ldq % 8 != 0 || ldo % 8 != 0) return WQ_ERR_ALIGN;
+  a.q = static_cast<const uint16_t*>(q);
+  a.ldq = ldq;
+  a.out = static_cast<uint16_t*>(out);
+  a.ldo = ldo;
+  a.lse = lse;
+  a.scale = scale;
+  a.R = (int)(q_heads / k->heads);
+  a.causal = causal != 0;
+  if (*workspace == nullptr) {
+    *workspace = c->ws;
+    *workspace_bytes = c->ws_bytes;
+  } else if (!al16(*workspace)) {
+    return WQ_ERR_ALIGN;
+  }
+  return WQ_OK;
 }
 
 int64_t wq_kv_attention_workspace_bytes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B) {
@@ -959,26 +988,9 @@ int wq_kv_attention(wq_ctx* c, const wq_kv_cache* k, const void* q, int64_t ldq,
                     float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   if (!c || !k) return WQ_ERR_NULL;
   wq::KvAttnArgs a{};
-  if (int r = kv_args(k, T, B, offsets, lens, &a.c)) return r;
-  if (!kv_heads_ok(k, q_heads, T, B)) return WQ_ERR_SHAPE;
-  if (ldq < q_heads * k->head_dim || ldo < q_heads * k->head_dim || !std::isfinite(scale)) return WQ_ERR_SHAPE;
+  if (int r = attention_args(c, k, q, ldq, T, q_heads, B, offsets, lens, scale, causal, out, ldo, lse, &workspace, &workspace_bytes, &a))
+    return r;
   if (T == 0 || B == 0) return WQ_OK;
-  if (!q || !out) return WQ_ERR_NULL;
-  if (!al16(q) || !al16(out) || ldq % 8 != 0 || ldo % 8 != 0) return WQ_ERR_ALIGN;
-  a.q = static_cast<const uint16_t*>(q);
-  a.ldq = ldq;
-  a.out = static_cast<uint16_t*>(out);
-  a.ldo = ldo;
-  a.lse = lse;
-  a.scale = scale;
-  a.R = (int)(q_heads / k->heads);
-  a.causal = causal != 0;
-  if (workspace == nullptr) {
-    workspace = c->ws;
-    workspace_bytes = c->ws_bytes;
-  } else if (!al16(workspace)) {
-    return WQ_ERR_ALIGN;
-  }
   if (workspace_bytes < wq::kv_attention_workspace(a.c, a.R, c->num_cu)) return WQ_ERR_WORKSPACE;
   DeviceGuard g(c->device);
   hipError_t e = wq::launch_kv_attention(a, k->code == WQ_KV_INT8, c->num_cu, workspace,
@@ -987,6 +999,120 @@ int wq_kv_attention(wq_ctx* c, const wq_kv_cache* k, const void* q, int64_t ldq,
     std::fprintf(stderr, "[wq] kv_attention %s T=%lld B=%lld heads=%lld/%lld D=%lld page=%lld: path %d\n",
                  k->code == WQ_KV_INT8 ? "int8" : "e4m3", (long long)T, (long long)B, (long long)q_heads,
                  (long long)k->heads, (long long)k->head_dim, (long long)k->page_tokens, wq::kv_attention_path(a.c, a.R, c->num_cu));
+  return status_of(e);
+}
+
+int wq_add_rms_quant(wq_ctx* c, const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* rms_gamma, float rms_eps,
+                     int64_t M, int64_t K, int payload, void* x_q, void* x_s, void* sum, int64_t lds, void* y, int64_t ldy,
+                     void* stream) {
+  if (!c) return WQ_ERR_NULL;
+  if (payload != WQ_PAYLOAD_INT8 && payload != WQ_PAYLOAD_FP8_E4M3 && payload != WQ_PAYLOAD_MXFP8)
+    return payload == WQ_PAYLOAD_MXFP4 || payload == WQ_PAYLOAD_MXFP8_W4 ? WQ_ERR_UNSUPPORTED : WQ_ERR_SHAPE;
+  const int64_t unit = payload == WQ_PAYLOAD_INT8 ? 16 : payload == WQ_PAYLOAD_FP8_E4M3 ? 128 : 32;
+  if (M < 0 || M > INT32_MAX - 3 || K <= 0 || K % unit != 0 || K > 65536 || ldx < K || (residual && ldr < K) || (sum && lds < K) ||
+      (y && ldy < K))
+    return WQ_ERR_SHAPE;
+  if (M == 0) return WQ_OK;
+  if (!x || !rms_gamma || !x_q || !x_s) return WQ_ERR_NULL;
+  if (!al16(x) || !al16(residual) || !al16(rms_gamma) || !al16(x_q) || !al16(x_s) || !al16(sum) || !al16(y) || ldx % 8 != 0 ||
+      (residual && ldr % 8 != 0) || (sum && lds % 8 != 0) || (y && ldy % 8 != 0))
+    return WQ_ERR_ALIGN;
+  wq::NormArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.ldr = ldr;
+  a.gamma = static_cast<const uint16_t*>(rms_gamma);
+  a.eps = rms_eps;
+  a.inv_k = 1.0 / (double)K;
+  a.M = M;
+  a.K = (int)K;
+  a.sum = static_cast<uint16_t*>(sum);
+  a.lds = lds;
+  a.y = static_cast<uint16_t*>(y);
+  a.ldy = ldy;
+  a.xq = static_cast<uint8_t*>(x_q);
+  a.xs = x_s;
+  DeviceGuard g(c->device);
+  hipError_t e = wq::launch_add_rms_quant(
+      a, payload == WQ_PAYLOAD_INT8 ? wq::kNormInt8 : payload == WQ_PAYLOAD_FP8_E4M3 ? wq::kNormE4m3 : wq::kNormMx, c->num_cu,
+      static_cast<hipStream_t>(stream));
+  if (c->log)
+    std::fprintf(stderr, "[wq] add_rms_quant payload=%d M=%lld K=%lld residual=%d sum=%d y=%d\n", payload, (long long)M, (long long)K,
+                 residual != nullptr, sum != nullptr, y != nullptr);
+  return status_of(e);
+}
+
+int wq_kv_append_rotated(wq_ctx* c, const wq_kv_cache* k, const void* k_new, int64_t ldk, const void* v_new, int64_t ldv, const void* q,
+                         int64_t ldq, int64_t q_heads, void* q_out, int64_t ldo, const float* angles, int64_t positions, int64_t rot_dim,
+                         int interleaved, int64_t T, int64_t B, const int64_t* offsets, const int32_t* lens, void* stream) {
+  if (!c || !k) return WQ_ERR_NULL;
+  wq::KvArgs a{};
+  if (int r = kv_args(k, T, B, offsets, lens, &a)) return r;
+  const int64_t row = k->heads * k->head_dim;
+  if (ldk < row || ldv < row || rot_dim < 16 || rot_dim % 16 != 0 || rot_dim > k->head_dim || positions < 1 || positions > INT32_MAX)
+    return WQ_ERR_SHAPE;
+  if ((q != nullptr) != (q_out != nullptr)) return WQ_ERR_NULL;
+  if (q && (q_heads < k->heads || q_heads % k->heads != 0 || q_heads > (1 << 20) || ldq < q_heads * k->head_dim ||
+            ldo < q_heads * k->head_dim))
+    return WQ_ERR_SHAPE;
+  if (T == 0 || B == 0) return WQ_OK;
+  if (!k_new || !v_new || !angles) return WQ_ERR_NULL;
+  if (!al16(k_new) || !al16(v_new) || !al16(q) || !al16(q_out) || !al16(angles) || ldk % 8 != 0 || ldv % 8 != 0 ||
+      (q && (ldq % 8 != 0 || ldo % 8 != 0)))
+    return WQ_ERR_ALIGN;
+  wq::TurnArgs t{};
+  t.angles = angles;
+  t.positions = positions;
+  t.rot = (int)rot_dim;
+  t.q = static_cast<const uint16_t*>(q);
+  t.ldq = ldq;
+  t.q_out = static_cast<uint16_t*>(q_out);
+  t.ldo = ldo;
+  t.R = q ? (int)(q_heads / k->heads) : 0;
+  DeviceGuard g(c->device);
+  hipError_t e = wq::launch_kv_append_rotated(a, k->code == WQ_KV_INT8, interleaved != 0, static_cast<const uint16_t*>(k_new), ldk,
+                                              static_cast<const uint16_t*>(v_new), ldv, t, static_cast<hipStream_t>(stream));
+  if (c->log)
+    std::fprintf(stderr, "[wq] kv_append_rotated %s T=%lld B=%lld heads=%lld/%lld D=%lld turned=%lld page=%lld\n",
+                 k->code == WQ_KV_INT8 ? "int8" : "e4m3", (long long)T, (long long)B, (long long)(q ? q_heads : 0), (long long)k->heads,
+                 (long long)k->head_dim, (long long)rot_dim, (long long)k->page_tokens);
+  return status_of(e);
+}
+
+// attention behind a shared prefix: up to twice the tiles, up to three units a step
+constexpr double kSharedUnit = 8.0;
+
+int64_t wq_kv_attention_shared_workspace_bytes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B) {
+  wq::KvArgs a{};
+  if (int r = kv_sizes(c, k, T, q_heads, B, &a, kSharedUnit)) return r < 0 ? r : 0;
+  return (int64_t)wq::kv_shared_workspace(a, (int)(q_heads / k->heads), c->num_cu);
+}
+
+int wq_kv_attention_shared_path(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B) {
+  wq::KvArgs a{};
+  if (int r = kv_sizes(c, k, T, q_heads, B, &a, kSharedUnit)) return r < 0 ? r : 0;
+  return wq::kv_shared_path(a, (int)(q_heads / k->heads), c->num_cu);
+}
+
+int wq_kv_attention_shared(wq_ctx* c, const wq_kv_cache* k, const void* q, int64_t ldq, int64_t T, int64_t q_heads, int64_t B,
+                           const int64_t* offsets, const int32_t* lens, const int32_t* group, const int32_t* shared, float scale,
+                           int causal, void* out, int64_t ldo, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!c || !k) return WQ_ERR_NULL;
+  wq::KvAttnArgs a{};
+  if (int r = attention_args(c, k, q, ldq, T, q_heads, B, offsets, lens, scale, causal, out, ldo, lse, &workspace, &workspace_bytes, &a))
+    return r;
+  if (T == 0 || B == 0) return WQ_OK;
+  if (!kv_heads_ok(k, q_heads, T, B, kSharedUnit)) return WQ_ERR_SHAPE;
+  if (!group || !shared) return WQ_ERR_NULL;
+  if (workspace_bytes < wq::kv_shared_workspace(a.c, a.R, c->num_cu)) return WQ_ERR_WORKSPACE;
+  DeviceGuard g(c->device);
+  hipError_t e = wq::launch_kv_attention_shared(a, k->code == WQ_KV_INT8, group, shared, c->num_cu, workspace,
+                                                static_cast<hipStream_t>(stream));
+  if (c->log)
+    std::fprintf(stderr, "[wq] kv_attention_shared %s T=%lld B=%lld heads=%lld/%lld D=%lld page=%lld: path %d\n",
+                 k->code == WQ_KV_INT8 ? "int8" : "e4m3", (long long)T, (long long)B, (long long)q_heads, (long long)k->heads,
+                 (long long)k->head_dim, (long long)k->page_tokens, wq::kv_shared_path(a.c, a.R, c->num_cu));
   return status_of(e);
 }
 

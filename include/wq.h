@@ -193,6 +193,30 @@ int wq_group_quant_mxfp4(wq_ctx* ctx, const void* x, int64_t T, int64_t G, int64
 int wq_group_dequant_mxfp4(wq_ctx* ctx, const uint8_t* x_q, const int32_t* x_s, int64_t T, int64_t G, int64_t D,
                            void* y, void* stream);
 
+/* ---- residual, RMSNorm and 8-bit rows ---------------------------------------------------
+ * What stands in front of a layer's projections, in one pass: the residual's addition, the norm
+ * of "DeepSeek V4 950 低精度优化全复盘" section 2.3 and the quantisation that the payload reads.
+ * x, residual: bf16 [M, K], row strides ldx, ldr (elements); residual may be NULL.
+ *   h[k] = bf16_RN(x[k] + residual[k])                    (x[k] without a residual)
+ *   v[k] = (h[k] * inv) * rms_gamma[k],  inv = 1 / sqrt(f32(sum_k h^2 / K) + rms_eps)
+ * with the sum in f64 and every other step one f32 rounding; v is not rounded before its codes.
+ * sum: bf16 [M, K], row stride lds, gets h; y: bf16 [M, K], row stride ldy, gets bf16_RN(v); either
+ * may be NULL, and sum may be x or residual itself, at its own stride (the residual stream in
+ * place); outputs overlap nothing else.
+ *   WQ_PAYLOAD_INT8: x_q int8 [M, K], x_s f32 [M], as wq_dynamic_quant:
+ *     x_s = RN(max |v| / 127), x_q = rint(RN(v / x_s))    (0 where the row is 0); K % 16 == 0
+ *   WQ_PAYLOAD_FP8_E4M3, WQ_PAYLOAD_MXFP8: x_q E4M3 codes [M, K], x_s the packed words
+ *     [1, PH, TA] of wq_group_quant_fp8_ue8m0 and wq_group_quant_mxfp8 with G = 1 (TA = 4 ceil(M / 4)):
+ *     e = max(-127, smallest e with 448 * 2^e >= max |v| of the block), x_q = E4M3FN(v * 2^-e);
+ *     K % 128 == 0, K % 32 == 0; every word's byte that stands for no block is zero.
+ *   Other payloads: WQ_ERR_UNSUPPORTED.
+ * A row whose h holds a NaN or an infinity has v = NaN throughout.  A row of INT8 or a block that
+ * holds a value that is not finite gets zero codes and the scale NaN, or byte 255, UE8M0's NaN:
+ * products with it give NaN.  1 <= K <= 65536. */
+int wq_add_rms_quant(wq_ctx* ctx, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                     const void* rms_gamma, float rms_eps, int64_t M, int64_t K, int payload, void* x_q, void* x_s,
+                     void* sum, int64_t lds, void* y, int64_t ldy, void* stream);
+
 /* ---- quantised matmul ---------------------------------------------------------------
  * INT8 (section 一 of the W8A8 article; npu_quant_matmul, and the tuple-reuse path where
  * an upstream producer already gave (x_q, x_scale)):
@@ -380,6 +404,25 @@ typedef struct {
 int wq_kv_append(wq_ctx* ctx, const wq_kv_cache* cache, const void* k_new, int64_t ldk, const void* v_new, int64_t ldv,
                  int64_t T, int64_t B, const int64_t* offsets, const int32_t* lens, void* stream);
 
+/* wq_kv_append with the keys turned by their tokens' positions on the way (rotary positions), and
+ * the queries of the same rows turned by the same angles, in one launch.
+ * angles: f32 [positions][2][rot_dim / 2], for each position the cosines and then the sines of its
+ * frequencies (made once); 16 <= rot_dim <= head_dim, rot_dim % 16 == 0.  Of each head the first
+ * rot_dim elements are turned in pairs (a, b): elements (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ * interleaved != 0, by frequency i:
+ *   a' = a c - b s,  b' = b c + a s                       (f32, each product and sum rounded)
+ * The position is the token's in its sequence, lens[b] - n + i for row i of n.  Keys go to their
+ * codes from a' and b' as they are (in wq_kv_append's rules read them for x), values as in
+ * wq_kv_append; q_out gets bf16_RN of the queries.  q, q_out: bf16 [T, q_heads * head_dim], row
+ * strides ldq, ldo, q_heads a multiple of the cache's heads; q_out may be q at the same stride; both
+ * NULL: no queries.  A position outside [0, positions) has no angle: its elements in pairs become
+ * NaN (a key's page is then marked as wq_kv_append marks it; tokens at negative positions are not
+ * written).  Rows of no sequence are left as they are in q_out. */
+int wq_kv_append_rotated(wq_ctx* ctx, const wq_kv_cache* cache, const void* k_new, int64_t ldk, const void* v_new,
+                         int64_t ldv, const void* q, int64_t ldq, int64_t q_heads, void* q_out, int64_t ldo,
+                         const float* angles, int64_t positions, int64_t rot_dim, int interleaved, int64_t T,
+                         int64_t B, const int64_t* offsets, const int32_t* lens, void* stream);
+
 /* Attention of T query rows over the cache: q bf16 [T, q_heads * head_dim], row stride ldq;
  * q_heads = R * heads, query head i reads cache head i / R.  Row i of n of sequence b sees the
  * tokens 0 .. lens[b] - n + i (causal != 0) or 0 .. lens[b] - 1:
@@ -414,6 +457,32 @@ int64_t wq_kv_attention_workspace_bytes(const wq_ctx* ctx, const wq_kv_cache* ca
  *   8 more where the items are few and their parts many, so that a join is split over columns.
  * 0 for an empty problem; a negative value is -status.  Host only: no device work. */
 int wq_kv_attention_path(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T, int64_t q_heads, int64_t B);
+
+/* wq_kv_attention of sequences that begin with the same pages (a system prompt, several answers to
+ * one question): the same rows, masks and outputs, with what is shared read and multiplied once for
+ * all rows that share it.  group, shared: device int32 [B].  Neighbouring sequences with the same
+ * id, not negative, are a group; shared[b] is the number of tokens from its first on that sequence b
+ * has in common with the others of its group, in the same pages: the tables' first
+ * floor(shared / page_tokens) entries are equal over the group (where they are not, the entries of
+ * its first sequence with rows are taken).  A group's least such number counts, in whole pages and
+ * whole steps of 64 tokens, and no more than every row of it sees; the remaining tokens are read for
+ * each sequence.  Results differ from wq_kv_attention's by the order of f32 sums alone.
+ * workspace: as there, of at least wq_kv_attention_shared_workspace_bytes(); NULL: the context's
+ * (WQ_ERR_WORKSPACE where that is too small). */
+int wq_kv_attention_shared(wq_ctx* ctx, const wq_kv_cache* cache, const void* q, int64_t ldq, int64_t T,
+                           int64_t q_heads, int64_t B, const int64_t* offsets, const int32_t* lens,
+                           const int32_t* group, const int32_t* shared, float scale, int causal, void* out,
+                           int64_t ldo, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* As wq_kv_attention_workspace_bytes, of wq_kv_attention_shared: two f32 rows for every output row
+ * besides the workgroups' own; not bounded by the context's workspace. */
+int64_t wq_kv_attention_shared_workspace_bytes(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T,
+                                               int64_t q_heads, int64_t B);
+
+/* As wq_kv_attention_path, of wq_kv_attention_shared: 16 where the shared tokens are taken once;
+ * sequences of 64 rows and more on average (rows times q_heads / heads) fill row tiles of their own
+ * and take wq_kv_attention's kernels, numbered as there. */
+int wq_kv_attention_shared_path(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T, int64_t q_heads, int64_t B);
 
 /* ---- expert sort (MoE) ---------------------------------------------------------------
  * "DeepSeek V4 950" section 3.2: sort the (token, slot) pairs by expert id before the

@@ -27,6 +27,7 @@ Modules:
   moe         expert sort, RMSNorm+quant, segmented GEMM, SwiGLU+requant.
   mxfp4       4-bit microscaled blocks: quant, inverse, product.
   kv_cache    paged 8-bit cache: append, attention.
+  layer       residual, norm and 8-bit rows; keys turned on their way into the cache.
 """
 
-from . import numerics, int8_linear, fp8_group, moe, mxfp4, kv_cache  # noqa: F401
+from . import numerics, int8_linear, fp8_group, moe, mxfp4, kv_cache, layer  # noqa: F401
