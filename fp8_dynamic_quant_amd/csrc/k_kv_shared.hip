@@ -3,16 +3,20 @@
 // Neighbouring sequences of one group id share their first tokens.  A softmax over [shared | own]
 // splits into one over each, joined by their maxima and sums, so that the shared tokens are taken
 // once for all rows of the group: its rows are one run of rows (row * R + query head, as in
-// attention of one sequence) in tiles of up to 128, all of which see all of those tokens.  Each
-// sequence's own tokens are taken for its rows alone.
+// attention of one sequence) in tiles, all of which see all of those tokens.  Each sequence's own
+// tokens are taken for its rows alone.
 //
-// The work of both kinds, (sequence, head, row tile) items over own tokens and (group, head, row
-// tile) items over shared ones, is laid on one axis in units of cost and cut into equal runs, one a
-// workgroup.  A row's parts, of at least two items where it shares and of as many runs as cut them,
-// go to the workspace in f32 and are joined by a second kernel, in the order of the axis: results
-// do not depend on timing.
+// Items are (sequence, head, row tile) over own tokens and (group, head, row tile) over shared ones.
+// Of up to 16 rows they are narrow: a wave takes one alone, straight from memory.  Of more they are
+// wide: a workgroup of eight waves takes one (Wide).  The items of either kind lie on an axis of
+// their own, in units of a step of 64 tokens and a constant for an item's beginning and end, which
+// is cut into equal runs: of narrow ones one a wave, of wide ones one a workgroup.  Reading bounds
+// the narrow, arithmetic the wide, so half of the workgroups begin with one kind and half with the
+// other.  A row's parts, of both items where it shares and of as many runs as cut them, go to the
+// workspace in f32 and are joined by a second kernel in the order of the axes: results do not depend
+// on timing.
 #include "wq_kernels.h"
-#include "wq_kv_attn.h"
+#include "wq_kv_wide.h"
 #include "wq_layer.h"
 
 namespace wq {
@@ -20,36 +24,26 @@ namespace wq {
 namespace {
 
 constexpr int kShareSeqs = 512;  // sequences of one launch (their plan is held in LDS)
-constexpr int kMaxParts = 1024;  // parts of an item: no more than runs
+constexpr int kThreads = 64 * kWideWaves;
+
+enum { kNarrow = 0, kWide = 1 };
+constexpr int kNarrowRows = 16;
+__host__ __device__ constexpr int wide_rows(int D) { return D == 256 ? 128 : 256; }
+// rows of the workspace for the narrow runs of a workgroup (a wave does not hold a head of 256)
+__host__ __device__ constexpr int narrow_slots(int D) { return D == 256 ? 0 : kWideWaves * kNarrowRows; }
 
 struct ShareArgs {
-  KvAttnArgs a;            // part, stat: [2 T Hq + runs * tile] rows; runs, least
+  KvAttnArgs a;            // part, stat: [2 keys + workgroups * (narrow_slots + wide_rows)] rows
   const int32_t* group;    // [B]
   const int32_t* shared;   // [B]
-  uint4* desc;             // [T * Hq]
+  uint4* desc;             // [keys], keys = T * Hq
+  uint32_t least[2];       // units of a run, by kind
 };
-
-// Where the parts of a row are: of its own tokens' item and of the shared ones' item the first run,
-// how many, and the row's place in the tile.  Part 0 of an item has a slot by (token, query head),
-// part p > 0 one by its run, which begins inside no other item.
-__device__ __forceinline__ uint4 pack_desc(int run0, int parts0, int tile_row0, int run1, int parts1, int tile_row1) {
-  return uint4{(uint32_t)run0 | (uint32_t)parts0 << 16, (uint32_t)run1 | (uint32_t)parts1 << 16,
-               (uint32_t)tile_row0 | (uint32_t)tile_row1 << 16, 0u};
-}
-
-// Rows of a tile, the units that a step of 64 tokens costs, and an item besides its steps.
-struct Cost {
-  int tile, step, fixed;
-};
-template <int D>
-__device__ __forceinline__ Cost cost_of(int64_t rows) {
-  if (D < 256 && rows <= 16) return Cost{16, 1, 2 * kAttnWaves};
-  if (D == 256 || rows <= 64) return Cost{64, 2, 8};
-  return Cost{128, 3, 12};
-}
+// units that an item counts besides its steps
+__device__ __forceinline__ uint32_t fixed_units(int kind) { return kind == kNarrow ? 4u : 6u; }
 
 struct ShareLds {
-  int64_t pre[kShareSeqs + 1];  // units before sequence b, for one head
+  uint32_t pre[2][kShareSeqs + 1];  // by kind: units before sequence b, for one head
   int row0[kShareSeqs + 1];
   int len[kShareSeqs];
   int id[kShareSeqs];
@@ -58,8 +52,8 @@ struct ShareLds {
   int end[kShareSeqs];     // where its rows end,
   int many[kShareSeqs];    // how many sequences have rows,
   int holder[kShareSeqs];  // the first that does: its table names the shared pages
-  int64_t carry[kAttnWaves];
-  int last[kAttnWaves];
+  uint32_t carry[2][kWideWaves];
+  int last[kWideWaves];
 };
 
 // steps that the group led by sequence `lead` shares
@@ -70,464 +64,527 @@ __device__ __forceinline__ uint32_t shared_steps(const ShareLds& l, int lead) {
 __device__ __forceinline__ uint32_t own_steps(const KvArgs& c, int len, uint32_t shared) {
   return (uint32_t)max((int)steps_of(c, len) - (int)shared, 1);
 }
+__device__ __forceinline__ uint32_t own_rows(const ShareLds& l, int b) { return (uint32_t)max(l.row0[b + 1] - l.row0[b], 0); }
+__device__ __forceinline__ uint32_t group_rows(const ShareLds& l, int lead) { return (uint32_t)max(l.end[lead] - l.row0[lead], 0); }
 
-__device__ __forceinline__ int64_t group_rows(const ShareLds& l, int lead) { return max(l.end[lead] - l.row0[lead], 0); }
-
-struct SharePlan {
-  int64_t units, per;
-  int runs;
+// The items of `rows` rows (tokens times R) over `steps` steps
+struct Kind {
+  int kind;
+  uint32_t tile, tiles, steps, units;  // rows of a tile; tiles; units of an item
 };
-__device__ __forceinline__ int64_t item_units(const Cost& k, uint32_t steps) { return k.fixed + (int64_t)k.step * steps; }
-__device__ __forceinline__ int tiles_of(const Cost& k, int64_t rows) { return (int)((rows + k.tile - 1) / k.tile); }
+template <int D>
+__device__ __forceinline__ Kind kind_of(uint32_t rows, uint32_t steps) {
+  Kind k;
+  k.kind = D < 256 && rows <= kNarrowRows ? kNarrow : kWide;
+  k.tile = k.kind == kNarrow ? kNarrowRows : wide_rows(D);
+  k.tiles = (rows + k.tile - 1) / k.tile;
+  k.steps = steps;
+  k.units = steps + fixed_units(k.kind);
+  return k;
+}
 
+struct Axis {
+  uint32_t units, per, runs;
+};
+struct SharePlan {
+  Axis axis[2];
+};
 // Every thread of the workgroup takes part.
 template <int D>
 __device__ __forceinline__ SharePlan make_share_plan(const ShareArgs& s, ShareLds& l) {
   const KvAttnArgs& a = s.a;
   const KvArgs& c = a.c;
-  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
-  constexpr int kThreads = 64 * kAttnWaves;
-  for (int b = t; b < c.B; b += kThreads) {
-    const int64_t lo = seq_offset(c, b), rows = max(seq_offset(c, b + 1) - lo, (int64_t)0);
-    l.row0[b] = (int)lo;
-    l.len[b] = c.lens[b];
-    l.id[b] = s.group[b];
+  const int b = threadIdx.x, lane = b & 63, wv = b >> 6;
+  const bool in = b < c.B;
+  static_assert(kShareSeqs == kThreads, "a thread for each sequence");
+  int row0 = 0, rows = 0, len = 0, wants = 0, id = -1;
+  if (in) {
+    row0 = (int)seq_offset(c, b);
+    rows = max((int)seq_offset(c, b + 1) - row0, 0);
+    len = c.lens[b];
+    id = s.group[b];
+    wants = s.shared[b];
+    l.row0[b] = row0;
+    l.len[b] = len;
+    l.id[b] = id;
     l.steps[b] = INT32_MAX;
     l.end[b] = 0;
     l.many[b] = 0;
     l.holder[b] = INT32_MAX;
-    if (b == c.B - 1) l.row0[c.B] = (int)(lo + rows);
+    if (b == c.B - 1) l.row0[c.B] = row0 + rows;
   }
   __syncthreads();
-  int before = 0;
-  for (int b0 = 0; b0 < c.B; b0 += kThreads) {
-    // the last sequence up to b that begins a group
-    const int b = b0 + t;
-    int lead = b < c.B && b > 0 && (l.id[b] < 0 || l.id[b] != l.id[b - 1]) ? b : 0;
+  // the last sequence up to b that begins a group
+  int lead = in && b > 0 && (id < 0 || id != l.id[b - 1]) ? b : 0;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(lead, o, 64);
+    if (lane >= o) lead = max(lead, u);
+  }
+  if (lane == 63) l.last[wv] = lead;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWideWaves; ++w)
+    if (w < wv) lead = max(lead, l.last[w]);
+  if (in) {
+    l.lead[b] = lead;
+    if (rows > 0) {
+      // the whole pages that all of its rows see, in whole steps
+      int64_t own = min((int64_t)len - (a.causal ? rows : 0), (int64_t)c.max_pages * c.P);
+      own = max(min((int64_t)wants, own), (int64_t)0);
+      atomicMin(&l.steps[lead], (int)((uint32_t)own / (uint32_t)c.P * (uint32_t)c.P / kTokTile));
+      atomicMax(&l.end[lead], row0 + rows);
+      atomicAdd(&l.many[lead], 1);
+      atomicMin(&l.holder[lead], b);
+    }
+  }
+  __syncthreads();
+  uint32_t v[2] = {0, 0};
+  if (in) {
+    auto add = [&](const Kind& k) __attribute__((always_inline)) {
+      v[kNarrow] += k.kind == kNarrow ? k.tiles * k.units : 0u;
+      v[kWide] += k.kind == kWide ? k.tiles * k.units : 0u;
+    };
+    const uint32_t sh = shared_steps(l, lead);
+    add(kind_of<D>((uint32_t)rows * (uint32_t)a.R, own_steps(c, len, sh)));
+    if (lead == b && sh > 0) add(kind_of<D>(group_rows(l, b) * (uint32_t)a.R, sh));
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(lead, o, 64);
-      if (lane >= o) lead = max(lead, u);
+      const uint32_t u = (uint32_t)__shfl_up((int)v[k], o, 64);
+      if (lane >= o) v[k] += u;
     }
-    if (lane == 63) l.last[wv] = lead;
-    __syncthreads();
-    lead = max(lead, before);
-#pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
-      if (w < wv) lead = max(lead, l.last[w]);
-      before = max(before, l.last[w]);
-    }
-    if (b < c.B) {
-      l.lead[b] = lead;
-      const int row0 = l.row0[b], rows = l.row0[b + 1] - row0;
-      if (rows > 0) {
-        // the whole pages that all of its rows see, in whole steps
-        int64_t own = min((int64_t)l.len[b] - (a.causal ? rows : 0), (int64_t)c.max_pages * c.P);
-        own = max(min((int64_t)s.shared[b], own), (int64_t)0);
-        atomicMin(&l.steps[lead], (int)(own / c.P * c.P / kTokTile));
-        atomicMax(&l.end[lead], row0 + rows);
-        atomicAdd(&l.many[lead], 1);
-        atomicMin(&l.holder[lead], b);
-      }
-    }
-    __syncthreads();
+    if (lane == 63) l.carry[k][wv] = v[k];
   }
-  int64_t sum = 0;
-  for (int b0 = 0; b0 < c.B; b0 += kThreads) {
-    const int b = b0 + t;
-    int64_t v = 0;
-    if (b < c.B) {
-      const int row0 = l.row0[b], lead = l.lead[b];
-      const int64_t rows = (int64_t)max(l.row0[b + 1] - row0, 0) * a.R;
-      const uint32_t sh = shared_steps(l, lead);
-      const Cost k = cost_of<D>(rows);
-      v = tiles_of(k, rows) * item_units(k, own_steps(c, l.len[b], sh));
-      if (lead == b && sh > 0) {
-        const int64_t all = group_rows(l, b) * a.R;
-        const Cost kg = cost_of<D>(all);
-        v += tiles_of(kg, all) * item_units(kg, sh);
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t u = __shfl_up(v, o, 64);
-      if (lane >= o) v += u;
-    }
-    if (lane == 63) l.carry[wv] = v;
-    __syncthreads();
-    int64_t base = sum;
-    for (int w = 0; w < wv; ++w) base += l.carry[w];
-    if (b < c.B) l.pre[b + 1] = base + v;
-#pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) sum += l.carry[w];
-    if (b == 0) l.pre[0] = 0;
-    __syncthreads();
-  }
+  __syncthreads();
   SharePlan p;
-  p.units = sum * c.H;
-  p.per = max(quotient(p.units + a.runs - 1, a.runs), (int64_t)a.least);
-  p.runs = (int)quotient(p.units + p.per - 1, p.per);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t base = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWideWaves; ++w) {
+      base += w < wv ? l.carry[k][w] : 0u;
+      sum += l.carry[k][w];
+    }
+    if (in) l.pre[k][b + 1] = base + v[k];
+    if (b == 0) l.pre[k][0] = 0;
+    Axis& x = p.axis[k];
+    const uint32_t runs = (uint32_t)gridDim.x * (k == kNarrow ? kWideWaves : 1);
+    x.units = (uint32_t)uniform((int)(sum * (uint32_t)c.H));
+    x.per = max((x.units + runs - 1) / runs, s.least[k]);
+    x.runs = (x.units + x.per - 1) / x.per;
+  }
+  __syncthreads();
   return p;
 }
 
-// The item that unit u is in.  Of a sequence's units, those of its own tokens' items come first,
-// then, of a group's first sequence, the shared ones'.
+// The item of a kind that unit u of its axis is in.  Of a sequence's units those of its own tokens'
+// items come first, then, of a group's first sequence, the shared ones'.
 struct ShareItem {
   int b;             // the sequence, or the one whose table the group takes
   bool of_group;
-  int h, tile;
-  Cost cost;
+  uint32_t h, tile;
+  Kind k;
   uint32_t shared;   // steps that the group shares: own tokens' steps begin there
-  uint32_t steps;    // of the item
-  int64_t row0;      // token rows
-  int rows;
-  int64_t i0, units; // the item's units
+  int row0, rows;    // tokens
+  uint32_t i0;       // the item's first unit
 };
-template <int D>
-__device__ __forceinline__ ShareItem share_item(const ShareArgs& s, const ShareLds& l, int64_t u) {
+template <int D, int KIND>
+__device__ __forceinline__ ShareItem share_item(const ShareArgs& s, const ShareLds& l, uint32_t u, int lane) {
   const KvArgs& c = s.a.c;
-  int lo = 0, hi = c.B - 1;
-  while (lo < hi) {  // the last sequence that begins at or before u (of equal ones the one with work)
-    const int mid = (lo + hi + 1) >> 1;
-    if (l.pre[mid] * c.H <= u) lo = mid;
-    else hi = mid - 1;
-  }
+  const uint32_t* pre = l.pre[KIND];
+  // the last sequence that begins at or before u (of equal ones the one with work): eight at a time, then one
+  const uint32_t H = (uint32_t)c.H;
+  const int far = 8 * (__popcll(__ballot(8 * lane < c.B && pre[min(8 * lane, c.B)] * H <= u)) - 1);
+  const int lo = uniform(far + __popcll(__ballot(lane < 8 && far + lane < c.B && pre[min(far + lane, c.B)] * H <= u)) - 1);
   ShareItem it;
-  it.b = lo = uniform(lo);
   const int lead = uniform(l.lead[lo]);
   it.shared = (uint32_t)uniform((int)shared_steps(l, lead));
+  it.b = lo;
   it.row0 = uniform(l.row0[lo]);
-  it.rows = uniform(max(l.row0[lo + 1] - l.row0[lo], 0));
-  it.steps = own_steps(c, uniform(l.len[lo]), it.shared);
-  it.cost = cost_of<D>((int64_t)it.rows * s.a.R);
-  it.units = item_units(it.cost, it.steps);
-  int64_t first = l.pre[lo] * c.H;
-  const int64_t own = (int64_t)tiles_of(it.cost, (int64_t)it.rows * s.a.R) * it.units * c.H;
+  it.rows = uniform((int)own_rows(l, lo));
+  it.k = kind_of<D>((uint32_t)it.rows * (uint32_t)s.a.R, own_steps(c, uniform(l.len[lo]), it.shared));
+  uint32_t first = (uint32_t)uniform((int)pre[lo]) * H;
+  const uint32_t own = it.k.kind == KIND ? it.k.tiles * it.k.units * H : 0u;
   it.of_group = u - first >= own;
   if (it.of_group) {
     first += own;
     it.rows = uniform((int)group_rows(l, lo));
     it.b = uniform(l.holder[lo]);
-    it.steps = it.shared;
-    it.cost = cost_of<D>((int64_t)it.rows * s.a.R);
-    it.units = item_units(it.cost, it.steps);
+    it.k = kind_of<D>((uint32_t)it.rows * (uint32_t)s.a.R, it.shared);
   }
-  const int64_t item = quotient(u - first, it.units);
-  it.i0 = first + item * it.units;
-  const int tiles = tiles_of(it.cost, (int64_t)it.rows * s.a.R);
-  it.h = uniform((int)quotient(item, tiles));
-  it.tile = uniform((int)(item - (int64_t)it.h * tiles));
+  const uint32_t item = (u - first) / it.k.units;
+  it.i0 = first + item * it.k.units;
+  it.h = item / it.k.tiles;
+  it.tile = item - it.h * it.k.tiles;
   return it;
 }
-// Step p of an item lies at unit fixed + p * step of it: a run that begins in front of that and ends
-// behind it takes the step.
-__device__ __forceinline__ uint32_t step_at(const ShareItem& it, int64_t x) {
-  if (x <= it.cost.fixed) return 0;
-  if (x >= it.units) return it.steps;
-  return (uint32_t)uniform((int)quotient(x - it.cost.fixed + it.cost.step - 1, it.cost.step));
+// step p of an item lies at its unit fixed + p: a run that begins at or before that and ends behind it
+// takes the step
+__device__ __forceinline__ uint32_t step_at(const Kind& k, uint32_t x) {
+  const uint32_t f = fixed_units(k.kind);
+  return x <= f ? 0u : min(x - f, k.steps);
 }
-__device__ __forceinline__ int run_of(const SharePlan& p, int64_t unit) { return uniform((int)quotient(unit, p.per)); }
 
-// What a run has of a row: where its output or its part goes
+// What a run has of an item, and where its rows' output or part goes
 struct Share {
   const ShareArgs& s;
+  const KvAttnArgs& a;
   ShareItem it;
   Seq q;             // the item's rows and tokens
-  KvAttnArgs a;      // (rows of a group are not masked)
-  bool first, whole; // the run has the item's first step; all of them, and nobody shares
-  int run;
+  uint32_t from, to; // steps of the sequence
+  bool whole;        // all of them, and nobody shares
+  uint32_t run;
 
-  __device__ __forceinline__ int64_t key(int64_t rr) const {  // (token, query head) of row rr
-    const int i = (int)rr / a.R;
-    return (q.row0 + i) * (int64_t)(a.c.H * a.R) + it.h * a.R + ((int)rr - i * a.R);
+  // (token, query head) of row rr
+  __device__ __forceinline__ int64_t key(uint32_t rr) const {
+    const uint32_t i = rr / (uint32_t)a.R;
+    return (q.row0 + i) * (int64_t)(a.c.H * a.R) + (it.h * (uint32_t)a.R + (rr - i * (uint32_t)a.R));
   }
-  __device__ __forceinline__ int64_t slot(int64_t rr) const {
+  __device__ __forceinline__ bool begins() const { return from == (it.of_group ? 0u : it.shared); }  // has the item's first step
+  // the row of its part: by key where the run begins the item, else by the run, which begins inside no
+  // other item
+  template <int D>
+  __device__ __forceinline__ int64_t slot(uint32_t rr, int64_t key) const {
     const int64_t keys = a.c.T * a.c.H * a.R;
-    if (first) return (it.of_group ? keys : 0) + key(rr);
-    return 2 * keys + (int64_t)run * a.tile_rows + (rr - (int64_t)it.tile * it.cost.tile);
+    if (begins()) return (it.of_group ? keys : 0) + key;
+    const int64_t at = 2 * keys + (it.k.kind == kNarrow ? (int64_t)run * kNarrowRows : (int64_t)gridDim.x * narrow_slots(D) + (int64_t)run * wide_rows(D));
+    return at + (rr - it.tile * it.k.tile);
   }
 };
-
-// The join of row rr of an own item: told by the run that has the item's first step.
-template <int D>
-__device__ __forceinline__ void tell_row(const Share& r, const SharePlan& p, const ShareLds& l, int64_t rr) {
+template <int D, int KIND>
+__device__ __forceinline__ bool take_share(Share& r, const SharePlan& p, const ShareLds& l, uint32_t u, uint32_t end, int lane) {
+  const ShareArgs& s = r.s;
+  r.it = share_item<D, KIND>(s, l, u, lane);
   const ShareItem& it = r.it;
-  if (r.whole) {
-    r.s.desc[r.key(rr)] = uint4{0, 0, 0, 0};
-    return;
+  r.from = step_at(it.k, u - it.i0);
+  r.to = step_at(it.k, min(end - it.i0, it.k.units));
+  if (r.from >= r.to) return false;
+  r.whole = !it.of_group && it.shared == 0 && r.from == 0 && r.to == it.k.steps;
+  r.q.row0 = it.row0;
+  r.q.rows = it.rows;
+  r.q.nrows = (int64_t)it.rows * s.a.R;
+  r.q.len = uniform(l.len[it.b]);
+  r.q.seen = (uint32_t)min((int64_t)max(r.q.len, 0), (int64_t)s.a.c.max_pages * s.a.c.P);
+  r.q.table = s.a.c.table + it.b * s.a.c.table_stride;
+  if (it.of_group) {  // all of its rows see all of it (limit_of, causal or not)
+    r.q.seen = it.shared * kTokTile;
+    r.q.len = (int)r.q.seen;
+    r.q.rows = 0;
+  } else {  // steps of the sequence
+    r.from += it.shared;
+    r.to += it.shared;
   }
-  auto at = [&](const Cost& k, int64_t i0, uint32_t step) { return (int)quotient(i0 + k.fixed + (int64_t)step * k.step, p.per); };
-  const int run0 = at(it.cost, it.i0, 0), parts0 = at(it.cost, it.i0, it.steps - 1) - run0 + 1;
-  int run1 = 0, parts1 = 0, row1 = 0;
-  if (it.shared > 0) {
-    const int lead = l.lead[it.b];
-    const int64_t ahead = (int64_t)l.row0[lead];
-    const int64_t all = group_rows(l, lead) * r.a.R, gr = (it.row0 - ahead) * r.a.R + rr;
-    const Cost k = cost_of<D>(all);
-    const int64_t units = item_units(k, it.shared);
-    const int tiles = tiles_of(k, all), tile = (int)(gr / k.tile);
-    // the group's units lie behind the own ones of its first sequence
-    const int64_t lr = (int64_t)max(l.row0[lead + 1] - l.row0[lead], 0) * r.a.R;
-    const Cost kl = cost_of<D>(lr);
-    const int64_t own = (int64_t)tiles_of(kl, lr) * item_units(kl, own_steps(r.a.c, l.len[lead], it.shared));
-    const int64_t i1 = (l.pre[lead] + own) * r.a.c.H + ((int64_t)it.h * tiles + tile) * units;
-    run1 = at(k, i1, 0);
-    parts1 = at(k, i1, it.shared - 1) - run1 + 1;
-    row1 = (int)(gr - (int64_t)tile * k.tile);
-  }
-  r.s.desc[r.key(rr)] = pack_desc(run0, parts0, (int)(rr - (int64_t)it.tile * it.cost.tile), run1, parts1, row1);
+  return true;
 }
 
-// A wave's own rows: to the output if nothing else has a part of them, else to the workspace
-template <int D, bool I8, int RT>
-__device__ __forceinline__ void store_share(const Share& r, Rows<D, I8, RT>& w, const SharePlan& p, const ShareLds& l, int64_t r0,
-                                            int j, int g) {
+// The join of row rr of an own item, told by the run that has the item's first step: of its own
+// tokens' item and of the shared ones' item the first run, how many, and the row's place in the tile.
+template <int D>
+__device__ __forceinline__ void tell_row(const Share& r, const SharePlan& p, const ShareLds& l, uint32_t rr, int64_t key) {
+  const ShareItem& it = r.it;
+  uint4 d{0, 0, 0, 0};
+  if (!r.whole) {
+    auto parts = [&](const Kind& k, uint32_t i0, uint32_t row) {
+      const uint32_t per = k.kind == kNarrow ? p.axis[kNarrow].per : p.axis[kWide].per, first = i0 + fixed_units(k.kind);
+      const uint32_t run = first / per;
+      return uint2{run | ((first + k.steps - 1) / per - run + 1) << 16, row % k.tile | (uint32_t)k.kind << 15};
+    };
+    const uint2 own = parts(it.k, it.i0, rr);
+    d.x = own.x;
+    d.z = own.y;
+    if (it.shared > 0) {
+      const int lead = l.lead[it.b];
+      const uint32_t R = (uint32_t)r.a.R, H = (uint32_t)r.a.c.H;
+      const uint32_t gr = (uint32_t)(it.row0 - l.row0[lead]) * R + rr;
+      const Kind k = kind_of<D>(group_rows(l, lead) * R, it.shared);
+      // the group's units lie behind the own ones of its first sequence
+      const Kind kl = kind_of<D>(own_rows(l, lead) * R, own_steps(r.a.c, l.len[lead], it.shared));
+      const uint32_t ahead = kl.kind == k.kind ? kl.tiles * kl.units : 0u;
+      const uint2 all = parts(k, (l.pre[k.kind][lead] + ahead) * H + (it.h * k.tiles + gr / k.tile) * k.units, gr);
+      d.y = all.x;
+      d.z |= all.y << 16;
+    }
+  }
+  r.s.desc[key] = d;
+}
+
+// A wave's own rows, to the output if nothing else has a part of them, else to the workspace: lane
+// (j, g) holds of row j the elements 16 i + 4 g .. + 3
+template <int D>
+__device__ __forceinline__ void store_share(const Share& r, const SharePlan& p, const ShareLds& l, const v4f (&o)[D / 16], float mx,
+                                            float sum, uint32_t rr, int g) {
+  const float total = groups_sum(sum);
+  if (rr >= (uint32_t)r.q.nrows) return;
+  const int64_t key = r.key(rr);
   if (r.whole) {
-    store_rows(r.a, r.q, w, r.it.h, r0, j, g);
+    const int64_t hq = r.a.c.H * r.a.R, token = r.q.row0 + rr / (uint32_t)r.a.R;
+    uint16_t* out = r.a.out + token * r.a.ldo + (key - token * hq) * D + 4 * g;
+    const float inv = inverse_sum(total);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const v4f v = o[i] * inv;
+      *reinterpret_cast<v2u*>(out + 16 * i) = v2u{f32_to_bf16_nan(v[0]) | f32_to_bf16_nan(v[1]) << 16,
+                                                  f32_to_bf16_nan(v[2]) | f32_to_bf16_nan(v[3]) << 16};
+    }
+    if (r.a.lse && g == 0) r.a.lse[key] = log_sum(mx, total);
   } else {
+    const int64_t slot = r.template slot<D>(rr, key);
+    float* to = r.a.part + slot * D + 4 * g;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const float sum = groups_sum(w.sum[rt]);
-      const int64_t rr = r0 + 16 * rt + j;
-      if (rr >= r.q.nrows) continue;
-      const int64_t slot = r.slot(rr);
-      float* to = r.a.part + slot * D + 4 * g;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) *reinterpret_cast<v4f*>(to + 16 * i) = w.o[rt][i];
-      if (g == 0) r.a.stat[slot] = float2{w.mx[rt], sum};
-    }
+    for (int i = 0; i < D / 16; ++i) *reinterpret_cast<v4f*>(to + 16 * i) = o[i];
+    if (g == 0) r.a.stat[slot] = float2{mx, total};
   }
-  if (r.first && !r.it.of_group && g == 0) {
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-      if (r0 + 16 * rt + j < r.q.nrows) tell_row<D>(r, p, l, r0 + 16 * rt + j);
-  }
+  if (g == 0 && !r.it.of_group && r.begins()) tell_row<D>(r, p, l, rr, key);
 }
 
-// 64 RT rows, whose waves share the keys through LDS
-template <int D, bool I8, int RT, int S>
-__device__ __forceinline__ void take_wide(const Share& r, const SharePlan& p, const ShareLds& l, uint32_t lo, uint32_t hi, uint8_t* smem,
-                                          int wv, int lane) {
-  const int j = lane & 15, g = lane >> 4;
-  const int64_t t0 = (int64_t)r.it.tile * 64 * RT, r0 = t0 + wv * 16 * RT;
-  auto steps_to = [&](int64_t row) {
-    return (uint32_t)uniform((int)((limit_of(r.a, r.q, (int)(row / r.a.R)) + kTokTile - 1) / kTokTile));
-  };
-  Rows<D, I8, RT> w;
-  w.limits(r.a, r.q, r0, j);
-  w.load_q(r.a, r.q, r.it.h, r0, j, g);
-  SharedRows<D, I8, RT, S>::run(w, r.a, r.q, r.it.h, lo, min(hi, steps_to(min(t0 + 64 * RT, r.q.nrows) - 1)),
-                                r0 < r.q.nrows ? steps_to(min(r0 + 16 * RT, r.q.nrows) - 1) : 0, smem, wv, lane);
-  store_share(r, w, p, l, r0, j, g);
+// the steps that the rows up to `row` see
+__device__ __forceinline__ uint32_t steps_to(const Share& r, int64_t row, uint32_t tokens) {
+  return (uint32_t)uniform((int)((limit_of(r.a, r.q, (int)(min(row, r.q.nrows) - 1) / r.a.R) + tokens - 1) / tokens));
 }
 
-// 16 rows, whose waves take steps in turn and are joined in LDS
 template <int D, bool I8>
-struct NarrowLds {
-  float o[kAttnWaves][16][D + 4], m[kAttnWaves][16], l[kAttnWaves][16];
-};
-template <int D, bool I8>
-__device__ __forceinline__ void take_narrow(const Share& r, const SharePlan& p, const ShareLds& l, uint32_t lo, uint32_t hi,
-                                            NarrowLds<D, I8>& n, int wv, int lane) {
+__device__ __forceinline__ void narrow_runs(const ShareArgs& s, const SharePlan& p, const ShareLds& l, uint32_t run, int lane) {
   const int j = lane & 15, g = lane >> 4;
-  const int64_t r0 = (int64_t)r.it.tile * 16;
-  const uint32_t most = (uint32_t)uniform((int)((limit_of(r.a, r.q, (int)((min(r0 + 16, r.q.nrows) - 1) / r.a.R)) + kTokTile - 1) / kTokTile));
-  {
+  const uint32_t per = p.axis[kNarrow].per, end = min((run + 1) * per, p.axis[kNarrow].units);
+  for (uint32_t u = run * per; u < end;) {
+    Share r{s, s.a};
+    r.run = run;
+    const bool some = take_share<D, kNarrow>(r, p, l, u, end, lane);
+    u = r.it.i0 + r.it.k.units;
+    if (!some) continue;
+    const int64_t r0 = (int64_t)r.it.tile * kNarrowRows;
     Rows<D, I8, 1> w;
-    w.run(r.a, r.q, r.it.h, r0, lo + wv, min(hi, most), kAttnWaves, j, g);
-    const float sum = groups_sum(w.sum[0]);
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) *reinterpret_cast<v4f*>(&n.o[wv][j][16 * i + 4 * g]) = w.o[0][i];
-    if (g == 0) {
-      n.m[wv][j] = w.mx[0];
-      n.l[wv][j] = sum;
-    }
+    w.run(r.a, r.q, (int)r.it.h, r0, r.from, min(r.to, steps_to(r, r0 + kNarrowRows, kTokTile)), 1, j, g);
+    store_share<D>(r, p, l, w.o[0], w.mx[0], w.sum[0], (uint32_t)r0 + j, g);
   }
-  __syncthreads();
-  // join the waves: 16 threads a row, D / 16 elements each
-  constexpr int E = D / 16;
-  typedef float vE __attribute__((ext_vector_type(E)));
-  const int row = threadIdx.x >> 4, q4 = (threadIdx.x & 15) * E;
-  const int64_t rr = r0 + row;
-  if (rr < r.q.nrows) {
-    float M = n.m[0][row];
-#pragma unroll
-    for (int x = 1; x < kAttnWaves; ++x) M = fmaxf(M, n.m[x][row]);
-    const float Mb = M == -INFINITY ? 0.0f : M;
-    float L = 0.0f;
-    vE v = 0.0f;
-#pragma unroll
-    for (int x = 0; x < kAttnWaves; ++x) {
-      const float wgt = __builtin_amdgcn_exp2f(n.m[x][row] - Mb);
-      L += wgt * n.l[x][row];
-      v += wgt * *reinterpret_cast<const vE*>(&n.o[x][row][q4]);
-    }
-    if (r.whole) {
-      v *= inverse_sum(L);
-      const int64_t key = r.key(rr), hq = r.a.c.H * r.a.R, token = r.q.row0 + (int)rr / r.a.R;
-      uint16_t* out = r.a.out + token * r.a.ldo + (key - token * hq) * D + q4;
-#pragma unroll
-      for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t*>(out + e) = f32_to_bf16_nan(v[e]) | f32_to_bf16_nan(v[e + 1]) << 16;
-      if (q4 == 0 && r.a.lse) r.a.lse[key] = log_sum(M, L);
-    } else {
-      const int64_t slot = r.slot(rr);
-      *reinterpret_cast<vE*>(r.a.part + slot * D + q4) = v;
-      if (q4 == 0) r.a.stat[slot] = float2{M, L};
-    }
-    if (q4 == 0 && r.first && !r.it.of_group) tell_row<D>(r, p, l, rr);
-  }
-  __syncthreads();  // the next item's waves write where this one's were read
 }
 
-template <int D, bool I8, int S>
-__global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_shared(ShareArgs s) {
+template <int D, bool I8, int RT, bool U>
+__device__ __forceinline__ void take_wide(const Share& r, const SharePlan& p, const ShareLds& l, uint8_t* smem, int wv, int lane) {
+  using W = Wide<D, I8, RT, U>;
+  constexpr uint32_t kSub = kTokTile / W::T;  // its steps to one of 64 tokens
+  const int j = lane & 15, g = lane >> 4;
+  const int64_t t0 = (int64_t)r.it.tile * wide_rows(D), r0 = t0 + wv * 16 * RT;
+  W w;
+  w.begin(r.a, r.q, (int)r.it.h, r0, j, g);
+  w.run(r.a, r.q, (int)r.it.h, r.from * kSub, min(r.to * kSub, steps_to(r, t0 + W::kRows, W::T)),
+        r0 < r.q.nrows, smem, wv, lane);
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) store_share<D>(r, p, l, w.o[rt], w.mx[rt], w.sum[rt], (uint32_t)r0 + 16 * rt + j, g);
+}
+
+template <int D, bool I8, bool U>
+__device__ __forceinline__ void wide_runs(const ShareArgs& s, const SharePlan& p, const ShareLds& l, uint32_t run, uint8_t* smem, int wv,
+                                          int lane) {
+  const uint32_t per = p.axis[kWide].per, end = min((run + 1) * per, p.axis[kWide].units);
+  for (uint32_t u = run * per; u < end;) {
+    Share r{s, s.a};
+    r.run = run;
+    const bool some = take_share<D, kWide>(r, p, l, u, end, lane);
+    u = r.it.i0 + r.it.k.units;
+    if (!some) continue;
+    if constexpr (D < 256) {
+      if ((uint32_t)r.q.nrows - r.it.tile * wide_rows(D) > 128u) {
+        take_wide<D, I8, 2, U>(r, p, l, smem, wv, lane);
+        continue;
+      }
+    }
+    take_wide<D, I8, 1, U>(r, p, l, smem, wv, lane);
+  }
+}
+
+template <int D, bool I8, bool U>
+__global__ __launch_bounds__(kThreads, 2) void k_kv_shared(ShareArgs s) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ ShareLds lds;
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const SharePlan plan = make_share_plan<D>(s, lds);
-  const int64_t end = min((blockIdx.x + 1) * plan.per, plan.units);
-  for (int64_t u = blockIdx.x * plan.per; u < end;) {
-    Share r{s, share_item<D>(s, lds, u)};
-    const ShareItem& it = r.it;
-    const uint32_t from = step_at(it, u - it.i0), to = step_at(it, end - it.i0);
-    u = it.i0 + it.units;
-    if (from >= to) continue;
-    r.a = s.a;
-    r.run = blockIdx.x;
-    r.first = from == 0;
-    r.whole = !it.of_group && it.shared == 0 && from == 0 && to == it.steps;
-    r.q.row0 = it.row0;
-    r.q.rows = it.rows;
-    r.q.nrows = (int64_t)it.rows * s.a.R;
-    r.q.len = uniform(lds.len[it.b]);
-    r.q.seen = (uint32_t)min((int64_t)max(r.q.len, 0), (int64_t)s.a.c.max_pages * s.a.c.P);
-    r.q.table = s.a.c.table + it.b * s.a.c.table_stride;
-    uint32_t base = it.shared;
-    if (it.of_group) {
-      r.q.seen = it.shared * kTokTile;
-      r.a.causal = 0;
-      base = 0;
+  // wide runs from the first workgroup on, narrow ones from the last, a wave of each in turn
+  const uint32_t wide = blockIdx.x, narrow = gridDim.x - 1 - blockIdx.x + (uint32_t)wv * gridDim.x;
+  const bool narrow_first = (blockIdx.x >> 3 & 1u) != 0;  // (workgroups go to the eight dies in turn)
+  for (int pass = 0; pass < 2; ++pass) {
+    if ((pass == 0) == narrow_first) {
+      if constexpr (D < 256) narrow_runs<D, I8>(s, plan, lds, narrow, lane);
+    } else {
+      wide_runs<D, I8, U>(s, plan, lds, wide, smem, wv, lane);
     }
-    if constexpr (D < 256) {
-      if (it.cost.tile == 16) {
-        take_narrow<D, I8>(r, plan, lds, base + from, base + to, *reinterpret_cast<NarrowLds<D, I8>*>(smem), wv, lane);
-        continue;
-      }
-      if (it.cost.tile == 128) {
-        take_wide<D, I8, 2, S>(r, plan, lds, base + from, base + to, smem, wv, lane);
-        continue;
-      }
-    }
-    take_wide<D, I8, 1, S>(r, plan, lds, base + from, base + to, smem, wv, lane);
   }
 }
 
-// One workgroup for each row with parts: D / 4 lanes of four columns take a part, 1024 / D parts go
-// at a time, and the sums are added in order.
+// The parts of a row, found by its descriptor
+struct JoinParts {
+  const ShareArgs& s;
+  int64_t key, keys;
+  uint4 d;
+  int own, all;  // parts of its own tokens; with the shared ones'
+  __device__ __forceinline__ JoinParts(const ShareArgs& s, int64_t key, int64_t keys, uint4 d)
+      : s(s), key(key), keys(keys), d(d), own((int)(d.x >> 16)), all((int)(d.x >> 16) + (int)(d.y >> 16)) {}
+  template <int D>
+  __device__ __forceinline__ int64_t slot(int p) const {
+    const bool mine = p < own;
+    const int k = mine ? p : p - own;
+    if (k == 0) return (mine ? 0 : keys) + key;
+    const uint32_t run = ((mine ? d.x : d.y) & 0xFFFFu) + k, at = mine ? d.z & 0xFFFFu : d.z >> 16;
+    const int64_t narrow = 2 * keys, wide = narrow + (int64_t)s.a.runs * narrow_slots(D);
+    return at & 0x8000u ? wide + (int64_t)run * wide_rows(D) + (at & 0x7FFFu) : narrow + (int64_t)run * kNarrowRows + at;
+  }
+};
+template <int D>
+__device__ __forceinline__ void store_joined(const ShareArgs& s, int64_t key, int64_t hq, int col, v4f acc, float M, float L) {
+  const float inv = inverse_sum(L);
+  const int64_t token = key / hq;
+  uint16_t* out = s.a.out + token * s.a.ldo + (key - token * hq) * D + col;
+  *reinterpret_cast<v2u*>(out) = v2u{f32_to_bf16_nan(acc[0] * inv) | f32_to_bf16_nan(acc[1] * inv) << 16,
+                                     f32_to_bf16_nan(acc[2] * inv) | f32_to_bf16_nan(acc[3] * inv) << 16};
+  if (col == 0 && s.a.lse) s.a.lse[key] = log_sum(M, L);
+}
+
+// A wave for each row: D / 4 lanes of four columns take a part, 256 / D parts at once, kAhead times in
+// flight; the running maximum and sum go with them.
 template <int D>
 __global__ __launch_bounds__(256) void k_kv_shared_join(ShareArgs s) {
-  constexpr int kLanes = D / 4, kAtOnce = 256 / kLanes, kAhead = 4;
-  __shared__ float wgt[2 * kMaxParts], red[8];
-  __shared__ v4f sums[kAtOnce][kLanes];
+  constexpr int kLanes = D / 4, kAtOnce = 64 / kLanes, kAhead = 4;
   const KvAttnArgs& a = s.a;
-  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+  const int lane = threadIdx.x & 63, mine = lane / kLanes, col = lane % kLanes * 4;
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t hq = (int64_t)a.c.H * a.R, keys = a.c.T * hq;
+  const int64_t end = seq_offset(a.c, a.c.B) * hq;
+  for (int64_t key = seq_offset(a.c, 0) * hq + (int64_t)blockIdx.x * 4 + wv; key < end; key += (int64_t)gridDim.x * 4) {
+    const JoinParts j(s, key, keys, s.desc[key]);
+    float M = -INFINITY, L = 0.0f;
+    v4f acc{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p0 = 0; p0 < j.all; p0 += kAtOnce * kAhead) {
+      v4f v[kAhead];
+      float2 st[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        const int64_t slot = j.template slot<D>(min(p0 + x * kAtOnce + mine, j.all - 1));
+        v[x] = *reinterpret_cast<const v4f*>(a.part + slot * D + col);
+        st[x] = a.stat[slot];
+        if (p0 + x * kAtOnce + mine >= j.all) st[x] = float2{-INFINITY, 0.0f};
+      }
+      float top = M;
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) top = fmaxf(top, st[x].x);
+      const float base = top == -INFINITY ? 0.0f : top, old = __builtin_amdgcn_exp2f(M - base);
+      L *= old;
+      acc *= old;
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        if (p0 + x * kAtOnce + mine >= j.all) continue;
+        const float w = __builtin_amdgcn_exp2f(st[x].x - base);
+        L += w * st[x].y;
+        acc += w * v[x];
+      }
+      M = top;
+    }
+    if (j.all == 0) continue;
+    // the lanes that took parts beside each other
+#pragma unroll
+    for (int o = kLanes; o < 64; o <<= 1) {
+      const float m = __shfl_xor(M, o, 64), top = fmaxf(M, m), base = top == -INFINITY ? 0.0f : top;
+      const float w0 = __builtin_amdgcn_exp2f(M - base), w1 = __builtin_amdgcn_exp2f(m - base);
+      L = w0 * L + w1 * __shfl_xor(L, o, 64);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = w0 * acc[e] + w1 * __shfl_xor(acc[e], o, 64);
+      M = top;
+    }
+    if (mine == 0) store_joined<D>(s, key, hq, col, acc, M, L);
+  }
+}
+
+// A workgroup for each row, where rows are few and may have hundreds of parts.
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_shared_join_wide(ShareArgs s) {
+  constexpr int kLanes = D / 4, kAtOnce = 256 / kLanes, kAhead = 4;
+  __shared__ float top_of[kAtOnce], sum_of[kAtOnce];
+  __shared__ v4f acc_of[kAtOnce][kLanes];
+  const KvAttnArgs& a = s.a;
+  const int t = threadIdx.x, mine = t / kLanes, col = t % kLanes * 4;
   const int64_t hq = (int64_t)a.c.H * a.R, keys = a.c.T * hq;
   const int64_t end = seq_offset(a.c, a.c.B) * hq;
   for (int64_t key = seq_offset(a.c, 0) * hq + blockIdx.x; key < end; key += gridDim.x) {
-    const uint4 d = s.desc[key];
-    const int parts0 = (int)(d.x >> 16), parts = parts0 + (int)(d.y >> 16);
-    if (parts == 0) continue;
-    auto slot = [&](int p) __attribute__((always_inline)) {
-      const bool own = p < parts0;
-      const int k = own ? p : p - parts0;
-      if (k == 0) return (own ? 0 : keys) + key;
-      const uint32_t run = ((own ? d.x : d.y) & 0xFFFFu) + k, row = own ? d.z & 0xFFFFu : d.z >> 16;
-      return 2 * keys + (int64_t)run * a.tile_rows + row;
-    };
-    // the first parts' sums are on their way while the weights are made
-    const int mine = t / kLanes, col = (t % kLanes) * 4;
-    v4f v[kAhead];
-    auto load = [&](int p0) __attribute__((always_inline)) {
-#pragma unroll
-      for (int x = 0; x < kAhead; ++x)
-        v[x] = *reinterpret_cast<const v4f*>(a.part + slot(min(p0 + x * kAtOnce + mine, parts - 1)) * D + col);
-    };
-    load(0);
-    float M = -INFINITY;
-    for (int p = t; p < parts; p += 256) {
-      const float m = a.stat[slot(p)].x;
-      wgt[p] = m;
-      M = fmaxf(M, m);
-    }
-    M = wave_max(M);
-    if (lane == 0) red[wv] = M;
-    __syncthreads();
-    M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float Mb = M == -INFINITY ? 0.0f : M;
-    float L = 0.0f;
-    for (int p = t; p < parts; p += 256) {
-      const float x = __builtin_amdgcn_exp2f(wgt[p] - Mb);
-      wgt[p] = x;
-      L += x * a.stat[slot(p)].y;
-    }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) L += __shfl_xor(L, o, 64);
-    if (lane == 0) red[4 + wv] = L;
-    __syncthreads();
-    L = (red[4] + red[5]) + (red[6] + red[7]);
+    const JoinParts j(s, key, keys, s.desc[key]);
+    if (j.all == 0) continue;
+    float M = -INFINITY, L = 0.0f;
     v4f acc{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int p0 = 0;;) {
+    for (int p0 = mine; p0 < j.all; p0 += kAtOnce * kAhead) {
+      v4f v[kAhead];
+      float2 st[kAhead];
 #pragma unroll
       for (int x = 0; x < kAhead; ++x) {
-        const int p = p0 + x * kAtOnce + mine;
-        if (p < parts) acc += wgt[p] * v[x];
+        const int64_t slot = j.template slot<D>(min(p0 + x * kAtOnce, j.all - 1));
+        v[x] = *reinterpret_cast<const v4f*>(a.part + slot * D + col);
+        st[x] = a.stat[slot];
+        if (p0 + x * kAtOnce >= j.all) st[x] = float2{-INFINITY, 0.0f};
       }
-      p0 += kAhead * kAtOnce;
-      if (p0 >= parts) break;
-      load(p0);
-    }
-    sums[mine][t % kLanes] = acc;
-    __syncthreads();
-    if (t < kLanes) {
+      float top = M;
 #pragma unroll
-      for (int w = 1; w < kAtOnce; ++w) acc += sums[w][t];
-      const float inv = inverse_sum(L);
-      const int64_t token = key / hq;
-      uint16_t* out = a.out + token * a.ldo + (key - token * hq) * D + col;
-      *reinterpret_cast<v2u*>(out) = v2u{f32_to_bf16_nan(acc[0] * inv) | f32_to_bf16_nan(acc[1] * inv) << 16,
-                                         f32_to_bf16_nan(acc[2] * inv) | f32_to_bf16_nan(acc[3] * inv) << 16};
-      if (t == 0 && a.lse) a.lse[key] = log_sum(M, L);
+      for (int x = 0; x < kAhead; ++x) top = fmaxf(top, st[x].x);
+      const float base = top == -INFINITY ? 0.0f : top, old = __builtin_amdgcn_exp2f(M - base);
+      L *= old;
+      acc *= old;
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        if (p0 + x * kAtOnce >= j.all) continue;
+        const float w = __builtin_amdgcn_exp2f(st[x].x - base);
+        L += w * st[x].y;
+        acc += w * v[x];
+      }
+      M = top;
     }
-    __syncthreads();  // the next row's weights and sums go where these were
+    if (col == 0) {
+      top_of[mine] = M;
+      sum_of[mine] = L;
+    }
+    acc_of[mine][t % kLanes] = acc;
+    __syncthreads();
+    if (mine == 0) {
+      float top = top_of[0];
+#pragma unroll
+      for (int w = 1; w < kAtOnce; ++w) top = fmaxf(top, top_of[w]);
+      const float base = top == -INFINITY ? 0.0f : top;
+      L = 0.0f;
+      acc = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < kAtOnce; ++w) {
+        const float x = __builtin_amdgcn_exp2f(top_of[w] - base);
+        L += x * sum_of[w];
+        acc += x * acc_of[w][t];
+      }
+      store_joined<D>(s, key, hq, col, acc, top, L);
+    }
+    __syncthreads();  // the next row's sums go where these were
   }
 }
 
 // How a call runs.  Sequences of many rows fill row tiles of their own, which read the shared
-// tokens once for each: attention as it is does that, with no parts to join.
+// tokens once for each: attention as it is does that, with no parts to join.  So do sizes whose
+// units are not counted in 32 bits.
 struct ShareShape {
   bool own;
-  int runs, tile, least;
+  int64_t keys, slots;  // output rows; rows of the workspace
 };
 ShareShape share_shape(const KvArgs& c, int R, int num_cu) {
   ShareShape s{};
-  s.own = c.T * R < 64 * (int64_t)c.B;
-  s.runs = (c.D == 256 ? 1 : 2) * num_cu;
-  s.tile = c.D == 256 ? 64 : 128;
-  s.least = 16;
+  const double tiles = 2.0 * ((double)c.T * R / kNarrowRows + c.B) * c.H, steps = (double)c.max_pages * c.P / kTokTile + 8;
+  s.own = c.T * R < 64 * (int64_t)c.B && tiles * steps < 2147483648.0;
+  s.keys = c.T * c.H * R;
+  s.slots = 2 * s.keys + (int64_t)num_cu * (narrow_slots(c.D) + wide_rows(c.D));
   return s;
 }
 
-template <int D, bool I8>
-hipError_t shared_of(ShareArgs s, hipStream_t st) {
-  constexpr int S = D == 256 ? 2 : 3;
-  constexpr int ring = SharedRows<D, I8, D == 256 ? 1 : 2, S>::kBytes;
-  constexpr int lds = ring > (int)sizeof(NarrowLds<D, I8>) || D == 256 ? ring : (int)sizeof(NarrowLds<D, I8>);
-  hipError_t e = set_lds_limit(reinterpret_cast<const void*>(k_kv_shared<D, I8, S>), lds);
+template <int D, bool I8, bool U>
+hipError_t shared_of(ShareArgs s, int64_t keys, hipStream_t st) {
+  constexpr int lds = Wide<D, I8, 1, U>::kBytes;
+  hipError_t e = set_lds_limit(reinterpret_cast<const void*>(k_kv_shared<D, I8, U>), lds);
   if (e != hipSuccess) return e;
   const ShareArgs all = s;
-  const int64_t keys = all.a.c.T * all.a.c.H * all.a.R;
+  const int cus = s.a.runs;
   for (int b = 0; b < all.a.c.B; b += kShareSeqs) {  // the launches of one stream use the workspace in turn
     s.a.c.B = min(all.a.c.B - b, kShareSeqs);
     s.a.c.offsets = all.a.c.offsets + b;
@@ -535,8 +592,12 @@ hipError_t shared_of(ShareArgs s, hipStream_t st) {
     s.a.c.table = all.a.c.table + b * all.a.c.table_stride;
     s.group = all.group + b;
     s.shared = all.shared + b;
-    hipLaunchKernelGGL((k_kv_shared<D, I8, S>), dim3((unsigned)s.a.runs), dim3(64 * kAttnWaves), lds, st, s);
-    hipLaunchKernelGGL(k_kv_shared_join<D>, dim3((unsigned)min(keys, (int64_t)1 << 16)), dim3(256), 0, st, s);
+    hipLaunchKernelGGL((k_kv_shared<D, I8, U>), dim3((unsigned)cus), dim3(kThreads), lds, st, s);
+    // a wave a row once that fills the chip (rows have few parts then)
+    if (keys >= 4 * cus)
+      hipLaunchKernelGGL(k_kv_shared_join<D>, dim3((unsigned)min((keys + 3) / 4, (int64_t)8 * cus)), dim3(256), 0, st, s);
+    else
+      hipLaunchKernelGGL(k_kv_shared_join_wide<D>, dim3((unsigned)keys), dim3(256), 0, st, s);
   }
   return hipGetLastError();
 }
@@ -546,8 +607,7 @@ hipError_t shared_of(ShareArgs s, hipStream_t st) {
 size_t kv_shared_workspace(const KvArgs& c, int R, int num_cu) {
   const ShareShape s = share_shape(c, R, num_cu);
   if (!s.own) return kv_attention_workspace(c, R, num_cu);
-  const size_t keys = (size_t)c.T * c.H * R;
-  return (2 * keys + (size_t)s.runs * s.tile) * (c.D * sizeof(float) + sizeof(float2)) + keys * sizeof(uint4);
+  return (size_t)s.slots * (c.D * sizeof(float) + sizeof(float2)) + (size_t)s.keys * sizeof(uint4);
 }
 
 int kv_shared_path(const KvArgs& c, int R, int num_cu) {
@@ -558,16 +618,15 @@ hipError_t launch_kv_attention_shared(KvAttnArgs a, bool i8, const int32_t* grou
                                       void* ws, hipStream_t st) {
   const ShareShape sh = share_shape(a.c, a.R, num_cu);
   if (!sh.own) return launch_kv_attention(a, i8, num_cu, ws, st);
-  const size_t keys = (size_t)a.c.T * a.c.H * a.R, slots = 2 * keys + (size_t)sh.runs * sh.tile;
-  a.runs = sh.runs;
-  a.least = sh.least;
-  a.tile_rows = sh.tile;
-  ShareArgs s{a, group, shared, static_cast<uint4*>(ws)};
-  s.a.part = reinterpret_cast<float*>(s.desc + keys);
-  s.a.stat = reinterpret_cast<float2*>(s.a.part + slots * a.c.D);
-  if (a.c.D == 64) return i8 ? shared_of<64, true>(s, st) : shared_of<64, false>(s, st);
-  if (a.c.D == 128) return i8 ? shared_of<128, true>(s, st) : shared_of<128, false>(s, st);
-  return i8 ? shared_of<256, true>(s, st) : shared_of<256, false>(s, st);
+  a.runs = num_cu;
+  ShareArgs s{a, group, shared, static_cast<uint4*>(ws), {8, 4}};
+  s.a.part = reinterpret_cast<float*>(s.desc + sh.keys);
+  s.a.stat = reinterpret_cast<float2*>(s.a.part + sh.slots * a.c.D);
+  auto go = [&](auto d, auto i, auto u) { return shared_of<decltype(d)::value, decltype(i)::value, decltype(u)::value>(s, sh.keys, st); };
+  auto codes = [&](auto d, auto u) { return i8 ? go(d, std::true_type{}, u) : go(d, std::false_type{}, u); };
+  auto pages = [&](auto d) { return a.c.P % kTokTile == 0 ? codes(d, std::true_type{}) : codes(d, std::false_type{}); };
+  if (a.c.D == 64) return pages(std::integral_constant<int, 64>{});
+  return a.c.D == 128 ? pages(std::integral_constant<int, 128>{}) : pages(std::integral_constant<int, 256>{});
 }
 
 }  // namespace wq

@@ -3,24 +3,24 @@ in whole numbers, and inputs for it."""
 
 import numpy as np
 
-WAVES, TILE, SEQS = 4, 64, 512
+TILE, SEQS, WAVES = 64, 512, 8
+NARROW, WIDE = 0, 1
+FIXED = (4, 6)  # units that an item counts besides its steps
 
 
-def cost_of(rows, D):
-    """(tile, units of a step, units of an item besides its steps)."""
+def kind_of(rows, D):
+    """(kind, rows of a tile)."""
     if D < 256 and rows <= 16:
-        return 16, 1, 8
-    if D == 256 or rows <= 64:
-        return 64, 2, 8
-    return 128, 3, 12
+        return NARROW, 16
+    return WIDE, 128 if D == 256 else 256
 
 
-def plan(ns, lens, group, shared, heads, R, D, P, width, num_runs, causal, least=16):
-    """Of one launch: {item: [(run, first step, last step + 1, slot kind, first row of its slots)]},
-    the joins as they are told, and the shared steps of each sequence."""
+def plan(ns, lens, group, shared, heads, R, D, P, width, workgroups, causal, least=(8, 4)):
+    """Of one launch: {item: [(run, first step, last step + 1, slot kind)]}, the joins as they are
+    told, the shared steps of each sequence and the one whose table it takes them from."""
     B = len(ns)
     row0 = np.concatenate(([0], np.cumsum(ns))).astype(int)
-    lead, first = [], {}
+    lead = []
     for b in range(B):
         begins = b > 0 and (group[b] < 0 or group[b] != group[b - 1])
         lead.append(b if begins or b == 0 else lead[-1])
@@ -35,76 +35,74 @@ def plan(ns, lens, group, shared, heads, R, D, P, width, num_runs, causal, least
             holder.setdefault(m, b)
     sh = [steps[lead[b]] if many.get(lead[b], 0) > 1 else 0 for b in range(B)]
 
-    def own_steps(b):
+    def items(rows, n):
+        """(kind, rows of a tile, tiles, steps, units of an item)."""
+        kind, tile = kind_of(rows, D)
+        return kind, tile, -(-rows // tile), n, n + FIXED[kind]
+
+    def own_items(b):
         seen = min(max(lens[b], 0), width * P)
-        return max(max(-(-seen // TILE), 1) - sh[b], 1)
+        return items(ns[b] * R, max(max(-(-seen // TILE), 1) - sh[b], 1))
 
-    def units(cost, n):
-        return cost[2] + cost[1] * n
+    def group_items(m):
+        return items((end[m] - row0[m]) * R, sh[m])
 
-    def tiles(cost, rows):
-        return -(-rows // cost[0])
-
-    pre = [0]
+    pre = [[0], [0]]
     for b in range(B):
-        rows = ns[b] * R
-        v = tiles(cost_of(rows, D), rows) * units(cost_of(rows, D), own_steps(b))
-        if lead[b] == b and sh[b] > 0:
-            rows = (end[b] - row0[b]) * R
-            v += tiles(cost_of(rows, D), rows) * units(cost_of(rows, D), sh[b])
-        pre.append(pre[-1] + v)
-    total = pre[-1] * heads
-    per = max(-(-total // num_runs), least)
+        v = [0, 0]
+        for k in [own_items(b)] + ([group_items(b)] if lead[b] == b and sh[b] > 0 else []):
+            v[k[0]] += k[2] * k[4]
+        for x in (0, 1):
+            pre[x].append(pre[x][-1] + v[x])
     taken, joins = {}, {}
+    runs = (workgroups * WAVES, workgroups)
+    per = [max(-(-pre[x][-1] * heads // runs[x]), least[x]) for x in (0, 1)]
 
-    def at(cost, i0, step):
-        return (i0 + cost[2] + step * cost[1]) // per
+    def told_of(k, i0, row):
+        first = i0 + FIXED[k[0]]
+        run = first // per[k[0]]
+        return run, (first + k[3] - 1) // per[k[0]] - run + 1, row % k[1]
 
-    for run in range(num_runs):
-        u, stop = run * per, min((run + 1) * per, total)
-        while u < stop:
-            b = max(b for b in range(B) if pre[b] * heads <= u)
-            rows, n, base = ns[b] * R, own_steps(b), pre[b] * heads
-            cost = cost_of(rows, D)
-            own = tiles(cost, rows) * units(cost, n) * heads
-            of_group = u - base >= own
-            if of_group:
-                base += own
-                rows, n = (end[b] - row0[b]) * R, sh[b]
-                cost = cost_of(rows, D)
-            each, t = units(cost, n), tiles(cost, rows)
-            item = (u - base) // each
-            i0, h, tile = base + item * each, item // t, item % t
-            assert h < heads and tile < t and i0 <= u < i0 + each
+    for axis in (NARROW, WIDE):
+        total = pre[axis][-1] * heads
+        for run in range(runs[axis]):
+            u, stop = run * per[axis], min((run + 1) * per[axis], total)
+            while u < stop:
+                b = max(b for b in range(B) if pre[axis][b] * heads <= u)
+                k, base = own_items(b), pre[axis][b] * heads
+                own = k[2] * k[4] * heads if k[0] == axis else 0
+                of_group = u - base >= own
+                if of_group:
+                    base += own
+                    k = group_items(b)
+                kind, size, tiles, n, each = k
+                assert kind == axis
+                item = (u - base) // each
+                i0, h, tile = base + item * each, item // tiles, item % tiles
+                assert h < heads and tile < tiles and i0 <= u < i0 + each
 
-            def step_at(x):
-                return 0 if x <= cost[2] else n if x >= each else -(-(x - cost[2]) // cost[1])
+                def step_at(x):
+                    return 0 if x <= FIXED[kind] else min(x - FIXED[kind], n)
 
-            lo, hi = step_at(u - i0), step_at(stop - i0)
-            assert i0 + each > u  # ends
-            u = i0 + each
-            if lo >= hi:
-                continue
-            whole = not of_group and sh[b] == 0 and lo == 0 and hi == n
-            kind = "out" if whole else "first" if lo == 0 else "run"
-            taken.setdefault((of_group, b, h, tile, n, cost[0], rows), []).append((run, lo, hi, kind))
-            if lo == 0 and not of_group:
-                for r in range(tile * cost[0], min((tile + 1) * cost[0], rows)):
-                    told = None
-                    if not whole:
-                        r0 = at(cost, i0, 0)
-                        told = (r0, at(cost, i0, n - 1) - r0 + 1, r - tile * cost[0])
-                        if sh[b] > 0:
-                            m = lead[b]
-                            all_rows, gr = (end[m] - row0[m]) * R, (row0[b] - row0[m]) * R + r
-                            k = cost_of(all_rows, D)
-                            lr = ns[m] * R
-                            kl = cost_of(lr, D)
-                            behind = tiles(kl, lr) * units(kl, own_steps(m))
-                            i1 = (pre[m] + behind) * heads + (h * tiles(k, all_rows) + gr // k[0]) * units(k, sh[m])
-                            r1 = at(k, i1, 0)
-                            told += (r1, at(k, i1, sh[m] - 1) - r1 + 1, gr % k[0], (True, m, h, gr // k[0]))
-                    joins[(b, h, r)] = told
+                lo, hi = step_at(u - i0), step_at(min(stop - i0, each))
+                u = i0 + each  # ends: beyond where it was
+                if lo >= hi:
+                    continue
+                whole = not of_group and sh[b] == 0 and lo == 0 and hi == n
+                rows = (end[b] - row0[b]) * R if of_group else ns[b] * R
+                taken.setdefault((of_group, b, h, tile), []).append((run, lo, hi, "out" if whole else "first" if lo == 0 else "run", kind, n))
+                if lo == 0 and not of_group:
+                    for r in range(tile * size, min((tile + 1) * size, rows)):
+                        told = None
+                        if not whole:
+                            told = told_of(k, i0, r)
+                            if sh[b] > 0:
+                                m = lead[b]
+                                gr, g, first = (row0[b] - row0[m]) * R + r, group_items(m), own_items(m)
+                                behind = first[2] * first[4] if first[0] == g[0] else 0
+                                i1 = (pre[g[0]][m] + behind) * heads + (h * g[2] + gr // g[1]) * g[4]
+                                told += told_of(g, i1, gr) + ((True, m, h, gr // g[1]),)
+                        joins[(b, h, r)] = told
     return taken, joins, sh, [holder.get(lead[b], b) for b in range(B)]
 
 
