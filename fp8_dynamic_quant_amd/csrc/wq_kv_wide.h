@@ -28,9 +28,9 @@ template <int D, bool I8, int RT, bool U>
 struct Wide {
   static constexpr int T = D == 256 ? 32 : 64;  // tokens of a step: two buffers of 32 KiB
   static constexpr int kGroups = T / 16, NT = T / 16, NK = D / 32, NV = D / 16, NM = T / 32;
-  static constexpr int kTile = T * D, kRaw = 2 * kTile, kBuf = 4 * kTile, kRing = 3;
-  static constexpr int kBufs = kRing * kRaw, kScales = kBufs + 2 * kBuf, kTable = kScales + 4 * 256, kBytes = kTable + 512;
-  static constexpr int kDma = D == 64 ? 2 : 3;  // of a wave and step
+  static constexpr int kTile = T * D, kRaw = 2 * kTile, kBuf = 2 * kTile, kRing = 3;
+  static constexpr int kKeys = kRing * kRaw, kValues = kKeys + 2 * kBuf, kScales = kValues + 2 * kBuf, kTable = kScales + 4 * 256, kBytes = kTable + 512;
+  static constexpr int kDma = D == 64 ? 1 : 2;  // of a wave and step, and the first wave's scale bytes
   static constexpr int kRows = 16 * RT * kWideWaves;
 
   v8bf qf[RT][NK];
@@ -153,33 +153,37 @@ struct Wide {
         if (D != 64 || wv >= 4)
           dma16_at(V + (uint64_t)held * page_step + (voff + slot_of(kGroups * (lo + b) + mine)), raw + kTile + vw * 1024);
       }
-      // scale bytes: word x the keys' of token group x, word 4 + x the values' (each wave writes the same)
-      dma1_at(scales + (uint64_t)held * H, lds0 + kScales + (b & 3) * 256);
+      // scale bytes: word x the keys' of token group x, word 4 + x the values'
+      if (wv == 0) dma1_at(scales + (uint64_t)held * H, lds0 + kScales + (b & 3) * 256);
     };
     const uint32_t* words = reinterpret_cast<const uint32_t*>(smem + kScales);
     // the thread's pieces of a step: read, and widened
     v4u kraw{0, 0, 0, 0}, vraw{0, 0, 0, 0};
-    float vscale = 1.0f;
+    uint32_t vword = 0;
     auto fetch = [&](uint32_t b, uint32_t none, int slot) __attribute__((always_inline)) {
       const uint8_t* raw = smem + slot * kRaw;
       if (D != 64 || t < 256) kraw = *reinterpret_cast<const v4u*>(raw + 16 * t);
       if (D != 64 || t >= 256) {
         const int u = D == 64 ? t - 256 : t, x = u % kGroups;
         vraw = *reinterpret_cast<const v4u*>(raw + kTile + 16 * u);
-        const uint32_t byte = words[(b & 3) * 64 + 4 + x], step = lo + b;
+        vword = words[(b & 3) * 64 + 4 + x];
+        const uint32_t step = lo + b;
         // codes behind the sequence's end and of pages that are none may be anything, E4M3's NaN too
-        if (none != 0 || (step + 1) * T > s.seen) vraw = keep_bytes(vraw, there_slots(s, !(none >> x & 1u), step * T + 16 * x));
-        vscale = byte == 255u ? 1.0f : scale_of(byte);
+        if (__builtin_expect(none != 0 || (step + 1) * T > s.seen, 0)) {
+          uint32_t at = step * T + 16 * x;
+          asm volatile("" : "+v"(at));  // (all of it in the branch)
+          vraw = keep_bytes(vraw, there_slots(s, !(none >> x & 1u), at));
+        }
       }
     };
     auto widen_keys = [&](uint32_t b) __attribute__((always_inline)) {
       const int tok = t / kPer;
-      if (D != 64 || t < 256) widen16(kraw, 1.0f, smem + kBufs + (b & 1) * kBuf + tok * 2 * D, 2 * (t % kPer), 1, key_place(tok));
+      if (D != 64 || t < 256) widen16(kraw, 1.0f, smem + kKeys + (b & 1) * kBuf + tok * 2 * D, 2 * (t % kPer), 1, key_place(tok));
     };
     auto widen_values = [&](uint32_t b) __attribute__((always_inline)) {
       const int u = D == 64 ? t - 256 : t, row = u / kGroups, x = u % kGroups;
       if (D != 64 || t >= 256)
-        widen16(vraw, vscale, smem + kBufs + (b & 1) * kBuf + 2 * kTile + row * 2 * T, T == 64 ? x : 2 * x, T == 64 ? 4 : 1, value_place(row));
+        widen16(vraw, vword == 255u ? 1.0f : scale_of(vword), smem + kValues + (b & 1) * kBuf + row * 2 * T, T == 64 ? x : 2 * x, T == 64 ? 4 : 1, value_place(row));
     };
     // ---- steps 0, 1, 2 on their way
     const int p0 = number(0), p1 = number(1), p2 = number(2);
@@ -192,7 +196,7 @@ struct Wide {
     auto told = [&](uint32_t step) __attribute__((always_inline)) {
       return *reinterpret_cast<const int*>(smem + kTable + ((kEach * step + (U ? 0 : mine)) & 127) * 4);
     };
-    send_entries(0);
+    if (wv == 0) send_entries(0);
     issue(0, p0, 0);
     if (n > 1) issue(1, p1, 1);
     if (n > 2) issue(2, p2, 2);
@@ -211,17 +215,45 @@ struct Wide {
     widen_keys(0);
     widen_values(0);
     const int kj = D == 64 ? j >> 1 : j;
-    const uint8_t* kread = smem + kBufs + ((T / 4) * (j >> 2) + (j & 3)) * 2 * D;
+    const uint8_t* kread = smem + kKeys + ((T / 4) * (j >> 2) + (j & 3)) * 2 * D;
     const uint32_t kpiece = (uint32_t)((g ^ kj) << 4);
-    const uint8_t* vread = smem + kBufs + 2 * kTile + j * 2 * T;
+    const uint8_t* vread = smem + kValues + j * 2 * T;
     const uint32_t vpiece = (uint32_t)((g ^ value_place(j)) << 4);
     const int x = T == 64 ? g : g >> 1;  // the lane's token group
-    int slot = 0, next_page = told(3);  // (read a step ahead)
-    for (uint32_t b = 0; b < n; ++b) {
-      if (b + 2 < n) wait_vm<kDma>();
-      else wait_vm<0>();
-      // the next step has landed for all; this one is widened; the one before has been read by all
+    int slot = 0, next_page = checked(3, U ? uniform(told(3)) : told(3));
+    // the next step has landed for all; this one is widened; the one before has been read by all
+    auto meet = [&](uint32_t b) __attribute__((always_inline)) {
+      if (b + 2 >= n) wait_vm<0>();
+      else if (wv == 0) wait_vm<kDma + 1>();
+      else wait_vm<kDma>();
       lds_barrier();
+    };
+    // step b + 3 on its way, in the place of step b, which has been widened
+    auto send = [&](uint32_t b) __attribute__((always_inline)) {
+      if (b + 3 < n) {
+        issue(b + 3, next_page, slot);
+        none |= none_of(next_page) << 12;
+        if (wv == 0 && (b * kEach) % 64 == 0 && b * kEach + 64 < kEach * n) send_entries(b * kEach / 64 + 1);
+      }
+      slot = slot == 2 ? 0 : slot + 1;
+      none >>= 4;
+    };
+    // step b + 1 is widened by all (behind the last step, what the ring happens to hold: nothing reads it)
+    if (!active) {
+      for (uint32_t b = 0; b < n; ++b) {
+        meet(b);
+        send(b);
+        fetch(b + 1, none & 15u, slot);
+        const int page = told(b + 4);
+        widen_keys(b + 1);
+        widen_values(b + 1);
+        next_page = checked(b + 4, U ? uniform(page) : page);
+      }
+      lds_barrier();  // the ring and the buffers may be filled again
+      return;
+    }
+    for (uint32_t b = 0; b < n; ++b) {
+      meet(b);
       const uint8_t* kp = kread + (b & 1) * kBuf;
       const uint8_t* vp = vread + (b & 1) * kBuf;
       auto key = [&](int i) __attribute__((always_inline)) {
@@ -234,26 +266,9 @@ struct Wide {
       constexpr int kAhead = 4;
       v8bf frag[kAhead];
       const uint32_t kbyte = words[(b & 3) * 64 + x], vbyte = words[(b & 3) * 64 + 4 + x];
-      if (active) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) frag[i] = key(i);
-      }
-      if (b + 3 < n) {
-        const int page = checked(b + 3, U ? uniform(next_page) : next_page);
-        next_page = told(b + 4);
-        issue(b + 3, page, slot);
-        none |= none_of(page) << 12;
-        if ((b * kEach) % 64 == 0 && b * kEach + 64 < kEach * n) send_entries(b * kEach / 64 + 1);
-      }
-      slot = slot == 2 ? 0 : slot + 1;
+      for (int i = 0; i < kAhead; ++i) frag[i] = key(i);
       const uint32_t gone = none & 15u;
-      none >>= 4;
-      const bool more = b + 1 < n;
-      if (more) fetch(b + 1, none & 15u, slot);
-      if (!active) {
-        if (more) widen_keys(b + 1), widen_values(b + 1);
-        continue;
-      }
       // The step in sections: the scores of 16 tokens beside the weights of the 16 before.  The weights are
       // relative to a base that follows the scores only where one passes it by 8 (weights up to 2^8 are as
       // exact as those up to 1, and sums of them stay far inside 32 bits), and to a whole number, so that
@@ -388,13 +403,23 @@ struct Wide {
       };
       constexpr int kAll = NM * NV;
       static_assert(NT * NK % kAhead == 0, "scores end with the first values in frag");
+      send(b);
+      fetch(b + 1, none & 15u, slot);
+      const int page = told(b + 4);
+      __builtin_amdgcn_sched_barrier(0);
       out(0, kAll / 4);
-      __builtin_amdgcn_sched_barrier(0);
-      if (more) widen_keys(b + 1);
+      widen_keys(b + 1);
       out(kAll / 4, kAll / 2);
-      __builtin_amdgcn_sched_barrier(0);
-      if (more) widen_values(b + 1);
+      widen_values(b + 1);
       out(kAll / 2, kAll);
+#pragma unroll
+      for (int i = 0; i < kAll; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // a read,
+        __builtin_amdgcn_sched_group_barrier(0x008, RT, 0);  // matrix instructions,
+        __builtin_amdgcn_sched_group_barrier(0x002, I8 ? 6 : 3, 0);
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+      }
+      next_page = checked(b + 4, U ? uniform(page) : page);
     }
     lds_barrier();  // the ring and the buffers may be filled again
   }
