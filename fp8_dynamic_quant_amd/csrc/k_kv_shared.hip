@@ -10,9 +10,8 @@
 // Of up to 16 rows they are narrow: a wave takes one alone, straight from memory.  Of more they are
 // wide: a workgroup of eight waves takes one (Wide).  The items of either kind lie on an axis of
 // their own, in units of a step of 64 tokens and a constant for an item's beginning and end, which
-// is cut into equal runs: of narrow ones one a wave, of wide ones one a workgroup.  Reading bounds
-// the narrow, arithmetic the wide, so half of the workgroups begin with one kind and half with the
-// other.  A row's parts, of both items where it shares and of as many runs as cut them, go to the
+// is cut into equal runs: of narrow ones one a wave, of wide ones one a workgroup.  Workgroups take
+// one kind or the other, as many of either as their units ask for.  A row's parts, of both items where it shares and of as many runs as cut them, go to the
 // workspace in f32 and are joined by a second kernel in the order of the axes: results do not depend
 // on timing.
 #include "wq_kernels.h"
@@ -37,8 +36,10 @@ struct ShareArgs {
   const int32_t* group;    // [B]
   const int32_t* shared;   // [B]
   uint4* desc;             // [keys], keys = T * Hq
-  uint32_t least[2];       // units of a run, by kind
 };
+// units of a run, by kind: fewer leave more parts to join.  (8 sequences of 50 own tokens behind 1000:
+// 15.2 us, with {8, 4} 18.4; 64 of 500 behind 8192, whose runs are longer than either: 41.)
+constexpr uint32_t kLeast[2] = {5, 2};
 // units that an item counts besides its steps
 __device__ __forceinline__ uint32_t fixed_units(int kind) { return kind == kNarrow ? 4u : 6u; }
 
@@ -85,6 +86,10 @@ __device__ __forceinline__ Kind kind_of(uint32_t rows, uint32_t steps) {
 
 struct Axis {
   uint32_t units, per, runs;
+  static __device__ __forceinline__ Axis cut(uint32_t units, uint32_t runs, uint32_t least) {
+    const uint32_t per = max((units + runs - 1) / runs, least);
+    return Axis{units, per, (units + per - 1) / per};
+  }
 };
 struct SharePlan {
   Axis axis[2];
@@ -160,6 +165,7 @@ __device__ __forceinline__ SharePlan make_share_plan(const ShareArgs& s, ShareLd
   }
   __syncthreads();
   SharePlan p;
+  uint32_t total[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     uint32_t base = 0, sum = 0;
@@ -170,12 +176,17 @@ __device__ __forceinline__ SharePlan make_share_plan(const ShareArgs& s, ShareLd
     }
     if (in) l.pre[k][b + 1] = base + v[k];
     if (b == 0) l.pre[k][0] = 0;
-    Axis& x = p.axis[k];
-    const uint32_t runs = (uint32_t)gridDim.x * (k == kNarrow ? kWideWaves : 1);
-    x.units = (uint32_t)uniform((int)(sum * (uint32_t)c.H));
-    x.per = max((x.units + runs - 1) / runs, s.least[k]);
-    x.runs = (x.units + x.per - 1) / x.per;
+    total[k] = (uint32_t)uniform((int)(sum * (uint32_t)c.H));
   }
+  // A narrow unit of one wave takes about 5 / 4 of the time of a wide one of eight.  (Weighed by 1/2, 1,
+  // 5/4, 2: 402, 257, 234, 238 us at 256 sequences of 1500 own tokens behind 32768, 32 heads of 128.
+  // Every workgroup taking both kinds, half of them one first and half the other: 238 us there, but
+  // 53 us, not 41, at 64 sequences of 500 own tokens behind 8192, where each waits for its slowest wave.)
+  const uint32_t all = gridDim.x;
+  const uint64_t narrow = ((uint64_t)total[kNarrow] * 5 + 4 * kWideWaves - 1) / (4 * kWideWaves);
+  const uint32_t share = (uint32_t)((uint64_t)all * total[kWide] / (total[kWide] + narrow + 1));
+  p.axis[kWide] = Axis::cut(total[kWide], total[kNarrow] == 0 ? all : min(max(share, 1u), all - 1), kLeast[kWide]);
+  p.axis[kNarrow] = Axis::cut(total[kNarrow], (all - min(p.axis[kWide].runs, all - 1)) * kWideWaves, kLeast[kNarrow]);
   __syncthreads();
   return p;
 }
@@ -403,15 +414,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_shared(ShareArgs s) {
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const SharePlan plan = make_share_plan<D>(s, lds);
-  // wide runs from the first workgroup on, narrow ones from the last, a wave of each in turn
-  const uint32_t wide = blockIdx.x, narrow = gridDim.x - 1 - blockIdx.x + (uint32_t)wv * gridDim.x;
-  const bool narrow_first = (blockIdx.x >> 3 & 1u) != 0;  // (workgroups go to the eight dies in turn)
-  for (int pass = 0; pass < 2; ++pass) {
-    if ((pass == 0) == narrow_first) {
-      if constexpr (D < 256) narrow_runs<D, I8>(s, plan, lds, narrow, lane);
-    } else {
-      wide_runs<D, I8, U>(s, plan, lds, wide, smem, wv, lane);
-    }
+  const uint32_t wide = plan.axis[kWide].runs;  // workgroups that take wide runs; the waves of the others narrow ones
+  if (blockIdx.x < wide) {
+    wide_runs<D, I8, U>(s, plan, lds, blockIdx.x, smem, wv, lane);
+  } else if constexpr (D < 256) {
+    narrow_runs<D, I8>(s, plan, lds, blockIdx.x - wide + (uint32_t)wv * (gridDim.x - wide), lane);
   }
 }
 
@@ -574,7 +581,7 @@ ShareShape share_shape(const KvArgs& c, int R, int num_cu) {
   const double tiles = 2.0 * ((double)c.T * R / kNarrowRows + c.B) * c.H, steps = (double)c.max_pages * c.P / kTokTile + 8;
   s.own = c.T * R < 64 * (int64_t)c.B && tiles * steps < 2147483648.0;
   s.keys = c.T * c.H * R;
-  s.slots = 2 * s.keys + (int64_t)num_cu * (narrow_slots(c.D) + wide_rows(c.D));
+  s.slots = 2 * s.keys + (int64_t)max(num_cu, 2) * (narrow_slots(c.D) + wide_rows(c.D));
   return s;
 }
 
@@ -618,8 +625,8 @@ hipError_t launch_kv_attention_shared(KvAttnArgs a, bool i8, const int32_t* grou
                                       void* ws, hipStream_t st) {
   const ShareShape sh = share_shape(a.c, a.R, num_cu);
   if (!sh.own) return launch_kv_attention(a, i8, num_cu, ws, st);
-  a.runs = num_cu;
-  ShareArgs s{a, group, shared, static_cast<uint4*>(ws), {8, 4}};
+  a.runs = max(num_cu, 2);  // workgroups: some for either kind
+  ShareArgs s{a, group, shared, static_cast<uint4*>(ws)};
   s.a.part = reinterpret_cast<float*>(s.desc + sh.keys);
   s.a.stat = reinterpret_cast<float2*>(s.a.part + sh.slots * a.c.D);
   auto go = [&](auto d, auto i, auto u) { return shared_of<decltype(d)::value, decltype(i)::value, decltype(u)::value>(s, sh.keys, st); };

@@ -15,7 +15,7 @@ def kind_of(rows, D):
     return WIDE, 128 if D == 256 else 256
 
 
-def plan(ns, lens, group, shared, heads, R, D, P, width, workgroups, causal, least=(8, 4)):
+def plan(ns, lens, group, shared, heads, R, D, P, width, workgroups, causal, least=(5, 2)):
     """Of one launch: {item: [(run, first step, last step + 1, slot kind)]}, the joins as they are
     told, the shared steps of each sequence and the one whose table it takes them from."""
     B = len(ns)
@@ -55,8 +55,16 @@ def plan(ns, lens, group, shared, heads, R, D, P, width, workgroups, causal, lea
         for x in (0, 1):
             pre[x].append(pre[x][-1] + v[x])
     taken, joins = {}, {}
-    runs = (workgroups * WAVES, workgroups)
-    per = [max(-(-pre[x][-1] * heads // runs[x]), least[x]) for x in (0, 1)]
+    assert workgroups > 1  # some for either kind
+    units = [pre[x][-1] * heads for x in (0, 1)]
+    share = workgroups * units[WIDE] // (units[WIDE] + -(-units[NARROW] * 5 // (4 * WAVES)) + 1)
+    wide = workgroups if units[NARROW] == 0 else min(max(share, 1), workgroups - 1)
+    per_wide = max(-(-units[WIDE] // wide), least[WIDE])
+    wide = -(-units[WIDE] // per_wide)  # workgroups that take wide runs; the others' waves take narrow ones
+    narrow = (workgroups - min(wide, workgroups - 1)) * WAVES
+    per = (max(-(-units[NARROW] // narrow), least[NARROW]), per_wide)
+    runs = (narrow, wide)
+    assert units[NARROW] == 0 or wide < workgroups
 
     def told_of(k, i0, row):
         first = i0 + FIXED[k[0]]

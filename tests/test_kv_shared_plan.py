@@ -14,7 +14,7 @@ def test_runs_cover_the_work(seed):
     ns, lens, group, shared, P, width = sp.batch(g)
     D, heads, R = int(g.choice([64, 256])), int(g.integers(1, 6)), int(g.choice([1, 4, 5, 16]))
     causal = bool(g.random() < 0.7)
-    runs = int(g.choice([1, 2, 7, 64, 256]))
+    runs = int(g.choice([2, 3, 7, 64, 256]))
     taken, joins, sh, holder = sp.plan(ns, lens, group, shared, heads, R, D, P, width, runs, causal)
     row0 = np.concatenate(([0], np.cumsum(ns)))
     slots = set()
