@@ -569,9 +569,11 @@ __global__ __launch_bounds__(256) void k_kv_shared_join_wide(ShareArgs s) {
   }
 }
 
-// How a call runs.  Sequences of many rows fill row tiles of their own, which read the shared
-// tokens once for each: attention as it is does that, with no parts to join.  So do sizes whose
-// units are not counted in 32 bits.
+// How a call runs.  Sequences of many rows fill row tiles of their own, which read the shared tokens
+// once for each: attention as it is does that, with no parts to join.  (32 heads of 128 in groups of
+// four, E4M3, that and this: 16 sequences of 128 rows behind 4096 shared tokens 217 and 150 us, of
+// 256 385 and 270; 4 of 512 behind 512, where a row's parts weigh as much as its tokens, 61 and 77.)
+// So do sizes whose units are not counted in 32 bits.
 struct ShareShape {
   bool own;
   int64_t keys, slots;  // output rows; rows of the workspace
@@ -579,7 +581,7 @@ struct ShareShape {
 ShareShape share_shape(const KvArgs& c, int R, int num_cu) {
   ShareShape s{};
   const double tiles = 2.0 * ((double)c.T * R / kNarrowRows + c.B) * c.H, steps = (double)c.max_pages * c.P / kTokTile + 8;
-  s.own = c.T * R < 64 * (int64_t)c.B && tiles * steps < 2147483648.0;
+  s.own = c.T * R < 2048 * (int64_t)c.B && tiles * steps < 2147483648.0;
   s.keys = c.T * c.H * R;
   s.slots = 2 * s.keys + (int64_t)max(num_cu, 2) * (narrow_slots(c.D) + wide_rows(c.D));
   return s;

@@ -480,7 +480,7 @@ int64_t wq_kv_attention_shared_workspace_bytes(const wq_ctx* ctx, const wq_kv_ca
                                                int64_t q_heads, int64_t B);
 
 /* As wq_kv_attention_path, of wq_kv_attention_shared: 16 where the shared tokens are taken once;
- * sequences of 64 rows and more on average (rows times q_heads / heads) fill row tiles of their own
+ * sequences of 2048 rows and more on average (rows times q_heads / heads) fill row tiles of their own
  * and take wq_kv_attention's kernels, numbered as there. */
 int wq_kv_attention_shared_path(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T, int64_t q_heads, int64_t B);
 

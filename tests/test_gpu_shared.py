@@ -154,6 +154,44 @@ def test_many_rows_to_a_sequence_take_their_own_tiles(D):
     _check(c, table, q, **f, causal=True, path=None)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("P", [48, 64])
+@pytest.mark.parametrize("D, i8", [(64, True), (128, False), (128, True), (256, False)])
+def test_row_tiles(D, i8, P, causal):
+    # own tiles of 256 rows and a rest of 24, 104 and 132 (128, and rests of 24, 104 and 4, with heads of
+    # 256); of the group 772 rows
+    f = dict(ns=[70, 90, 33], lens=[300, 290, 250], group=[0, 0, 0], shared=[192] * 3)
+    c, table, q = _inputs(4, D, i8, **f, P=P, width=7, H=2, R=4)
+    _check(c, table, q, **f, causal=causal)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompts_of_many_rows_are_attention_as_it_is(D):
+    f = dict(ns=[520, 540], lens=[590, 600], group=[0, 0], shared=[48] * 2)
+    c, table, q = _inputs(5, D, False, **f, P=16, width=38, H=1, R=4)
+    cd, args, _, _ = _check(c, table, q, **f, causal=True, path=None)
+    paths = [of(cd, *q.shape[:2], args[3]) for of in (wq.wq_kv_attention_shared_path, wq.wq_kv_attention_path)]
+    assert paths[0] == paths[1] != 16
+
+
+@pytest.mark.parametrize("falling", [False, True])
+@pytest.mark.parametrize("ns", [[1] * 8, [20] * 8])
+@pytest.mark.parametrize("D, i8", [(64, False), (128, False), (128, True), (256, True)])
+def test_scores_that_climb_and_fall(D, i8, ns, falling):
+    # the keys' scales double every second page, up to scores of 150 (of heads of 256, 113) or down from them: what weights are
+    # relative to has to follow, by steps of any size, and rows whose scores are all below zero take part
+    f = dict(ns=ns, lens=[900 + 3 * b for b in range(8)], group=[0] * 8, shared=[768] * 8)
+    c, table, q = _inputs(6, D, i8, **f, P=32, width=30, H=1, R=4)
+    order = np.arange(30)[::-1] if falling else np.arange(30)
+    least = int(c[2].max())
+    for b in range(8):
+        c[2][table[b]] = (least - 15 + order // 2)[:, None]
+    off = np.concatenate(([0], np.cumsum(ns))).astype(np.int64)
+    smag = kf.attention(c, q, off, f["lens"], table, 1.0, True)[3]
+    most = min(150.0, 0.9 * 2.0**15 / (D + 4))  # (_limits takes no larger ones)
+    _check(c, table, q, **f, causal=True, scale=most / float(smag.max()))
+
+
 @pytest.mark.parametrize("i8", [False, True])
 @pytest.mark.parametrize("D", [64, 256])
 def test_pages_marked_nan_and_rows_that_hold_one(D, i8):

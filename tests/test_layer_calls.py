@@ -103,7 +103,7 @@ def test_attention_workspace_and_path(ctx):
     # two f32 rows and their two numbers for every output row, and a tile for every workgroup
     assert need(64, 8, 64) >= 2 * 64 * 8 * 64 * 4
     assert _attend(ctx, one, T=64, B=64, n=need(64, 8, 64) - 1) == WORKSPACE
-    assert path(64, 8, 64) == 16 and path(64, 32, 16) == L.wq_kv_attention_path(ctx, ctypes.byref(one), 64, 32, 16) != 16
+    assert path(64, 8, 64) == 16 and path(4096, 32, 16) == L.wq_kv_attention_path(ctx, ctypes.byref(one), 4096, 32, 16) != 16
 
 
 def test_attention_refuses_work_beyond_52_bits(ctx):
