@@ -39,8 +39,14 @@ struct Turned {
   v4u x0, x1;
   v4f c[2], s[2];
   __device__ __forceinline__ void load(const uint16_t* x, const Unit& u, int i, const TurnArgs& r, int64_t pos) {
+    pieces(x, u);
+    angles(u, i, r, pos);
+  }
+  __device__ __forceinline__ void pieces(const uint16_t* x, const Unit& u) {
     x0 = *reinterpret_cast<const v4u*>(x + u.at0);
     x1 = *reinterpret_cast<const v4u*>(x + u.at1);
+  }
+  __device__ __forceinline__ void angles(const Unit& u, int i, const TurnArgs& r, int64_t pos) {
     const float nan = __uint_as_float(0x7FC00000u);
     c[0] = c[1] = v4f{nan, nan, nan, nan};
     s[0] = s[1] = c[0];
@@ -162,36 +168,75 @@ __device__ __forceinline__ void append_turned(const KvArgs& c, const Found& s, i
   }
 }
 
-// The queries of n rows from row0 on, heads h R .. h R + R - 1; pos[r] their positions, none: a row
-// of no sequence, left as it is.  A thread reads both pieces of a unit before it writes them, so
+// The queries of heads h R .. h R + R - 1 of rows from row0 on; pos[r] their positions, none: a row of
+// no sequence, left as it is.  A thread reads both pieces of a unit before it writes them, so
 // that the rows may be turned in place.
 constexpr int kNoRow = INT32_MIN;
 template <bool PAIRS>
-__device__ __forceinline__ void turn_queries(const KvArgs& c, int64_t row0, int n, int h, const TurnArgs& tr, const int* pos) {
-  const int per = c.D / 16, all = tr.R * per;
-  for (int i = threadIdx.x; i < n * all; i += 256) {
-    const int r = i / all, k = i - r * all, head = k / per, at = k - head * per;
-    if (pos[r] == kNoRow) continue;
+__device__ __forceinline__ void store_turned(const Turned<PAIRS>& w, const Unit& u, uint16_t* to) {
+  float y0[8], y1[8];
+  w.values(u, y0, y1);
+  auto pack = [](const float (&y)[8]) __attribute__((always_inline)) {
+    v4u o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = f32_to_bf16_nan(y[2 * e]) | f32_to_bf16_nan(y[2 * e + 1]) << 16;
+    return o;
+  };
+  *reinterpret_cast<v4u*>(to + u.at0) = pack(y0);
+  *reinterpret_cast<v4u*>(to + u.at1) = pack(y1);
+}
+// of one row, a thread a unit of a head
+template <bool PAIRS>
+__device__ __forceinline__ void turn_row(const KvArgs& c, int64_t row, int h, const TurnArgs& tr, int64_t pos) {
+  const int per = c.D / 16;
+  for (int i = threadIdx.x; i < tr.R * per; i += 256) {
+    const int head = i / per, at = i - head * per;
     const int64_t col = ((int64_t)h * tr.R + head) * c.D;
     const Unit u = unit_of<PAIRS>(at, tr.rot);
     Turned<PAIRS> w;
-    w.load(tr.q + (row0 + r) * tr.ldq + col, u, at, tr, pos[r]);
-    float y0[8], y1[8];
-    w.values(u, y0, y1);
+    w.load(tr.q + row * tr.ldq + col, u, at, tr, pos);
+    store_turned(w, u, tr.q_out + row * tr.ldo + col);
+  }
+}
+// of many, a thread a unit of kHeads heads, whose angles are the same
+constexpr int kHeads = 4;
+template <bool PAIRS>
+__device__ __forceinline__ void turn_rows(const KvArgs& c, int64_t row0, int n, int h, const TurnArgs& tr, const int* pos) {
+  const int per = c.D / 16, all = (tr.R + kHeads - 1) / kHeads * per;
+  for (int i = threadIdx.x; i < n * all; i += 256) {
+    const int r = i / all, k = i - r * all, h0 = k / per, at = k - h0 * per, heads = min(tr.R - kHeads * h0, kHeads);
+    if (pos[r] == kNoRow) continue;
+    const int64_t col = ((int64_t)h * tr.R + kHeads * h0) * c.D;
+    const uint16_t* from = tr.q + (row0 + r) * tr.ldq + col;
     uint16_t* to = tr.q_out + (row0 + r) * tr.ldo + col;
-    auto pack = [](const float (&y)[8]) __attribute__((always_inline)) {
-      v4u o;
+    const Unit u = unit_of<PAIRS>(at, tr.rot);
+    Turned<PAIRS> w[kHeads];
+    w[0].angles(u, at, tr, pos[r]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = f32_to_bf16_nan(y[2 * e]) | f32_to_bf16_nan(y[2 * e + 1]) << 16;
-      return o;
-    };
-    *reinterpret_cast<v4u*>(to + u.at0) = pack(y0);
-    *reinterpret_cast<v4u*>(to + u.at1) = pack(y1);
+    for (int e = 0; e < kHeads; ++e) w[e].pieces(from + min(e, heads - 1) * c.D, u);
+#pragma unroll
+    for (int e = 0; e < kHeads; ++e) {
+      if (e >= heads) break;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        w[e].c[x] = w[0].c[x];
+        w[e].s[x] = w[0].s[x];
+      }
+      store_turned(w[e], u, to + e * c.D);
+    }
   }
 }
 
+// Rows of a workgroup: one unit of kHeads heads for each of its threads.  (A page's rows for each, units
+// one after another: 8000 rows of 16 heads of 256 on one head of keys 137 us, so 30.)
+__host__ __device__ __forceinline__ int query_rows(const KvArgs& c, int R) {
+  const int all = (R + kHeads - 1) / kHeads * (c.D / 16);
+  return all >= 256 ? 1 : min(256 / all, c.P);
+}
+
 // Workgroups (slot, head, 0 and 1): keys and values of a sequence's rows in one page, as in
-// append.  (slot, head, 2): the head's queries of one row where slots are rows, of P rows otherwise.
+// append.  (slot, head, 2 and on): the head's queries of one row where slots are rows, otherwise of
+// P rows, some of them each (query_rows: so that a head has workgroups enough, whatever P and R are).
 template <bool I8, bool PAIRS>
 __global__ __launch_bounds__(256) void k_kv_append_rotated(KvArgs c, int64_t first_slot, int div, int per_seq, const uint16_t* k_new,
                                                            int64_t ldk, const uint16_t* v_new, int64_t ldv, TurnArgs tr) {
@@ -209,15 +254,14 @@ __global__ __launch_bounds__(256) void k_kv_append_rotated(KvArgs c, int64_t fir
       append_rows<I8>(c, s, h, 1, v_new, ldv, red);
     } else {
       if (s.rows <= 0 || s.j >= s.rows) return;
-      if (threadIdx.x == 0) pos[0] = (int)max(s.len - s.rows + s.j, (int64_t)-1);
-      __syncthreads();
-      turn_queries<PAIRS>(c, slot, 1, h, tr, pos);
+      turn_row<PAIRS>(c, slot, h, tr, s.len - s.rows + s.j);
     }
     return;
   }
-  const int64_t row0 = slot * c.P;
+  const int each = query_rows(c, tr.R), in = (side - 2) * each;
+  const int64_t row0 = slot * c.P + in;
   if (row0 >= c.T) return;
-  const int n = (int)min((int64_t)c.P, c.T - row0);
+  const int n = (int)min((int64_t)min(each, c.P - in), c.T - row0);
   if ((int)threadIdx.x < n) {
     const int64_t row = row0 + threadIdx.x;
     const SeqSlot s = find_slot(c, row, 1, 1, 0);
@@ -225,7 +269,7 @@ __global__ __launch_bounds__(256) void k_kv_append_rotated(KvArgs c, int64_t fir
     pos[threadIdx.x] = s.rows <= 0 || s.j >= s.rows ? kNoRow : (int)max(p, (int64_t)-1);
   }
   __syncthreads();
-  turn_queries<PAIRS>(c, row0, n, h, tr, pos);
+  turn_rows<PAIRS>(c, row0, n, h, tr, pos);
 }
 
 }  // namespace
@@ -238,7 +282,8 @@ hipError_t launch_kv_append_rotated(const KvArgs& c, bool i8, bool pairs, const 
   const int div = by_rows ? 1 : c.P, per = by_rows ? 0 : 2;
   const int64_t slots = by_rows ? c.T : by_pages;
   for (int64_t first = 0; first < slots; first += kGridX) {
-    const dim3 grid((unsigned)min(slots - first, (int64_t)kGridX), (unsigned)c.H, r.q ? 3 : 2);
+    const int queries = !r.q ? 0 : by_rows ? 1 : (c.P + query_rows(c, r.R) - 1) / query_rows(c, r.R);
+    const dim3 grid((unsigned)min(slots - first, (int64_t)kGridX), (unsigned)c.H, 2 + queries);
     auto go = [&](auto i, auto p) {
       hipLaunchKernelGGL((k_kv_append_rotated<decltype(i)::value, decltype(p)::value>), grid, dim3(256), 0, st, c, first, div, per,
                          k_new, ldk, v_new, ldv, r);
