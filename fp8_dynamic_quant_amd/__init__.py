@@ -39,6 +39,7 @@ WQ_KV_E4M3, WQ_KV_INT8 = 1, 2
 WQ_EPI_BF16, WQ_EPI_SWIGLU_F32 = 1, 2
 WQ_LAYOUT_PLAIN, WQ_LAYOUT_FRAGMENT = 0, 1
 
+_BF16, _U8, _I8, _I32, _I64 = torch.bfloat16, torch.uint8, torch.int8, torch.int32, torch.int64
 _c_void_p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 
@@ -276,12 +277,12 @@ def wq_group_quant_fp8_ue8m0(x: torch.Tensor, x_q: torch.Tensor | None = None, s
 
 def _rows_2d(name, x, M, K):
     """Row stride of bf16 rows [M, K] with unit stride along K."""
-    if x.shape != (M, K) or x.dtype != torch.bfloat16:
+    if x.shape != (M, K) or x.dtype is not _BF16:
         raise ValueError(f"{name} must be bf16 [{M}, {K}]")
-    s = x.stride()
-    if M and s[1] != 1 and K > 1:
+    row, one = x.stride()
+    if one != 1 and M and K > 1:
         raise ValueError(f"{name} must have unit stride along K")
-    return s[0] if M > 1 else K
+    return row if M > 1 else K
 
 
 def wq_add_rms_quant(x: torch.Tensor, residual: torch.Tensor | None, rms_gamma: torch.Tensor, rms_eps: float = 1e-6, *,
@@ -292,20 +293,22 @@ def wq_add_rms_quant(x: torch.Tensor, residual: torch.Tensor | None, rms_gamma: 
     payload WQ_PAYLOAD_INT8: x_q int8 [M, K], x_s f32 [M]; WQ_PAYLOAD_FP8_E4M3 and WQ_PAYLOAD_MXFP8:
     x_q uint8 [M, 1, K] and x_s the int32 storage [1, PH, TA], operands of wq_quant_matmul with
     fp8_groups=1.  sum_out may be residual or x itself."""
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be bf16 [M, K]")
-    M, K = x.shape
+    M, K = shape
     ldx = _rows_2d("x", x, M, K)
     ldr = _rows_2d("residual", residual, M, K) if residual is not None else 0
-    if rms_gamma.shape != (K,) or rms_gamma.dtype != torch.bfloat16 or not rms_gamma.is_contiguous():
+    if rms_gamma.shape != (K,) or rms_gamma.dtype is not _BF16 or not rms_gamma.is_contiguous():
         raise ValueError("rms_gamma must be contiguous bf16 [K]")
+    dense = x.is_contiguous()  # (empty_like is 1 us quicker than new_empty, a third of it)
     if payload == WQ_PAYLOAD_INT8:
         qshape, qtype, sshape, stype = (M, K), torch.int8, (M,), torch.float32
     else:
         packs = (K + 511) // 512 if payload == WQ_PAYLOAD_FP8_E4M3 else (K + 127) // 128
         qshape, qtype, sshape, stype = (M, 1, K), torch.uint8, (1, packs, (M + 3) // 4 * 4), torch.int32
     if x_q is None:
-        x_q = x.new_empty(qshape, dtype=qtype)
+        x_q = torch.empty_like(x, dtype=qtype) if dense and qshape == shape else x.new_empty(qshape, dtype=qtype)
     elif x_q.shape != qshape or x_q.dtype != qtype or not x_q.is_contiguous():
         raise ValueError(f"x_q must be contiguous {qtype} {list(qshape)}")
     if x_s is None:
@@ -315,16 +318,19 @@ def wq_add_rms_quant(x: torch.Tensor, residual: torch.Tensor | None, rms_gamma: 
     if sum_out is not None:
         lds = _rows_2d("sum_out", sum_out, M, K)
     elif residual is not None:
-        sum_out, lds = x.new_empty((M, K)), K
+        sum_out, lds = torch.empty_like(x) if dense else x.new_empty((M, K)), K
     else:
         lds = 0
     if y is not None:
         ldy = _rows_2d("y", y, M, K)
     elif return_y:
-        y, ldy = x.new_empty((M, K)), K
+        y, ldy = torch.empty_like(x) if dense else x.new_empty((M, K)), K
     else:
         ldy = 0
-    h, stream = _on("wq_add_rms_quant", x, rms_gamma, x_q, x_s, *(t for t in (residual, sum_out, y) if t is not None))
+    if residual is not None and sum_out is not None and y is None:
+        h, stream = _on("wq_add_rms_quant", x, rms_gamma, x_q, x_s, residual, sum_out)
+    else:
+        h, stream = _on("wq_add_rms_quant", x, rms_gamma, x_q, x_s, *(t for t in (residual, sum_out, y) if t is not None))
     st = lib().wq_add_rms_quant(h, x.data_ptr(), ldx, _ptr(residual), ldr, rms_gamma.data_ptr(), rms_eps, M, K, payload,
                                 x_q.data_ptr(), x_s.data_ptr(), _ptr(sum_out), lds, _ptr(y), ldy, stream)
     if st:
@@ -498,36 +504,38 @@ def kv_cache(pages: int, heads: int, page_tokens: int, head_dim: int, *, dtype=t
 
 def _kv_desc(cache, offsets, lens, table):
     k, v, ks, vs = cache
-    if k.dim() != 4 or (k.dtype != torch.uint8 and k.dtype != torch.int8) or v.dtype != k.dtype:
+    code, shape = k.dtype, k.shape
+    if len(shape) != 4 or (code is not _U8 and code is not _I8) or v.dtype is not code:
         raise ValueError("a cache's codes are uint8 (E4M3) or int8, k [pages, heads, page_tokens, D]")
-    pages, heads, page_tokens, D = k.shape
+    pages, heads, page_tokens, D = shape
     if v.shape != (pages, heads, D, page_tokens) or ks.shape != (pages, heads) or vs.shape != (pages, heads) \
-            or ks.dtype != torch.uint8 or vs.dtype != torch.uint8:
+            or ks.dtype is not _U8 or vs.dtype is not _U8:
         raise ValueError("a cache has v [pages, heads, D, page_tokens] and uint8 k_scale, v_scale [pages, heads]")
     if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
         raise ValueError("a cache's tensors must be contiguous")
-    if offsets.dtype != torch.int64 or lens.dtype != torch.int32 or table.dtype != torch.int32:
+    if offsets.dtype is not _I64 or lens.dtype is not _I32 or table.dtype is not _I32:
         raise ValueError("offsets are int64, lens and table int32")
-    B = lens.numel()
-    if lens.dim() != 1 or offsets.shape != (B + 1,) or table.dim() != 2 or not offsets.is_contiguous() \
+    B, rows = lens.numel(), table.shape
+    if lens.dim() != 1 or offsets.shape != (B + 1,) or len(rows) != 2 or not offsets.is_contiguous() \
             or not lens.is_contiguous():
         raise ValueError("offsets must be [B + 1], lens [B] and table [B, pages of a sequence]")
-    Bt, width = table.shape
+    Bt, width = rows
     ts = table.stride()
     if Bt != B or (width > 1 and ts[1] != 1):
         raise ValueError("table must be [B, pages of a sequence] with dense rows")
-    return KvCacheDesc(WQ_KV_INT8 if k.dtype == torch.int8 else WQ_KV_E4M3, pages, heads, page_tokens, D, k.data_ptr(),
+    return KvCacheDesc(WQ_KV_INT8 if code is _I8 else WQ_KV_E4M3, pages, heads, page_tokens, D, k.data_ptr(),
                        v.data_ptr(), ks.data_ptr(), vs.data_ptr(), table.data_ptr(), ts[0] if B > 1 else width, width), B
 
 
 def _kv_rows(name, x, heads, D):
     """Row stride of bf16 rows [T, heads, D] whose last two axes are dense."""
-    if x.dim() != 3 or x.dtype != torch.bfloat16 or x.shape[1] != heads or x.shape[2] != D:
+    shape = x.shape
+    if len(shape) != 3 or x.dtype is not _BF16 or shape[1] != heads or shape[2] != D:
         raise ValueError(f"{name} must be bf16 [T, {heads}, {D}]")
-    s = x.stride()
-    if x.shape[0] and (s[2] != 1 or (heads > 1 and s[1] != D)):
+    row, head, one = x.stride()
+    if shape[0] and (one != 1 or (heads > 1 and head != D)):
         raise ValueError(f"{name} must have dense rows")
-    return s[0] if x.shape[0] > 1 else heads * D
+    return row if shape[0] > 1 else heads * D
 
 
 def wq_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, offsets, lens, table) -> None:
@@ -569,12 +577,13 @@ def wq_kv_append_rotated(cache: KvCache, k: torch.Tensor, v: torch.Tensor, offse
         raise ValueError("angles must be contiguous f32 [positions, 2, rot_dim / 2]")
     heads, qp, ldq, qo, ldo = 0, None, 0, None, 0
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T:
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != T:
             raise ValueError("q must be bf16 [T, q_heads, D]")
-        heads = q.shape[1]
+        heads = shape[1]
         ldq = _kv_rows("q", q, heads, D)
         if q_out is None:
-            q_out, ldo = q.new_empty((T, heads, D)), heads * D
+            q_out, ldo = torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, heads, D)), heads * D
         else:
             if q_out.dim() != 3 or q_out.shape[0] != T:
                 raise ValueError("q_out must have q's shape")
@@ -593,12 +602,13 @@ def wq_kv_append_rotated(cache: KvCache, k: torch.Tensor, v: torch.Tensor, offse
 
 def _attention_outputs(d, q, out, lse, return_lse):
     """Sizes, strides and outputs that the attention calls have in common."""
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be bf16 [T, q_heads, D]")
-    T, heads, D = q.shape
+    T, heads, D = shape
     ldq = _kv_rows("q", q, heads, d.head_dim)
     if out is None:
-        out, ldo = q.new_empty((T, heads, D)), heads * D
+        out, ldo = torch.empty_like(q) if q.is_contiguous() else q.new_empty((T, heads, D)), heads * D
     else:
         if out.dim() != 3 or out.shape[0] != T:
             raise ValueError("out must have q's shape")
@@ -640,7 +650,7 @@ def wq_kv_attention_shared(cache: KvCache, q: torch.Tensor, offsets, lens, table
     are read and multiplied once for all of them."""
     d, B = _kv_desc(cache, offsets, lens, table)
     for name, x in (("group", group), ("shared", shared)):
-        if x.shape != (B,) or x.dtype != torch.int32 or not x.is_contiguous():
+        if x.shape != (B,) or x.dtype is not _I32 or not x.is_contiguous():
             raise ValueError(f"{name} must be contiguous int32 [B]")
     T, heads, D, ldq, out, ldo, lse = _attention_outputs(d, q, out, lse, return_lse)
     h, stream = _on("wq_kv_attention_shared", q, *cache, offsets, lens, table, group, shared, out, *(() if lse is None else (lse,)))
