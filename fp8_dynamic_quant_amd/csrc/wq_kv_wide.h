@@ -44,7 +44,7 @@ struct Wide {
     return D == 64 ? j >> 1 : j;
   }
   static __device__ __forceinline__ int value_place(int row) {
-    return T == 64 ? (row & 2) << 1 ^ (row & 4) >> 1 ^ ((row & 8) >> 3) * 3 : (row >> 2) & 3;
+    return T == 64 ? (row & 2) << 1 ^ (row & 4) >> 1 ^ ((row & 8) >> 3) * 3 : -(row >> 2) & 3;
   }
 
   // r0: the first row of the wave; rows past the last repeat it (and are not stored)
