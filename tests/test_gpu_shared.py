@@ -174,6 +174,59 @@ def test_prompts_of_many_rows_are_attention_as_it_is(D):
     assert paths[0] == paths[1] != 16
 
 
+def _dense64(cd, q, ns, lens, table, scale):
+    """kf.attention on the device, causal, of many tokens: (out, lse, mag, smag)."""
+    k, v, ks, vs = cd
+    P, (T, Hq, D) = k.shape[2], q.shape
+    H = k.shape[1]
+    value = lambda x: (x if x.dtype == torch.int8 else x.view(torch.float8_e4m3fn)).to(torch.float64)  # noqa: E731
+    out, lse = torch.empty((T, Hq, D), dtype=torch.float64), torch.empty((T, Hq), dtype=torch.float64)
+    mag, smag = torch.empty_like(out), torch.empty_like(lse)
+    row = 0
+    for n, length, pages in zip(ns, lens, dev(table).long()):
+        pages = pages[: -(-length // P)]
+        see = torch.arange(length, device=DEV)[None] <= (length - n + torch.arange(n, device=DEV))[:, None]
+        for h in range(H):
+            kk = (value(k[pages, h]) * torch.exp2(ks[pages, h].double() - 127)[:, None, None]).reshape(-1, D)[:length]
+            vv = (value(v[pages, h]).transpose(1, 2) * torch.exp2(vs[pages, h].double() - 127)[:, None, None]).reshape(-1, D)[:length]
+            at, rows = slice(h * (Hq // H), (h + 1) * (Hq // H)), slice(row, row + n)
+            x = q[rows, at].double().reshape(-1, D)
+            seen = see.repeat_interleave(Hq // H, 0)
+            back = lambda y: y.view(n, Hq // H, *y.shape[1:]).cpu()  # noqa: E731
+            smag[rows, at] = back(torch.where(seen, scale * (x.abs() @ kk.abs().T.contiguous()), 0.0).amax(1))
+            s = torch.where(seen, scale * (x @ kk.T.contiguous()), -torch.inf)
+            lse[rows, at] = back(torch.logsumexp(s, 1))
+            w = torch.softmax(s, 1)
+            out[rows, at], mag[rows, at] = back(w @ vv), back(w @ vv.abs())
+        row += n
+    return out.numpy(), lse.numpy(), mag.numpy(), smag.numpy()
+
+
+@pytest.mark.parametrize("D, i8, P, S", [(128, False, 64, 18 * 8192), (128, True, 48, 65536), (64, False, 128, 18 * 8192), (64, True, 16, 65536),
+                                         (256, False, 128, 5 * 16384), (256, True, 32, 32768)])
+def test_runs_of_many_steps(D, i8, P, S):
+    # more than 64 steps, or 64 groups of 16 tokens, in each of 256 runs: what tells pages is read 64 entries
+    # at a time.  The cache is small: tables name its pages again and again.
+    H, R, ns = 8, 2, [80, 100]
+    g = syn.rng(121, D, P)
+    c = list(kf.cache(g, 61, H, P, D, i8))
+    shared = S // P * P
+    lens = [shared + n + x for n, x in zip(ns, (3, 250))]
+    table = g.integers(0, 61, (2, -(-max(lens) // P))).astype(np.int32)
+    table[1, : shared // P] = table[0, : shared // P]
+    q = nm.f64_to_bf16_rn(g.standard_normal((sum(ns), H * R, D)))
+    cd = wq.KvCache(*(dev(x) for x in c))
+    args = [bf16_dev(q), dev(np.array([0, 80, 180], np.int64)), *(dev(np.array(x, np.int32)) for x in (lens, table, [0, 0], [shared] * 2))]
+    print(f"long runs D={D} i8={i8} P={P} tokens={lens}", flush=True)
+    assert wq.wq_kv_attention_shared_path(cd, 180, H * R, args[3]) == 16
+    out, lse = wq.wq_kv_attention_shared(cd, *args, return_lse=True)
+    want, want_lse, mag, smag = _dense64(cd, args[0], ns, lens, table, D**-0.5)
+    # sums of this many terms in f32: a step's 64 weights go into one sum, and there is one sum a step
+    lim, lim_lse = _limits(want, want_lse, mag, smag, max(lens) // 64 + 64, D)
+    got, got_lse = nm.bf16_to_f32(host_bf16_bits(out)), host(lse)
+    assert (np.abs(got - want) <= lim).all() and (np.abs(got_lse - want_lse) <= lim_lse).all()
+
+
 @pytest.mark.parametrize("falling", [False, True])
 @pytest.mark.parametrize("ns", [[1] * 8, [20] * 8])
 @pytest.mark.parametrize("D, i8", [(64, False), (128, False), (128, True), (256, True)])
