@@ -373,9 +373,9 @@ __device__ __forceinline__ void narrow_runs(const ShareArgs& s, const SharePlan&
   }
 }
 
-template <int D, bool I8, int RT, bool U>
+template <int D, bool I8, int RT>
 __device__ __forceinline__ void take_wide(const Share& r, const SharePlan& p, const ShareLds& l, uint8_t* smem, int wv, int lane) {
-  using W = Wide<D, I8, RT, U>;
+  using W = Wide<D, I8, RT>;
   constexpr uint32_t kSub = kTokTile / W::T;  // its steps to one of 64 tokens
   const int j = lane & 15, g = lane >> 4;
   const int64_t t0 = (int64_t)r.it.tile * wide_rows(D), r0 = t0 + wv * 16 * RT;
@@ -387,7 +387,7 @@ __device__ __forceinline__ void take_wide(const Share& r, const SharePlan& p, co
   for (int rt = 0; rt < RT; ++rt) store_share<D>(r, p, l, w.o[rt], w.mx[rt], w.sum[rt], (uint32_t)r0 + 16 * rt + j, g);
 }
 
-template <int D, bool I8, bool U>
+template <int D, bool I8>
 __device__ __forceinline__ void wide_runs(const ShareArgs& s, const SharePlan& p, const ShareLds& l, uint32_t run, uint8_t* smem, int wv,
                                           int lane) {
   const uint32_t per = p.axis[kWide].per, end = min((run + 1) * per, p.axis[kWide].units);
@@ -399,15 +399,15 @@ __device__ __forceinline__ void wide_runs(const ShareArgs& s, const SharePlan& p
     if (!some) continue;
     if constexpr (D < 256) {
       if ((uint32_t)r.q.nrows - r.it.tile * wide_rows(D) > 128u) {
-        take_wide<D, I8, 2, U>(r, p, l, smem, wv, lane);
+        take_wide<D, I8, 2>(r, p, l, smem, wv, lane);
         continue;
       }
     }
-    take_wide<D, I8, 1, U>(r, p, l, smem, wv, lane);
+    take_wide<D, I8, 1>(r, p, l, smem, wv, lane);
   }
 }
 
-template <int D, bool I8, bool U>
+template <int D, bool I8>
 __global__ __launch_bounds__(kThreads, 2) void k_kv_shared(ShareArgs s) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ ShareLds lds;
@@ -416,7 +416,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_shared(ShareArgs s) {
   const SharePlan plan = make_share_plan<D>(s, lds);
   const uint32_t wide = plan.axis[kWide].runs;  // workgroups that take wide runs; the waves of the others narrow ones
   if (blockIdx.x < wide) {
-    wide_runs<D, I8, U>(s, plan, lds, blockIdx.x, smem, wv, lane);
+    wide_runs<D, I8>(s, plan, lds, blockIdx.x, smem, wv, lane);
   } else if constexpr (D < 256) {
     narrow_runs<D, I8>(s, plan, lds, blockIdx.x - wide + (uint32_t)wv * (gridDim.x - wide), lane);
   }
@@ -587,10 +587,10 @@ ShareShape share_shape(const KvArgs& c, int R, int num_cu) {
   return s;
 }
 
-template <int D, bool I8, bool U>
+template <int D, bool I8>
 hipError_t shared_of(ShareArgs s, int64_t keys, hipStream_t st) {
-  constexpr int lds = Wide<D, I8, 1, U>::kBytes;
-  hipError_t e = set_lds_limit(reinterpret_cast<const void*>(k_kv_shared<D, I8, U>), lds);
+  constexpr int lds = Wide<D, I8, 1>::kBytes;
+  hipError_t e = set_lds_limit(reinterpret_cast<const void*>(k_kv_shared<D, I8>), lds);
   if (e != hipSuccess) return e;
   const ShareArgs all = s;
   const int cus = s.a.runs;
@@ -601,7 +601,7 @@ hipError_t shared_of(ShareArgs s, int64_t keys, hipStream_t st) {
     s.a.c.table = all.a.c.table + b * all.a.c.table_stride;
     s.group = all.group + b;
     s.shared = all.shared + b;
-    hipLaunchKernelGGL((k_kv_shared<D, I8, U>), dim3((unsigned)cus), dim3(kThreads), lds, st, s);
+    hipLaunchKernelGGL((k_kv_shared<D, I8>), dim3((unsigned)cus), dim3(kThreads), lds, st, s);
     // a wave a row once that fills the chip (rows have few parts then): 2048 rows of 128 in up to 22
     // parts 41.0 us with what comes before, a workgroup a row 41.7; 1536 rows of 256 77.2 and 75.0
     if (keys >= 8 * cus)
@@ -632,11 +632,12 @@ hipError_t launch_kv_attention_shared(KvAttnArgs a, bool i8, const int32_t* grou
   ShareArgs s{a, group, shared, static_cast<uint4*>(ws)};
   s.a.part = reinterpret_cast<float*>(s.desc + sh.keys);
   s.a.stat = reinterpret_cast<float2*>(s.a.part + sh.slots * a.c.D);
-  auto go = [&](auto d, auto i, auto u) { return shared_of<decltype(d)::value, decltype(i)::value, decltype(u)::value>(s, sh.keys, st); };
-  auto codes = [&](auto d, auto u) { return i8 ? go(d, std::true_type{}, u) : go(d, std::false_type{}, u); };
-  auto pages = [&](auto d) { return a.c.P % kTokTile == 0 ? codes(d, std::true_type{}) : codes(d, std::false_type{}); };
-  if (a.c.D == 64) return pages(std::integral_constant<int, 64>{});
-  return a.c.D == 128 ? pages(std::integral_constant<int, 128>{}) : pages(std::integral_constant<int, 256>{});
+  auto go = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    return i8 ? shared_of<D, true>(s, sh.keys, st) : shared_of<D, false>(s, sh.keys, st);
+  };
+  if (a.c.D == 64) return go(std::integral_constant<int, 64>{});
+  return a.c.D == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 256>{});
 }
 
 }  // namespace wq

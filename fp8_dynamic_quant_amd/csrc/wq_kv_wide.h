@@ -22,14 +22,15 @@ constexpr int kWideWaves = 8;
 //
 // Pieces of 16 bytes are XORed with their row so that the sixteen lanes of a read meet sixteen different
 // places of 256 bytes: key rows by the lane that reads them, value rows by their number.
-// U: pages hold whole steps (P a multiple of 64), so that a step lies in one page and its place is the
-// same for the whole workgroup: page numbers come by scalar loads, and DMA takes scalar bases.
-template <int D, bool I8, int RT, bool U>
+// A step's token groups of 16 each have a page of their own to look up; taking one for the whole step
+// where pages hold whole ones, with scalar addresses, was 1 % quicker at best (183 and 186 us).
+template <int D, bool I8, int RT>
 struct Wide {
   static constexpr int T = D == 256 ? 32 : 64;  // tokens of a step: two buffers of 32 KiB
   static constexpr int kGroups = T / 16, NT = T / 16, NK = D / 32, NV = D / 16, NM = T / 32;
   static constexpr int kTile = T * D, kRaw = 2 * kTile, kBuf = 2 * kTile, kRing = 3;
-  static constexpr int kKeys = kRing * kRaw, kValues = kKeys + 2 * kBuf, kScales = kValues + 2 * kBuf, kTable = kScales + 4 * 256, kBytes = kTable + 512;
+  static constexpr int kKeys = kRing * kRaw, kValues = kKeys + 2 * kBuf, kScales = kValues + 2 * kBuf;
+  static constexpr int kTable = kScales + 4 * 256, kBytes = kTable + 512;
   static constexpr int kDma = D == 64 ? 1 : 2;  // of a wave and step, and the first wave's scale bytes
   static constexpr int kRows = 16 * RT * kWideWaves;
 
@@ -125,34 +126,26 @@ struct Wide {
     const uint8_t* scales = (lane & 4 ? c.v_scale : c.k_scale) + h;
     auto slot_of = [&](uint32_t tg) __attribute__((always_inline)) { return (tg - by_page(tg, recip, one) * per) * 16; };
     auto entry = [&](uint32_t tg) __attribute__((always_inline)) { return 16 * tg < s.seen ? by_page(tg, recip, one) : 0u; };
-    // page of a step (U), or of its token group `mine`; -1 where there is none
+    // page of a step's token group `mine`; -1 where there is none
     auto checked = [&](uint32_t step, int page) __attribute__((always_inline)) {
-      return 16 * (kGroups * (lo + step) + (U ? 0 : mine)) < s.seen && (uint32_t)page < (uint32_t)c.pages ? page : -1;
+      return 16 * (kGroups * (lo + step) + mine) < s.seen && (uint32_t)page < (uint32_t)c.pages ? page : -1;
     };
     auto number = [&](uint32_t step) __attribute__((always_inline)) {  // the table's, of a step in any case
       const uint32_t at = min(step, n - 1);
-      if constexpr (U) return checked(at, uniform(s.table[entry(kGroups * (lo + at))]));
-      else return checked(at, s.table[entry(kGroups * (lo + at) + mine)]);
+      return checked(at, s.table[entry(kGroups * (lo + at) + mine)]);
     };
     auto none_of = [&](int page) __attribute__((always_inline)) {
-      return U ? (page < 0 ? 15u : 0u) : (uint32_t)__ballot(page < 0) & ((1u << kGroups) - 1u);
+      return (uint32_t)__ballot(page < 0) & ((1u << kGroups) - 1u);
     };
     // step b at the group's page (page 0 where there is none: it is masked)
     auto issue = [&](uint32_t b, int page_of, int slot) __attribute__((always_inline)) {
       const uint32_t raw = lds0 + slot * kRaw, held = (uint32_t)max(page_of, 0);
-      if constexpr (U) {
-        const uint64_t at = (uint64_t)held * page_step;
-        const uint32_t in = slot_of(kGroups * (lo + b));
-        if (D != 64 || wv < 4) dma16(K + at + in * D, kgroup * 16 * D + koff, raw + kw * 1024);
-        if (D != 64 || wv >= 4) dma16(V + at + in, voff + 16 * mine, raw + kTile + vw * 1024);
-      } else {
-        if (D != 64 || wv < 4) {
-          const uint32_t page = (uint32_t)__builtin_amdgcn_readlane((int)held, kgroup);
-          dma16(K + (uint64_t)page * page_step + slot_of(kGroups * (lo + b) + kgroup) * D, koff, raw + kw * 1024);
-        }
-        if (D != 64 || wv >= 4)
-          dma16_at(V + (uint64_t)held * page_step + (voff + slot_of(kGroups * (lo + b) + mine)), raw + kTile + vw * 1024);
+      if (D != 64 || wv < 4) {
+        const uint32_t page = (uint32_t)__builtin_amdgcn_readlane((int)held, kgroup);
+        dma16(K + (uint64_t)page * page_step + slot_of(kGroups * (lo + b) + kgroup) * D, koff, raw + kw * 1024);
       }
+      if (D != 64 || wv >= 4)
+        dma16_at(V + (uint64_t)held * page_step + (voff + slot_of(kGroups * (lo + b) + mine)), raw + kTile + vw * 1024);
       // scale bytes: word x the keys' of token group x, word 4 + x the values'
       if (wv == 0) dma1_at(scales + (uint64_t)held * H, lds0 + kScales + (b & 3) * 256);
     };
@@ -187,14 +180,12 @@ struct Wide {
     };
     // ---- steps 0, 1, 2 on their way
     const int p0 = number(0), p1 = number(1), p2 = number(2);
-    // table entries, 64 of steps (U) or token groups at a time, by DMA: half (q & 1) of 512 bytes holds
-    // those from 64 q on
-    constexpr uint32_t kEach = U ? 1 : kGroups;  // of a step
+    // table entries of 64 token groups at a time, by DMA: half (q & 1) of 512 bytes holds those from 64 q on
     auto send_entries = [&](uint32_t q) __attribute__((always_inline)) {
-      dma4_at(s.table + entry(kGroups * lo + min(64 * q + lane, kEach * n - 1) * (kGroups / kEach)), lds0 + kTable + (q & 1) * 256);
+      dma4_at(s.table + entry(kGroups * lo + min(64 * q + lane, kGroups * n - 1)), lds0 + kTable + (q & 1) * 256);
     };
     auto told = [&](uint32_t step) __attribute__((always_inline)) {
-      return *reinterpret_cast<const int*>(smem + kTable + ((kEach * step + (U ? 0 : mine)) & 127) * 4);
+      return *reinterpret_cast<const int*>(smem + kTable + ((kGroups * step + mine) & 127) * 4);
     };
     if (wv == 0) send_entries(0);
     issue(0, p0, 0);
@@ -220,7 +211,7 @@ struct Wide {
     const uint8_t* vread = smem + kValues + j * 2 * T;
     const uint32_t vpiece = (uint32_t)((g ^ value_place(j)) << 4);
     const int x = T == 64 ? g : g >> 1;  // the lane's token group
-    int slot = 0, next_page = checked(3, U ? uniform(told(3)) : told(3));
+    int slot = 0, next_page = checked(3, told(3));
     // the next step has landed for all; this one is widened; the one before has been read by all
     auto meet = [&](uint32_t b) __attribute__((always_inline)) {
       if (b + 2 >= n) wait_vm<0>();
@@ -233,7 +224,7 @@ struct Wide {
       if (b + 3 < n) {
         issue(b + 3, next_page, slot);
         none |= none_of(next_page) << 12;
-        if (wv == 0 && (b * kEach) % 64 == 0 && b * kEach + 64 < kEach * n) send_entries(b * kEach / 64 + 1);
+        if (wv == 0 && (b * kGroups) % 64 == 0 && b * kGroups + 64 < kGroups * n) send_entries(b * kGroups / 64 + 1);
       }
       slot = slot == 2 ? 0 : slot + 1;
       none >>= 4;
@@ -244,10 +235,9 @@ struct Wide {
         meet(b);
         send(b);
         fetch(b + 1, none & 15u, slot);
-        const int page = told(b + 4);
+        next_page = checked(b + 4, told(b + 4));
         widen_keys(b + 1);
         widen_values(b + 1);
-        next_page = checked(b + 4, U ? uniform(page) : page);
       }
       lds_barrier();  // the ring and the buffers may be filled again
       return;
@@ -419,7 +409,7 @@ struct Wide {
         __builtin_amdgcn_sched_group_barrier(0x002, I8 ? 6 : 3, 0);
         __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
       }
-      next_page = checked(b + 4, U ? uniform(page) : page);
+      next_page = checked(b + 4, page);
     }
     lds_barrier();  // the ring and the buffers may be filled again
   }
