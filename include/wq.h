@@ -466,7 +466,9 @@ int wq_kv_attention_path(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T,
  * floor(shared / page_tokens) entries are equal over the group (where they are not, the entries of
  * its first sequence with rows are taken).  A group's least such number counts, in whole pages and
  * whole steps of 64 tokens, and no more than every row of it sees; the remaining tokens are read for
- * each sequence.  Results differ from wq_kv_attention's by the order of f32 sums alone.
+ * each sequence.  Results differ from wq_kv_attention's by the order of f32 sums and by where a
+ * weight's rounding to bf16 falls (2^-8 of it, as there); weights are up to 2^8 here, so that the
+ * values' weighted sums have to stay below 2^120.
  * workspace: as there, of at least wq_kv_attention_shared_workspace_bytes(); NULL: the context's
  * (WQ_ERR_WORKSPACE where that is too small). */
 int wq_kv_attention_shared(wq_ctx* ctx, const wq_kv_cache* cache, const void* q, int64_t ldq, int64_t T,
