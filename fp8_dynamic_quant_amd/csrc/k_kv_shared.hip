@@ -20,7 +20,7 @@
 //   64 of 500 behind 8192, the same heads, int8                      40.4   6  short runs: beginnings, parts
 //   256 of 1500 behind 32768, the same heads                          237  10  the wide kernel's arithmetic
 //   24 of 4 rows and 300 tokens behind four documents of 32768,
-//   16 heads of 256 on one                                           70.5   8  LDS reads of the wide kernel
+//   16 heads of 256 on one                                           70.5   8  chains of reads and products, a row tile a wave
 #include "wq_kernels.h"
 #include "wq_kv_wide.h"
 #include "wq_layer.h"
