@@ -107,6 +107,15 @@ def test_many_rows(kind, M, K):
     _check(kind, *_inputs(2, M, K), pad=16, want_y=M != 64)
 
 
+# rows on either side of two for each CU, where a row has fewer threads
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("K", [2176, 4096, 4224, 8192])
+def test_as_many_rows_as_fill_the_chip(kind, K):
+    most = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    for M in (most, most + 3):
+        _check(kind, *_inputs(5, M, K), want_y=M > most)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_without_a_residual(kind):
     _check(kind, *_inputs(3, 5, 1152, r=False))

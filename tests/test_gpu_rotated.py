@@ -100,6 +100,13 @@ def test_heads(H, R):
         _check(H + R, False, 32, 128, H, R, 128, False, ns, [30, 31, 60], 2, extra=2)
 
 
+# a page's queries by one workgroup or several, whole fours of heads and rests of them
+@pytest.mark.parametrize("P, D, H, R", [(128, 256, 1, 16), (256, 128, 2, 5), (64, 128, 1, 70), (256, 64, 3, 1), (48, 256, 2, 6)])
+def test_prompts_of_many_heads(P, D, H, R):
+    for pairs in (False, True):
+        _check(P + R, pairs, P, D, H, R, D // 2, pairs, [P + 40, 2, P - 7], [P + 43, P + 1, P - 7], 3, extra=5)
+
+
 @pytest.mark.parametrize("i8", [False, True])
 def test_without_queries(i8):
     _check(1, i8, 16, 64, 2, 2, 64, False, [1, 20, 0], [5, 33, 9], 4, with_q=False)
