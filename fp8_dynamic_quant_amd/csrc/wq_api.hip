@@ -920,18 +920,18 @@ int wq_kv_append(wq_ctx* c, const wq_kv_cache* k, const void* k_new, int64_t ldk
 
 // q_heads a multiple of the cache's heads; a cache head's rows and the row tiles are counted in 32
 // bits, the tiles' steps of 64 tokens in 52
-static bool kv_heads_ok(const wq_kv_cache* k, int64_t q_heads, int64_t T, int64_t B, double unit = 1.0) {
+static bool kv_heads_ok(const wq_kv_cache* k, int64_t q_heads, int64_t T, int64_t B) {
   if (q_heads < k->heads || q_heads % k->heads != 0 || q_heads > (1 << 20)) return false;
   const int64_t rows = T * (q_heads / k->heads), tiles = (rows / 16 + B) * k->heads;
-  return rows < ((int64_t)1 << 31) && tiles < ((int64_t)1 << 31) && unit * (double)tiles * ((double)k->max_pages * k->page_tokens / 64 + 16) < 4503599627370496.0;
+  return rows < ((int64_t)1 << 31) && tiles < ((int64_t)1 << 31) && (double)tiles * ((double)k->max_pages * k->page_tokens / 64 + 16) < 4503599627370496.0;
 }
 
 // the sizes that choose attention's kernels: 0, 1 for an empty problem, or -status
-static int kv_sizes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B, wq::KvArgs* a, double unit = 1.0) {
+static int kv_sizes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B, wq::KvArgs* a) {
   if (!c || !k) return -WQ_ERR_NULL;
   if (k->heads < 1 || k->page_tokens < 16 || k->page_tokens > 256 || k->max_pages < 1 || k->max_pages > INT32_MAX ||
       !wq::kv_head_dim_ok(k->head_dim) || T < 0 || B < 0 || T > ((int64_t)1 << 30) || B > ((int64_t)1 << 24) ||
-      !kv_heads_ok(k, q_heads, T, B, unit))
+      !kv_heads_ok(k, q_heads, T, B))
     return -WQ_ERR_SHAPE;
   if (T == 0 || B == 0) return 1;
   a->H = (int)k->heads;
@@ -1080,18 +1080,15 @@ int wq_kv_append_rotated(wq_ctx* c, const wq_kv_cache* k, const void* k_new, int
   return status_of(e);
 }
 
-// attention behind a shared prefix: up to twice the tiles, up to three units a step
-constexpr double kSharedUnit = 8.0;
-
 int64_t wq_kv_attention_shared_workspace_bytes(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B) {
   wq::KvArgs a{};
-  if (int r = kv_sizes(c, k, T, q_heads, B, &a, kSharedUnit)) return r < 0 ? r : 0;
+  if (int r = kv_sizes(c, k, T, q_heads, B, &a)) return r < 0 ? r : 0;
   return (int64_t)wq::kv_shared_workspace(a, (int)(q_heads / k->heads), c->num_cu);
 }
 
 int wq_kv_attention_shared_path(const wq_ctx* c, const wq_kv_cache* k, int64_t T, int64_t q_heads, int64_t B) {
   wq::KvArgs a{};
-  if (int r = kv_sizes(c, k, T, q_heads, B, &a, kSharedUnit)) return r < 0 ? r : 0;
+  if (int r = kv_sizes(c, k, T, q_heads, B, &a)) return r < 0 ? r : 0;
   return wq::kv_shared_path(a, (int)(q_heads / k->heads), c->num_cu);
 }
 
@@ -1103,7 +1100,6 @@ int wq_kv_attention_shared(wq_ctx* c, const wq_kv_cache* k, const void* q, int64
   if (int r = attention_args(c, k, q, ldq, T, q_heads, B, offsets, lens, scale, causal, out, ldo, lse, &workspace, &workspace_bytes, &a))
     return r;
   if (T == 0 || B == 0) return WQ_OK;
-  if (!kv_heads_ok(k, q_heads, T, B, kSharedUnit)) return WQ_ERR_SHAPE;
   if (!group || !shared) return WQ_ERR_NULL;
   if (workspace_bytes < wq::kv_shared_workspace(a.c, a.R, c->num_cu)) return WQ_ERR_WORKSPACE;
   DeviceGuard g(c->device);
