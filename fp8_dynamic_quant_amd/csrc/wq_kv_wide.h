@@ -133,14 +133,14 @@ struct Wide {
     const uint32_t voff = (uint32_t)((vw * (64 / kGroups) + lane / kGroups) * c.P);
     const uint8_t* scales = (lane & 4 ? c.v_scale : c.k_scale) + h;
     auto slot_of = [&](uint32_t tg) __attribute__((always_inline)) { return (tg - by_page(tg, recip, one) * per) * 16; };
-    auto entry = [&](uint32_t tg) __attribute__((always_inline)) { return 16 * tg < s.seen ? by_page(tg, recip, one) : 0u; };
+    auto entry = [&](uint32_t tg) __attribute__((always_inline)) {  // (a choice, no branch: loads of several go together)
+      uint32_t at = by_page(tg, recip, one);
+      asm volatile("" : "+v"(at));
+      return 16 * tg < s.seen ? at : 0u;
+    };
     // page of a step's token group `mine`; -1 where there is none
     auto checked = [&](uint32_t step, int page) __attribute__((always_inline)) {
       return 16 * (kGroups * (lo + step) + mine) < s.seen && (uint32_t)page < (uint32_t)c.pages ? page : -1;
-    };
-    auto number = [&](uint32_t step) __attribute__((always_inline)) {  // the table's, of a step in any case
-      const uint32_t at = min(step, n - 1);
-      return checked(at, s.table[entry(kGroups * (lo + at) + mine)]);
     };
     auto none_of = [&](int page) __attribute__((always_inline)) {
       return (uint32_t)__ballot(page < 0) & ((1u << kGroups) - 1u);
@@ -186,8 +186,21 @@ struct Wide {
       if (D != 64 || t >= 256)
         widen16(vraw, vword == 255u ? 1.0f : scale_of(vword), smem + kValues + (b & 1) * kBuf + row * 2 * T, T == 64 ? x : 2 * x, T == 64 ? 4 : 1, value_place(row));
     };
-    // ---- steps 0, 1, 2 on their way
-    const int p0 = number(0), p1 = number(1), p2 = number(2);
+    // ---- steps 0, 1, 2 on their way (of a step in any case)
+    const int* table = s.table;
+    auto read = [&](uint32_t step) __attribute__((always_inline)) { return table[entry(kGroups * (lo + min(step, n - 1)) + mine)]; };
+    int e0 = read(0), e1 = read(1), e2 = read(2);
+    asm volatile("" : "+v"(e0), "+v"(e1), "+v"(e2));  // all of them are here before the first DMA, which waits would count
+    const int p0 = checked(0, e0), p1 = checked(min(1u, n - 1), e1), p2 = checked(min(2u, n - 1), e2);
+    // the queries have come with them: from here on the waits count DMAs alone
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        v4u q = __builtin_bit_cast(v4u, qf[rt][k]);
+        asm volatile("" : "+v"(q));
+        qf[rt][k] = __builtin_bit_cast(v8bf, q);
+      }
     // table entries of 64 token groups at a time, by DMA: half (q & 1) of 512 bytes holds those from 64 q on
     auto send_entries = [&](uint32_t q) __attribute__((always_inline)) {
       dma4_at(s.table + entry(kGroups * lo + min(64 * q + lane, kGroups * n - 1)), lds0 + kTable + (q & 1) * 256);
@@ -200,15 +213,10 @@ struct Wide {
     if (n > 1) issue(1, p1, 1);
     if (n > 2) issue(2, p2, 2);
     uint32_t none = none_of(p0) | none_of(p1) << 4 | none_of(p2) << 8;  // of step b on, four bits each
-    wait_vm<0>();  // and the queries: the loop's waits then count DMAs alone
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        v4u q = __builtin_bit_cast(v4u, qf[rt][k]);
-        asm volatile("" : "+v"(q));
-        qf[rt][k] = __builtin_bit_cast(v8bf, q);
-      }
+    // step 0 has landed (16 KB a workgroup of 48, and the chip's memory in a third of the time)
+    if (n <= 2) wait_vm<0>();
+    else if (wv == 0) wait_vm<2 * (kDma + 1)>();
+    else wait_vm<2 * kDma>();
     lds_barrier();
     fetch(0, none & 15u, 0);
     widen_keys(0);
