@@ -17,10 +17,13 @@
 //
 // What a call takes, and of it the join, in us:
 //   8 sequences of 50 own tokens behind 1000, 32 heads of 128 on 8   14.7   4  launches, the plan (2.5), steps in turn
-//   64 of 500 behind 8192, the same heads, int8                      40.4   6  short runs: beginnings, parts
+//   64 of 500 behind 8192, the same heads, int8                      38.8   6  short runs: beginnings, parts
 //   256 of 1500 behind 32768, the same heads                          237  10  the wide kernel's arithmetic
 //   24 of 4 rows and 300 tokens behind four documents of 32768,
 //   16 heads of 256 on one                                           70.5   8  chains of reads and products, a row tile a wave
+// A wide run of the second begins its first step 9 us after the launch: plan 2.7, its item found 1.9,
+// rows and limits 1.5, page numbers 1, addresses 1.1, the first step 0.7 (latency, and code that is
+// fetched as it runs); seven steps take 17, their parts 3.
 // Beside attention of each sequence alone, E4M3, 32 query heads of 128 on 8: 64 sequences of 200 own
 // tokens behind 4096 34 and 72, of 2000 behind 512 42 and 47.  Where little is shared the plan and the
 // parts may cost more than it saves: 200 sequences of 500 behind 256, 64 heads of 64 on 8, 38 and 31.
