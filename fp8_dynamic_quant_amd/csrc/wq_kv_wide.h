@@ -276,10 +276,12 @@ struct Wide {
       for (int i = 0; i < kAhead; ++i) frag[i] = key(i);
       const uint32_t gone = none & 15u;
       // The step in sections: the scores of 16 tokens beside the weights of the 16 before.  The weights are
-      // relative to a base that follows the scores only where one passes it by 8 (weights up to 2^8 are as
-      // exact as those up to 1, and sums of them stay far inside 32 bits), and to a whole number, so that
-      // what is summed is scaled by a power of two.  So no maximum is taken: weights that come out too
-      // large, or infinite or NaN where there is no base yet, tell that the step is made again with another.
+      // relative to a base that follows the scores only where they pass it far (weights up to 2^8 are as
+      // exact as those up to 1), and to a whole number, so that what is summed is scaled by a power of two.
+      // So no maximum is taken: a lane's weights whose sum passes 2^8, or is infinite or NaN where there is
+      // no base yet, tell that the step is made again with another.  That sum bounds each of them, and only
+      // passes 2^8 where one of at most 16 passes 2^4: rows with such a score get a new base, and the others'
+      // weights are small enough without.  So none is ever used that is larger than 2^8.
       const uint32_t tok0 = (lo + b) * T, gt = tok0 + (T / 4) * g;
       const bool there = !(gone >> x & 1u), bad = kbyte == 255u || vbyte == 255u;
       const bool mask = uniform(gone != 0 || tok0 + T > s.seen || tok0 + T > first || __any(bad)) != 0;
@@ -352,7 +354,7 @@ struct Wide {
         weights(NT - 1);
         bool far = false;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) far |= !(part[rt] <= 4.0f * NT * 256.0f);
+        for (int rt = 0; rt < RT; ++rt) far |= !(part[rt] <= 256.0f);
         // (once: rows that hold NaN, or see nothing yet, stay as they are)
         if (__builtin_expect(tries != 0 || __any(far) == 0, 1)) break;
         asm volatile("");
@@ -373,7 +375,7 @@ struct Wide {
         }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          const float row = groups_max(top[rt] * ks), mn = row > mx[rt] + 8.0f ? ceilf(row) : mx[rt];
+          const float row = groups_max(top[rt] * ks), mn = row > mx[rt] + 4.0f ? ceilf(row) : mx[rt];
           const float base = mn == -INFINITY ? 0.0f : mn;
           alpha[rt] = __builtin_amdgcn_exp2f(mx[rt] - base);  // a power of two
           mx[rt] = mn;
