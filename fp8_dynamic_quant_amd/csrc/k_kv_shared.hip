@@ -338,17 +338,22 @@ __device__ __forceinline__ void tell_row(const Share& r, const SharePlan& p, con
 }
 
 // A wave's own rows, to the output if nothing else has a part of them, else to the workspace: lane
-// (j, g) holds of row j the elements 16 i + 4 g .. + 3
+// (j, g) holds of row j the elements 16 i + 4 g .. + 3.  total: the sum of the weights, kept: of the
+// weights that o was made with, total itself where the largest of them is 1.
+//
+// Wide's are rounded, the largest too, which may be anything in (1/2, 2^8].  Over their own sum that rounding
+// cancels as far as it is common to what a row sees, so that a row of one token is that token's value; over
+// the other sum it would leave up to 2^-8 of everything (rows of a few large weights: 0.0023 off against 64
+// bits, 0.0017 so, which is the output's own rounding; of many 0.0024 and 0.0021).  o comes to the scale of `total` here, which lse and the join go by.
 template <int D>
 __device__ __forceinline__ void store_share(const Share& r, const SharePlan& p, const ShareLds& l, const v4f (&o)[D / 16], float mx,
-                                            float sum, uint32_t rr, int g) {
-  const float total = groups_sum(sum);
+                                            float total, float kept, uint32_t rr, int g) {
   if (rr >= (uint32_t)r.q.nrows) return;
   const int64_t key = r.key(rr);
   if (r.whole) {
     const int64_t hq = r.a.c.H * r.a.R, token = r.q.row0 + rr / (uint32_t)r.a.R;
     uint16_t* out = r.a.out + token * r.a.ldo + (key - token * hq) * D + 4 * g;
-    const float inv = inverse_sum(total);
+    const float inv = inverse_sum(kept);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       const v4f v = o[i] * inv;
@@ -359,8 +364,9 @@ __device__ __forceinline__ void store_share(const Share& r, const SharePlan& p, 
   } else {
     const int64_t slot = r.template slot<D>(rr, key);
     float* to = r.a.part + slot * D + 4 * g;
+    const float back = kept > 0.0f ? total / kept : 1.0f;  // (rows that saw nothing: zeros; NaN is in o as well)
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) *reinterpret_cast<v4f*>(to + 16 * i) = o[i];
+    for (int i = 0; i < D / 16; ++i) *reinterpret_cast<v4f*>(to + 16 * i) = o[i] * back;
     if (g == 0) r.a.stat[slot] = float2{mx, total};
   }
   if (g == 0 && !r.it.of_group && r.begins()) tell_row<D>(r, p, l, rr, key);
@@ -384,7 +390,8 @@ __device__ __forceinline__ void narrow_runs(const ShareArgs& s, const SharePlan&
     const int64_t r0 = (int64_t)r.it.tile * kNarrowRows;
     Rows<D, I8, 1> w;
     w.run(r.a, r.q, (int)r.it.h, r0, r.from, min(r.to, steps_to(r, r0 + kNarrowRows, kTokTile)), 1, j, g);
-    store_share<D>(r, p, l, w.o[0], w.mx[0], w.sum[0], (uint32_t)r0 + j, g);
+    const float total = groups_sum(w.sum[0]);
+    store_share<D>(r, p, l, w.o[0], w.mx[0], total, total, (uint32_t)r0 + j, g);
   }
 }
 
@@ -399,7 +406,8 @@ __device__ __forceinline__ void take_wide(const Share& r, const SharePlan& p, co
   w.run(r.a, r.q, (int)r.it.h, r.from * kSub, min(r.to * kSub, steps_to(r, t0 + W::kRows, W::T)),
         r0 < r.q.nrows, smem, wv, lane);
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) store_share<D>(r, p, l, w.o[rt], w.mx[rt], w.sum[rt], (uint32_t)r0 + 16 * rt + j, g);
+  for (int rt = 0; rt < RT; ++rt)
+    store_share<D>(r, p, l, w.o[rt], w.mx[rt], groups_sum(w.sum[rt]), w.kept[rt][0], (uint32_t)r0 + 16 * rt + j, g);
 }
 
 template <int D, bool I8>

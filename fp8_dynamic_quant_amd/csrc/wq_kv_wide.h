@@ -45,6 +45,7 @@ struct Wide {
   v8bf qf[RT][NK];
   v4f o[RT][NV];
   float mx[RT], sum[RT];  // what weights are relative to (log2), and this lane group's part of their sum
+  v4f kept[RT];           // in each element the whole sum of the weights as they are rounded for o
   float down[RT];         // what a score is lowered by
   uint32_t limit[RT];
 
@@ -70,6 +71,7 @@ struct Wide {
       mx[rt] = -INFINITY;
       down[rt] = INFINITY;
       sum[rt] = 0.0f;
+      kept[rt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < NV; ++i) o[rt][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -389,6 +391,7 @@ struct Wide {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
           sum[rt] *= alpha[rt];
+          kept[rt] *= alpha[rt];
 #pragma unroll
           for (int d = 0; d < NV; ++d) o[rt][d] *= alpha[rt];
         }
@@ -398,12 +401,19 @@ struct Wide {
         sum[rt] += part[rt];
         down[rt] = -mx[rt];  // (infinite where a row has seen nothing)
       }
-      // values: (m, y) in order
+      // values: (m, y) in order, and before each m's a row of ones, with which the matrix unit adds up the
+      // rounded weights (the vector instructions, which bound the step, have no room for that)
+      constexpr uint32_t kOnes = 0x3F803F80u;
+      const v8bf ones = __builtin_bit_cast(v8bf, v4u{kOnes, kOnes, kOnes, kOnes});
       auto out = [&](int from, int to) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = from; i < to; ++i) {
           const v8bf now = frag[i % kAhead];
           if (i + kAhead < NM * NV) frag[i % kAhead] = value(i + kAhead);
+          if (i % NV == 0) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) kept[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pf[rt][i / NV], kept[rt], 0, 0, 0);
+          }
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
             o[rt][i % NV] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now, pf[rt][i / NV], o[rt][i % NV], 0, 0, 0);
@@ -424,6 +434,7 @@ struct Wide {
       for (int i = 0; i < kAll; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // a read,
         __builtin_amdgcn_sched_group_barrier(0x008, RT, 0);  // matrix instructions,
+        if (i % NV == 0) __builtin_amdgcn_sched_group_barrier(0x008, RT, 0);
         __builtin_amdgcn_sched_group_barrier(0x002, I8 ? 6 : 3, 0);
         __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
       }

@@ -466,9 +466,11 @@ int wq_kv_attention_path(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T,
  * floor(shared / page_tokens) entries are equal over the group (where they are not, the entries of
  * its first sequence with rows are taken).  A group's least such number counts, in whole pages and
  * whole steps of 64 tokens, and no more than every row of it sees; the remaining tokens are read for
- * each sequence.  Results differ from wq_kv_attention's by the order of f32 sums and by where a
- * weight's rounding to bf16 falls (2^-8 of it, as there); weights are up to 2^8 here, so that the
- * values' weighted sums have to stay below 2^120.  It pays from some hundreds of shared tokens on:
+ * each sequence.  Results differ from wq_kv_attention's by the order of f32 sums and by the weights'
+ * rounding to bf16: each is off by at most 2^-8 of itself, as there, but here the largest is rounded
+ * too and the quotient is over the rounded weights' sum, so that an output is off by at most 2^-8 of
+ * the weighted sum of |value - output| (lse is of the weights as they are).  Weights are up to 2^8
+ * here, so that the values' weighted sums have to stay below 2^120.  It pays from some hundreds of shared tokens on:
  * with fewer wq_kv_attention may be quicker.
  * workspace: as there, of at least wq_kv_attention_shared_workspace_bytes(); NULL: the context's
  * (WQ_ERR_WORKSPACE where that is too small). */
