@@ -69,7 +69,7 @@ struct ShareLds {
   int many[kShareSeqs];    // how many sequences have rows,
   int holder[kShareSeqs];  // the first that does: its table names the shared pages
   uint32_t carry[2][kWideWaves];
-  int last[kWideWaves];
+  int last[kWideWaves], most[kWideWaves];
 };
 
 // steps that the group led by sequence `lead` shares
@@ -80,8 +80,9 @@ __device__ __forceinline__ uint32_t shared_steps(const ShareLds& l, int lead) {
 __device__ __forceinline__ uint32_t own_steps(const KvArgs& c, int len, uint32_t shared) {
   return (uint32_t)max((int)steps_of(c, len) - (int)shared, 1);
 }
-__device__ __forceinline__ uint32_t own_rows(const ShareLds& l, int b) { return (uint32_t)max(l.row0[b + 1] - l.row0[b], 0); }
-__device__ __forceinline__ uint32_t group_rows(const ShareLds& l, int lead) { return (uint32_t)max(l.end[lead] - l.row0[lead], 0); }
+__device__ __forceinline__ uint32_t own_rows(const ShareLds& l, int b) { return (uint32_t)(l.row0[b + 1] - l.row0[b]); }
+// (of a group that shares steps: some of its sequences have rows)
+__device__ __forceinline__ uint32_t group_rows(const ShareLds& l, int lead) { return (uint32_t)(l.end[lead] - l.row0[lead]); }
 
 // The items of `rows` rows (tokens times R) over `steps` steps
 struct Kind {
@@ -109,7 +110,9 @@ struct Axis {
 struct SharePlan {
   Axis axis[2];
 };
-// Every thread of the workgroup takes part.
+// Every thread of the workgroup takes part.  Offsets are read as their running maximum, which is what they
+// are where they do not decrease: whatever they hold, sequences have rows of their own, side by side, no
+// more than T in all, so that units stay in 32 bits and what tell_row says lies in the workspace.
 template <int D>
 __device__ __forceinline__ SharePlan make_share_plan(const ShareArgs& s, ShareLds& l) {
   const KvAttnArgs& a = s.a;
@@ -117,36 +120,46 @@ __device__ __forceinline__ SharePlan make_share_plan(const ShareArgs& s, ShareLd
   const int b = threadIdx.x, lane = b & 63, wv = b >> 6;
   const bool in = b < c.B;
   static_assert(kShareSeqs == kThreads, "a thread for each sequence");
-  int row0 = 0, rows = 0, len = 0, wants = 0, id = -1;
+  int row0 = 0, next = 0, len = 0, wants = 0, id = -1;
   if (in) {
     row0 = (int)seq_offset(c, b);
-    rows = max((int)seq_offset(c, b + 1) - row0, 0);
+    next = (int)seq_offset(c, b + 1);
     len = c.lens[b];
     id = s.group[b];
     wants = s.shared[b];
-    l.row0[b] = row0;
     l.len[b] = len;
     l.id[b] = id;
     l.steps[b] = INT32_MAX;
     l.end[b] = 0;
     l.many[b] = 0;
     l.holder[b] = INT32_MAX;
-    if (b == c.B - 1) l.row0[c.B] = row0 + rows;
   }
   __syncthreads();
   // the last sequence up to b that begins a group
   int lead = in && b > 0 && (id < 0 || id != l.id[b - 1]) ? b : 0;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(lead, o, 64);
-    if (lane >= o) lead = max(lead, u);
+    const int u = __shfl_up(lead, o, 64), v = __shfl_up(row0, o, 64);
+    if (lane >= o) {
+      lead = max(lead, u);
+      row0 = max(row0, v);
+    }
   }
-  if (lane == 63) l.last[wv] = lead;
+  if (lane == 63) {
+    l.last[wv] = lead;
+    l.most[wv] = row0;
+  }
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWideWaves; ++w)
-    if (w < wv) lead = max(lead, l.last[w]);
+    if (w < wv) {
+      lead = max(lead, l.last[w]);
+      row0 = max(row0, l.most[w]);
+    }
+  const int rows = max(next - row0, 0);
   if (in) {
+    l.row0[b] = row0;
+    if (b == c.B - 1) l.row0[c.B] = row0 + rows;
     l.lead[b] = lead;
     if (rows > 0) {
       // the whole pages that all of its rows see, in whole steps
