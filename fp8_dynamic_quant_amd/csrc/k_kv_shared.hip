@@ -28,6 +28,7 @@
 // tokens behind 4096 34 and 72, of 2000 behind 512 42 and 47.  Where little is shared the plan and the
 // parts may cost more than it saves: 200 sequences of 500 behind 256, 64 heads of 64 on 8, 38 and 31.
 #include "wq_kernels.h"
+#include "wq_kv_plan.h"
 #include "wq_kv_wide.h"
 #include "wq_layer.h"
 
@@ -35,28 +36,15 @@ namespace wq {
 
 namespace {
 
-constexpr int kShareSeqs = 512;  // sequences of one launch (their plan is held in LDS)
 constexpr int kThreads = 64 * kWideWaves;
-
-enum { kNarrow = 0, kWide = 1 };
-constexpr int kNarrowRows = 16;
-__host__ __device__ constexpr int wide_rows(int D) { return D == 256 ? 128 : 256; }
-// rows of the workspace for the narrow runs of a workgroup (a wave does not hold a head of 256)
-__host__ __device__ constexpr int narrow_slots(int D) { return D == 256 ? 0 : kWideWaves * kNarrowRows; }
+static_assert(kWideWaves == kShareWaves, "the plan's workgroups are the wide kernel's");
 
 struct ShareArgs {
-  KvAttnArgs a;            // part, stat: [2 keys + workgroups * (narrow_slots + wide_rows)] rows
+  KvAttnArgs a;            // part, stat: [share_slots] rows
   const int32_t* group;    // [B]
   const int32_t* shared;   // [B]
   uint4* desc;             // [keys], keys = T * Hq
 };
-// units of a run, by kind: fewer leave more parts to join.  (8 sequences of 50 own tokens behind 1000:
-// 15.2 us, with {8, 4} 18.4; 64 of 500 behind 8192, whose runs are longer than either: 41.)
-constexpr uint32_t kLeast[2] = {5, 2};
-// units that an item counts besides its steps: a run of either kind has 7 to 9 us of its own (plan, first
-// loads, parts) beside 2 to 2.7 us a step, and an item inside it 2 to 4.  (2 and 4 instead: from 4 %
-// quicker to 5 % slower over twelve shapes.)
-__device__ __forceinline__ uint32_t fixed_units(int kind) { return kind == kNarrow ? 4u : 6u; }
 
 struct ShareLds {
   uint32_t pre[2][kShareSeqs + 1];  // by kind: units before sequence b, for one head
@@ -84,32 +72,6 @@ __device__ __forceinline__ uint32_t own_rows(const ShareLds& l, int b) { return 
 // (of a group that shares steps: some of its sequences have rows)
 __device__ __forceinline__ uint32_t group_rows(const ShareLds& l, int lead) { return (uint32_t)(l.end[lead] - l.row0[lead]); }
 
-// The items of `rows` rows (tokens times R) over `steps` steps
-struct Kind {
-  int kind;
-  uint32_t tile, tiles, steps, units;  // rows of a tile; tiles; units of an item
-};
-template <int D>
-__device__ __forceinline__ Kind kind_of(uint32_t rows, uint32_t steps) {
-  Kind k;
-  k.kind = D < 256 && rows <= kNarrowRows ? kNarrow : kWide;
-  k.tile = k.kind == kNarrow ? kNarrowRows : wide_rows(D);
-  k.tiles = (rows + k.tile - 1) / k.tile;
-  k.steps = steps;
-  k.units = steps + fixed_units(k.kind);
-  return k;
-}
-
-struct Axis {
-  uint32_t units, per, runs;
-  static __device__ __forceinline__ Axis cut(uint32_t units, uint32_t runs, uint32_t least) {
-    const uint32_t per = max((units + runs - 1) / runs, least);
-    return Axis{units, per, (units + per - 1) / per};
-  }
-};
-struct SharePlan {
-  Axis axis[2];
-};
 // Every thread of the workgroup takes part.  Offsets are read as their running maximum, which is what they
 // are where they do not decrease: whatever they hold, sequences have rows of their own, side by side, no
 // more than T in all, so that units stay in 32 bits and what tell_row says lies in the workspace.
@@ -192,7 +154,6 @@ __device__ __forceinline__ SharePlan make_share_plan(const ShareArgs& s, ShareLd
     if (lane == 63) l.carry[k][wv] = v[k];
   }
   __syncthreads();
-  SharePlan p;
   uint32_t total[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -206,15 +167,7 @@ __device__ __forceinline__ SharePlan make_share_plan(const ShareArgs& s, ShareLd
     if (b == 0) l.pre[k][0] = 0;
     total[k] = (uint32_t)uniform((int)(sum * (uint32_t)c.H));
   }
-  // A narrow unit of one wave takes about 5 / 4 of the time of a wide one of eight.  (Weighed by 1/2, 1,
-  // 5/4, 2: 402, 257, 234, 238 us at 256 sequences of 1500 own tokens behind 32768, 32 heads of 128.
-  // Every workgroup taking both kinds, half of them one first and half the other: 238 us there, but
-  // 53 us, not 41, at 64 sequences of 500 own tokens behind 8192, where each waits for its slowest wave.)
-  const uint32_t all = gridDim.x;
-  const uint64_t narrow = ((uint64_t)total[kNarrow] * 5 + 4 * kWideWaves - 1) / (4 * kWideWaves);
-  const uint32_t share = (uint32_t)((uint64_t)all * total[kWide] / (total[kWide] + narrow + 1));
-  p.axis[kWide] = Axis::cut(total[kWide], total[kNarrow] == 0 ? all : min(max(share, 1u), all - 1), kLeast[kWide]);
-  p.axis[kNarrow] = Axis::cut(total[kNarrow], (all - min(p.axis[kWide].runs, all - 1)) * kWideWaves, kLeast[kNarrow]);
+  const SharePlan p = cut_axes(total[kNarrow], total[kWide], gridDim.x);
   __syncthreads();
   return p;
 }
@@ -260,13 +213,6 @@ __device__ __forceinline__ ShareItem share_item(const ShareArgs& s, const ShareL
   it.tile = item - it.h * it.k.tiles;
   return it;
 }
-// step p of an item lies at its unit fixed + p: a run that begins at or before that and ends behind it
-// takes the step
-__device__ __forceinline__ uint32_t step_at(const Kind& k, uint32_t x) {
-  const uint32_t f = fixed_units(k.kind);
-  return x <= f ? 0u : min(x - f, k.steps);
-}
-
 // What a run has of an item, and where its rows' output or part goes
 struct Share {
   const ShareArgs& s;
@@ -288,9 +234,8 @@ struct Share {
   template <int D>
   __device__ __forceinline__ int64_t slot(uint32_t rr, int64_t key) const {
     const int64_t keys = a.c.T * a.c.H * a.R;
-    if (begins()) return (it.of_group ? keys : 0) + key;
-    const int64_t at = 2 * keys + (it.k.kind == kNarrow ? (int64_t)run * kNarrowRows : (int64_t)gridDim.x * narrow_slots(D) + (int64_t)run * wide_rows(D));
-    return at + (rr - it.tile * it.k.tile);
+    if (begins()) return first_slot(keys, key, it.of_group);
+    return run_slot<D>(keys, gridDim.x, it.k.kind, run, rr - it.tile * it.k.tile);
   }
 };
 template <int D, int KIND>
@@ -327,9 +272,8 @@ __device__ __forceinline__ void tell_row(const Share& r, const SharePlan& p, con
   uint4 d{0, 0, 0, 0};
   if (!r.whole) {
     auto parts = [&](const Kind& k, uint32_t i0, uint32_t row) {
-      const uint32_t per = k.kind == kNarrow ? p.axis[kNarrow].per : p.axis[kWide].per, first = i0 + fixed_units(k.kind);
-      const uint32_t run = first / per;
-      return uint2{run | ((first + k.steps - 1) / per - run + 1) << 16, row % k.tile | (uint32_t)k.kind << 15};
+      const Parts t = parts_of(k, p, i0, row);
+      return uint2{t.run | t.count << 16, t.at};
     };
     const uint2 own = parts(it.k, it.i0, rr);
     d.x = own.x;
@@ -470,10 +414,9 @@ struct JoinParts {
   __device__ __forceinline__ int64_t slot(int p) const {
     const bool mine = p < own;
     const int k = mine ? p : p - own;
-    if (k == 0) return (mine ? 0 : keys) + key;
+    if (k == 0) return first_slot(keys, key, !mine);
     const uint32_t run = ((mine ? d.x : d.y) & 0xFFFFu) + k, at = mine ? d.z & 0xFFFFu : d.z >> 16;
-    const int64_t narrow = 2 * keys, wide = narrow + (int64_t)s.a.runs * narrow_slots(D);
-    return at & 0x8000u ? wide + (int64_t)run * wide_rows(D) + (at & 0x7FFFu) : narrow + (int64_t)run * kNarrowRows + at;
+    return run_slot<D>(keys, s.a.runs, at & 0x8000u ? kWide : kNarrow, run, at & 0x7FFFu);
   }
 };
 template <int D>
@@ -619,7 +562,7 @@ ShareShape share_shape(const KvArgs& c, int R, int num_cu) {
   const double tiles = 2.0 * ((double)c.T * R / kNarrowRows + c.B) * c.H, steps = (double)c.max_pages * c.P / kTokTile + 8;
   s.own = c.T * R < 2048 * (int64_t)c.B && tiles * steps < 2147483648.0;
   s.keys = c.T * c.H * R;
-  s.slots = 2 * s.keys + (int64_t)max(num_cu, 2) * (narrow_slots(c.D) + wide_rows(c.D));
+  s.slots = share_slots(s.keys, max(num_cu, 2), c.D);
   return s;
 }
 
