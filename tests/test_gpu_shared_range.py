@@ -173,3 +173,30 @@ def test_errors_are_those_of_independent_roundings(D, i8, ns):
                     allowed += np.square(half).sum() / 3 + 0.541 * 2.0**-16 / 3 * (np.square(w) @ np.square(v[: len(w)] - want)).sum()
     assert np.mean(most) > 0.4, "rows of a few large weights"
     assert error <= 1.15**2 * allowed, (error / allowed) ** 0.5
+
+
+@pytest.mark.parametrize("ns", [[1] * 8, [20] * 4])
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_without_groups_outputs_are_those_of_attention(D, i8, ns):
+    # each within what its roundings allow of the definition: both weights' (2^-8 of sum w |v|, and of |out| where
+    # the sum is of rounded ones) and both outputs' (2^-8), and the f32 sums of either
+    H, R, P, width = 2, 4, 16, 26
+    g = syn.rng(134, D, int(i8), len(ns))
+    B = len(ns)
+    lens = [300 + 13 * b for b in range(B)]
+    c = kf.cache(g, B * width, H, P, D, i8)
+    table = g.permutation(B * width).reshape(B, width).astype(np.int32)
+    q = nm.f64_to_bf16_rn(g.standard_normal((sum(ns), H * R, D)))
+    off = np.concatenate(([0], np.cumsum(ns))).astype(np.int64)
+    cd = wq.KvCache(*(dev(x) for x in c))
+    args = [bf16_dev(q), dev(off), dev(np.array(lens, np.int32)), dev(table)]
+    ids, none = (dev(np.full(B, x, np.int32)) for x in (-1, 0))
+    assert wq.wq_kv_attention_shared_path(cd, *q.shape[:2], args[3]) == 16
+    got, got_lse = wq.wq_kv_attention_shared(cd, *args, ids, none, return_lse=True)
+    ref, ref_lse = wq.wq_kv_attention(cd, *args, return_lse=True)
+    want, want_lse, mag, smag = kf.attention(c, q, off, lens, table, D**-0.5, True)
+    lim, lim_lse = _limits(want, want_lse, mag, smag, max(lens), D)
+    a, b = (nm.bf16_to_f32(host_bf16_bits(x)).astype(np.float64) for x in (got, ref))
+    assert (np.abs(a - b) <= 2 * lim + (2.0**-8 + 2.0**-14) * np.abs(want) + 2.0**-14 * mag).all()
+    assert (np.abs(host(got_lse) - host(ref_lse)) <= 2 * lim_lse).all()
