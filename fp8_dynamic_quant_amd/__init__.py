@@ -647,7 +647,7 @@ def wq_kv_attention_shared(cache: KvCache, q: torch.Tensor, offsets, lens, table
                            out=None, lse=None, return_lse=False):
     """wq_kv_attention of sequences that begin with the same pages: neighbours with the same id in
     group (int32 [B], not negative) have their first shared[b] tokens (int32 [B]) in common, which
-    are read and multiplied once for all of them."""
+    are read once for every 256 of their rows (wq.h: from how many tokens on that pays)."""
     d, B = _kv_desc(cache, offsets, lens, table)
     for name, x in (("group", group), ("shared", shared)):
         if x.shape != (B,) or x.dtype is not _I32 or not x.is_contiguous():

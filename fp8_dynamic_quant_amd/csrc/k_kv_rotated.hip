@@ -6,8 +6,8 @@
 // in 32 bits: two products, each rounded, and their sum.  Keys go from there to their 8-bit codes
 // with no rounding between; queries are rounded once to bf16, what attention takes.
 //
-// One launch for all three.  6000 rows of 32 heads on 8 of 128, int8: 23.8 us with pages of 32 tokens,
-// 20.1 of 64 (3.8 and 4.5 TB/s read and written; a copy 5.2), where values leave in words of four tokens;
+// One launch for all three.  3900 rows (2000, 1300 and 600) of 32 heads on 8 of 128, int8: 23.8 to 25.4 us with
+// pages of 32 tokens, 20.1 of 64 (3.5 to 3.8 and 4.5 TB/s read and written; a copy 5.2), where values leave in words of four tokens;
 // a token of one sequence 5.6, of 64 sequences 7.6: the launch, and offsets, length, page number, rows
 // and the old scale in turn.
 #include "wq_kv_device.h"

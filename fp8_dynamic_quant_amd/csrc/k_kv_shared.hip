@@ -16,17 +16,19 @@
 // second kernel in the order of the axes: results do not depend on timing.
 //
 // What a call takes, and of it the join, in us:
-//   8 sequences of 50 own tokens behind 1000, 32 heads of 128 on 8   14.7   4  launches, the plan (2.5), steps in turn
-//   64 of 500 behind 8192, the same heads, int8                      38.8   6  short runs: beginnings, parts
-//   256 of 1500 behind 32768, the same heads                          237  10  the wide kernel's arithmetic
+//   8 sequences of 50 own tokens behind 1000, 32 heads of 128 on 8   14.9   4  launches, the plan (2.5), steps in turn
+//   64 of 500 behind 8192, the same heads, int8                        40   6  short runs: beginnings, parts
+//   256 of 1500 behind 32768, the same heads                          236  10  the wide kernel's arithmetic
 //   24 of 4 rows and 300 tokens behind four documents of 32768,
-//   16 heads of 256 on one                                           70.5   8  chains of reads and products, a row tile a wave
+//   16 heads of 256 on one                                             72   8  chains of reads and products, a row tile a wave
 // A wide run of the second begins its first step 9 us after the launch: plan 2.7, its item found 1.9,
 // rows and limits 1.5, page numbers 1, addresses 1.1, the first step 0.7 (latency, and code that is
 // fetched as it runs); seven steps take 17, their parts 3.
-// Beside attention of each sequence alone, E4M3, 32 query heads of 128 on 8: 64 sequences of 200 own
-// tokens behind 4096 34 and 72, of 2000 behind 512 42 and 47.  Where little is shared the plan and the
-// parts may cost more than it saves: 200 sequences of 500 behind 256, 64 heads of 64 on 8, 38 and 31.
+// Beside attention of each sequence alone, E4M3, one token each, 32 query heads of 128 on 8: 64 sequences of
+// up to 200 own tokens behind 4096 35 and 73, of 2000 behind 512 42 and 48.  Where little is shared the plan
+// and the parts cost more than it saves: 64 of 200 behind 512 28.6 and 20.5, behind 1024 29.6 and 36.1;
+// 8 of 50 15.2 and 13.3, 15.5 and 17.8; 200 of 500 less from 64 on (42 and 50), but with 64 heads of 64 on 8
+// 39 and 35 behind 512, 45 and 55 behind 1024.
 #include "wq_kernels.h"
 #include "wq_kv_plan.h"
 #include "wq_kv_wide.h"
@@ -549,9 +551,14 @@ __global__ __launch_bounds__(256) void k_kv_shared_join_wide(ShareArgs s) {
 }
 
 // How a call runs.  Sequences of many rows fill row tiles of their own, which read the shared tokens
-// once for each: attention as it is does that, with no parts to join.  (32 heads of 128 in groups of
-// four, E4M3, that and this: 16 sequences of 128 rows behind 4096 shared tokens 217 and 150 us, of
-// 256 385 and 270; 4 of 512 behind 512, where a row's parts weigh as much as its tokens, 61 and 77.)
+// once for each: attention as it is does that, with no parts to join.  What is shared decides which is
+// quicker, and the host does not know it: the rule lies where either gains about what the other would, an
+// average of 512 new tokens here.  (32 heads of 128 in groups of four, E4M3, attention as it is and this, by
+// the new tokens of the longest sequence, the average being 0.63 of that with 16 and 0.68 with 4 sequences:
+//   16 behind 4096:  128 228 and 150 us, 256 389 and 282, 512 634 and 525, 768 899 and 771
+//   16 behind 512:    64 44 and 50,      128 48 and 71,   256 83 and 117,  768 227 and 363
+//   4 behind 4096:   128 76 and 60,      256 122 and 95,  512 231 and 160, 768 348 and 241
+//   4 behind 512:    128 38 and 38,      256 47 and 51,   512 62 and 79,   768 76 and 113)
 // So do sizes whose units are not counted in 32 bits.
 struct ShareShape {
   bool own;

@@ -16,13 +16,17 @@ constexpr int kWideWaves = 8;
 // wave for itself, as attention of one sequence's rows does (SharedRows), is a third of that kernel's
 // vector instructions with E4M3 codes and more than half with int8.
 //
-// What bounds it.  1024 rows of 8 heads of 128 over 32768 tokens, E4M3: 184 us, 750 TFLOP/s (int8 193);
-// with each wave widening for itself 257 and 320.  Of the SIMDs' cycles matrix instructions take 37 %,
-// other vector instructions 36 %, and two waves a SIMD do not hide each other: half of the waves of a
+// What bounds it.  1024 rows of 8 heads of 128 over 32768 tokens, E4M3: 187 us, 735 TFLOP/s (int8 196);
+// with each wave widening for itself 257 and 320.  Of the SIMDs' cycles matrix instructions take 41 %,
+// other vector instructions 40 %, and two waves a SIMD do not hide each other: half of the waves of a
 // workgroup reach the barrier a quarter of a step before the others.  (The later four waves half a step
-// behind, products with values beside scores: 187 and 188.)  Heads of 256, with one row tile a wave:
-// a step of 32 tokens 2700 cycles, LDS 40 % of them, matrix instructions 21 %, the others 26 %, waves
-// waiting for reads and barriers 41 % of their time; registers do not hold a second row tile.
+// behind, products with values beside scores: 2 % slower.)  Heads of 64, 8 to a cache head: 233.  Heads of
+// 256, 4 to each of 4: 281, one row tile a wave: a step of 32 tokens 2700 cycles, LDS 40 % of them, matrix
+// instructions 22 %, the others 27 %, waves waiting for reads and barriers 42 % of their time; registers
+// do not hold a second row tile.
+// The row of ones (below) costs 1 to 2 % of that, of heads of 64, whose products are fewest, 3.5 %: 184, 193,
+// 226 and 276 without.  Two-element dot products instead: 264 with heads of 64, and with heads of 128 453, whose
+// registers do not hold them.
 //
 // Lane (j, g) = (l % 16, l / 16).  s^T = k q^T in instructions t of 16 tokens: the lane that supplies key
 // row i takes token (T / 4) (i / 4) + 4 t + i % 4, so that lane group g ends with the T / 4 consecutive
@@ -31,7 +35,7 @@ constexpr int kWideWaves = 8;
 // Pieces of 16 bytes are XORed with their row so that the sixteen lanes of a read meet sixteen different
 // places of 256 bytes: key rows by the lane that reads them, value rows by their number.
 // A step's token groups of 16 each have a page of their own to look up; taking one for the whole step
-// where pages hold whole ones, with scalar addresses, was 1 % quicker at best (183 and 186 us).
+// where pages hold whole ones, with scalar addresses, was 1 % quicker at best.
 template <int D, bool I8, int RT>
 struct Wide {
   static constexpr int T = D == 256 ? 32 : 64;  // tokens of a step: two buffers of 32 KiB

@@ -459,8 +459,8 @@ int64_t wq_kv_attention_workspace_bytes(const wq_ctx* ctx, const wq_kv_cache* ca
 int wq_kv_attention_path(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T, int64_t q_heads, int64_t B);
 
 /* wq_kv_attention of sequences that begin with the same pages (a system prompt, several answers to
- * one question): the same rows, masks and outputs, with what is shared read and multiplied once for
- * all rows that share it.  group, shared: device int32 [B].  Neighbouring sequences with the same
+ * one question): the same rows, masks and outputs, with what is shared read once for every 256 of the
+ * rows that share it (new rows times q_heads / heads; 128 with heads of 256).  group, shared: device int32 [B].  Neighbouring sequences with the same
  * id, not negative, are a group; shared[b] is the number of tokens from its first on that sequence b
  * has in common with the others of its group, in the same pages: the tables' first
  * floor(shared / page_tokens) entries are equal over the group (where they are not, the entries of
@@ -470,8 +470,13 @@ int wq_kv_attention_path(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T,
  * rounding to bf16: each is off by at most 2^-8 of itself, as there, but here the largest is rounded
  * too and the quotient is over the rounded weights' sum, so that an output is off by at most 2^-8 of
  * the weighted sum of |value - output| (lse is of the weights as they are).  Weights are up to 2^8
- * here, so that the values' weighted sums have to stay below 2^120.  It pays from some hundreds of shared tokens on:
- * with fewer wq_kv_attention may be quicker.
+ * here, so that the values' weighted sums have to stay below 2^120, and int8 pages with values that
+ * read as infinity may reach as NaN rows that do not see them, as those of E4M3 codes may there.
+ * The call shares whatever it is told, also where wq_kv_attention would be quicker: for single tokens
+ * it pays from about 1000 shared tokens on (2000 to 4000 for 8 sequences with heads of 64; from a
+ * few hundred with heads of 256; at any number for 200 sequences of 500 own tokens with heads of
+ * 128), and below that it may take twice as long; prompts of 64 new tokens and more take 1 to 1.6 times
+ * as long behind 512 tokens (heads of 64: 1.9) and 0.6 to 1.1 times behind 4096.
  * workspace: as there, of at least wq_kv_attention_shared_workspace_bytes(); NULL: the context's
  * (WQ_ERR_WORKSPACE where that is too small). */
 int wq_kv_attention_shared(wq_ctx* ctx, const wq_kv_cache* cache, const void* q, int64_t ldq, int64_t T,
@@ -479,8 +484,10 @@ int wq_kv_attention_shared(wq_ctx* ctx, const wq_kv_cache* cache, const void* q,
                            const int32_t* group, const int32_t* shared, float scale, int causal, void* out,
                            int64_t ldo, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
-/* As wq_kv_attention_workspace_bytes, of wq_kv_attention_shared: two f32 rows for every output row
- * besides the workgroups' own; not bounded by the context's workspace. */
+/* As wq_kv_attention_workspace_bytes, of wq_kv_attention_shared: two f32 rows for every output row (a row
+ * and query head), 8 head_dim + 32 bytes, besides the workgroups' own (51 MB on 256 CUs with heads of
+ * 128).  It grows with T and is not bounded by the context's workspace: 64 sequences of 500 new tokens
+ * with 32 heads of 128 take 1.1 GB, single tokens of 512 sequences 68 MB. */
 int64_t wq_kv_attention_shared_workspace_bytes(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T,
                                                int64_t q_heads, int64_t B);
 
