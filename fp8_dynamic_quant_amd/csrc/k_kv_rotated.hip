@@ -7,8 +7,8 @@
 // with no rounding between; queries are rounded once to bf16, what attention takes.
 //
 // One launch for all three.  3900 rows (2000, 1300 and 600) of 32 heads on 8 of 128, int8: 23.8 to 25.4 us with
-// pages of 32 tokens, 20.1 of 64 (3.5 to 3.8 and 4.5 TB/s read and written; a copy 5.2), where values leave in words of four tokens;
-// a token of one sequence 5.6, of 64 sequences 7.6: the launch, and offsets, length, page number, rows
+// pages of 32 tokens, 20.1 of 64 (3.5 to 3.8 and 4.5 TB/s read and written; a copy 5.2), where values leave
+// in words of four tokens; a token of one sequence 5.6, of 64 sequences 7.6: the launch, and offsets, length, page number, rows
 // and the old scale in turn.
 #include "wq_kv_device.h"
 #include "wq_layer.h"

@@ -303,7 +303,8 @@ __device__ __forceinline__ void tell_row(const Share& r, const SharePlan& p, con
 // Wide's are rounded, the largest too, which may be anything in (1/2, 2^8].  Over their own sum that rounding
 // cancels as far as it is common to what a row sees, so that a row of one token is that token's value; over
 // the other sum it would leave up to 2^-8 of everything (rows of a few large weights: 0.0023 off against 64
-// bits, 0.0017 so, which is the output's own rounding; of many 0.0024 and 0.0021).  o comes to the scale of `total` here, which lse and the join go by.
+// bits, 0.0017 so, which is the output's own rounding; of many 0.0024 and 0.0021).  A part is brought to the
+// scale of `total`, which lse and the join go by.
 template <int D>
 __device__ __forceinline__ void store_share(const Share& r, const SharePlan& p, const ShareLds& l, const v4f (&o)[D / 16], float mx,
                                             float total, float kept, uint32_t rr, int g) {

@@ -460,8 +460,8 @@ int wq_kv_attention_path(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T,
 
 /* wq_kv_attention of sequences that begin with the same pages (a system prompt, several answers to
  * one question): the same rows, masks and outputs, with what is shared read once for every 256 of the
- * rows that share it (new rows times q_heads / heads; 128 with heads of 256).  group, shared: device int32 [B].  Neighbouring sequences with the same
- * id, not negative, are a group; shared[b] is the number of tokens from its first on that sequence b
+ * rows that share it (new rows times q_heads / heads; 128 with heads of 256).  group, shared: device
+ * int32 [B].  Neighbouring sequences with the same id, not negative, are a group; shared[b] is the number of tokens from its first on that sequence b
  * has in common with the others of its group, in the same pages: the tables' first
  * floor(shared / page_tokens) entries are equal over the group (where they are not, the entries of
  * its first sequence with rows are taken).  A group's least such number counts, in whole pages and
