@@ -461,12 +461,12 @@ int wq_kv_attention_path(const wq_ctx* ctx, const wq_kv_cache* cache, int64_t T,
 /* wq_kv_attention of sequences that begin with the same pages (a system prompt, several answers to
  * one question): the same rows, masks and outputs, with what is shared read once for every 256 of the
  * rows that share it (new rows times q_heads / heads; 128 with heads of 256).  group, shared: device
- * int32 [B].  Neighbouring sequences with the same id, not negative, are a group; shared[b] is the number of tokens from its first on that sequence b
- * has in common with the others of its group, in the same pages: the tables' first
- * floor(shared / page_tokens) entries are equal over the group (where they are not, the entries of
- * its first sequence with rows are taken).  A group's least such number counts, in whole pages and
- * whole steps of 64 tokens, and no more than every row of it sees; the remaining tokens are read for
- * each sequence.  Results differ from wq_kv_attention's by the order of f32 sums and by the weights'
+ * int32 [B].  Neighbouring sequences with the same id, not negative, are a group; shared[b] is the
+ * number of tokens from its first on that sequence b has in common with the others of its group, in
+ * the same pages: the tables' first floor(shared / page_tokens) entries are equal over the group
+ * (where they are not, the entries of its first sequence with rows are taken).  A group's least such
+ * number counts, in whole pages and whole steps of 64 tokens, and no more than every row of it sees;
+ * the remaining tokens are read for each sequence.  Results differ from wq_kv_attention's by the order of f32 sums and by the weights'
  * rounding to bf16: each is off by at most 2^-8 of itself, as there, but here the largest is rounded
  * too and the quotient is over the rounded weights' sum, so that an output is off by at most 2^-8 of
  * the weighted sum of |value - output| (lse is of the weights as they are).  Weights are up to 2^8
